@@ -1,0 +1,79 @@
+// ops_common.cuh -- 16-bit types and the epilogue of the products of moe_ops.h.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ops_internal.h"
+
+namespace moe {
+namespace ops {
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+// two values rounded to T, the first in the low half
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+
+// act(z), to about 2^-20 relative (the results are rounded to 16 bits). The tanh
+// form of GELU is z / (1 + exp(-2 i)), i its tanh argument: one exponential,
+// and no cancellation for negative z.
+__device__ __forceinline__ float unary_act(int act, float z) {
+    if (act == MOE_EPI_NONE) return z;
+    if (act == MOE_EPI_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    const float a = act == MOE_EPI_SILU ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);
+    return __fdividef(z, 1.0f + __expf(-a));
+}
+
+// a NaN stays a NaN (fminf and fmaxf would drop it)
+__device__ __forceinline__ float clamp_hi(float v, float hi) { return v > hi ? hi : v; }
+__device__ __forceinline__ float clamp_lo(float v, float lo) { return v < lo ? lo : v; }
+
+// act(g) * u with the clamp of a gated product (limit > 0)
+__device__ __forceinline__ float gated_act(int act, float limit, float g, float u) {
+    if (limit > 0.f) {
+        g = clamp_hi(g, limit);
+        u = clamp_lo(clamp_hi(u, limit), -limit);
+    }
+    return unary_act(act, g) * u;
+}
+
+// rows [lo, hi) of group e, inside 0..rows whatever the offsets hold
+__device__ __forceinline__ void group_rows(const Product &p, int e, int &lo, int &hi) {
+    if (!p.offsets) {
+        lo = 0;
+        hi = p.rows;
+        return;
+    }
+    lo = min(max(p.offsets[e], 0), p.rows);
+    hi = min(max(p.offsets[e + 1], lo), p.rows);
+}
+
+// the row of x that feeds row r, inside 0..x_rows-1 whatever row_token holds
+__device__ __forceinline__ int input_row(const Product &p, int r) {
+    return p.row_token ? min(max(p.row_token[r], 0), p.x_rows - 1) : min(r, p.x_rows - 1);
+}
+
+}  // namespace ops
+}  // namespace moe

@@ -1,0 +1,230 @@
+// ops_slots.cu -- the slot bookkeeping of moe_ops.h: grouping (moe_group_slots)
+// and the weighted combine (moe_combine_slots).
+//
+// Grouping is a stable counting sort of n * top_k expert ids with at most 1024
+// keys, in one launch of one cluster of up to 8 CTAs and without a workspace.
+// Slots are cut into contiguous runs, one per warp, in slot order.
+//   1. Each warp counts its run per expert. __match_any_sync groups the lanes of
+//      one round by id, the lowest lane of a group adds its size to the warp's
+//      own counter, so the counters need no atomics.
+//   2. Counters are summed: over the warps of a CTA into a prefix per (warp,
+//      expert), over the CTAs through distributed shared memory, over the
+//      experts by a block scan (the offsets).
+//   3. Each warp walks its run again: a slot's row is its warp's counter plus
+//      the number of lower lanes with the same id, and the leader moves the
+//      counter on. The order (expert, token, rank) needs no atomics either, so
+//      the result does not depend on timing.
+// Bound: latency. 8 slots take one CTA and a few dependent steps; 131072 slots
+// read and write 2 MB, which 8 SMs do in the time of the steps around it.
+#include <cooperative_groups.h>
+
+#include "ops_common.cuh"
+
+namespace moe {
+namespace ops {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+
+// slots [first, last) of warp `warp` of CTA `cta`: runs of a multiple of 32 slots
+__device__ __forceinline__ void warp_run(long long S, int ctas, int cta, int warp, long long &first, long long &last) {
+    const long long rounds = (S + 32LL * ctas * kWarps - 1) / (32LL * ctas * kWarps);
+    first = min((long long)(cta * kWarps + warp) * rounds * 32, S);
+    last = min(first + rounds * 32, S);
+}
+
+__global__ void __launch_bounds__(kThreads)
+    group_slots_kernel(const int *__restrict__ topk_idx, long long S, int top_k, int E, int e_lo, int e_hi,
+                       int *__restrict__ offsets, int *__restrict__ slot_token, int *__restrict__ slot_k,
+                       int *__restrict__ slot_of) {
+    extern __shared__ int sm[];
+    int *cnt = sm;                 // [kWarps][E] counters, then each warp's next row per expert
+    int *total = sm + kWarps * E;  // [E] this CTA's counts (read by the cluster)
+    __shared__ int warp_sum[kWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kWarps * E; i += kThreads) cnt[i] = 0;
+    __syncthreads();
+    long long first, last;
+    warp_run(S, ctas, cta, warp, first, last);
+    int *mine = cnt + warp * E;
+    for (long long i = first; i < last; i += 32) {
+        const int id = i + lane < last ? topk_idx[i + lane] : -1;
+        const bool in = id >= e_lo && id < e_hi;
+        const unsigned same = __match_any_sync(0xffffffffu, in ? id : -1);
+        if (in && (same & ((1u << lane) - 1)) == 0) mine[id] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // thread e: prefix over the CTA's warps (E <= kThreads)
+    int sum = 0;
+    if (tid < E) {
+#pragma unroll 8
+        for (int w = 0; w < kWarps; ++w) {
+            const int c = cnt[w * E + tid];
+            cnt[w * E + tid] = sum;
+            sum += c;
+        }
+        total[tid] = sum;
+    }
+    if (ctas > 1) cluster.sync();
+    // counts of the earlier CTAs and of all
+    int before = 0, all = sum;
+    if (ctas > 1 && tid < E) {
+        all = 0;
+        for (int c = 0; c < ctas; ++c) {
+            const int v = cluster.map_shared_rank(total, c)[tid];
+            if (c < cta) before += v;
+            all += v;
+        }
+    }
+    if (ctas > 1) cluster.sync();  // no CTA leaves while another reads its counts
+    // exclusive scan of the counts over the experts
+    int scan = all;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= d) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    if (warp == 0) {
+        int v = warp_sum[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += u;
+        }
+        warp_sum[lane] = v;
+    }
+    __syncthreads();
+    const int base = scan - all + (warp ? warp_sum[warp - 1] : 0);
+    const int rows = warp_sum[kWarps - 1];
+    if (tid < E) {
+        if (cta == 0) {
+            offsets[tid] = base;
+            if (tid == E - 1) offsets[E] = rows;
+        }
+        for (int w = 0; w < kWarps; ++w) cnt[w * E + tid] += base + before;
+    }
+    __syncthreads();
+    for (long long i = first; i < last; i += 32) {
+        const bool live = i + lane < last;
+        const int id = live ? topk_idx[i + lane] : -1;
+        const bool in = id >= e_lo && id < e_hi;
+        const unsigned same = __match_any_sync(0xffffffffu, in ? id : -1);
+        const unsigned lower = same & ((1u << lane) - 1);
+        const int at = in ? mine[id] + __popc(lower) : -1;
+        __syncwarp();
+        if (in && lower == 0) mine[id] += __popc(same);
+        __syncwarp();
+        if (live) slot_of[i + lane] = at;
+        if (in) {
+            const int slot = (int)(i + lane);
+            slot_token[at] = slot / top_k;
+            if (slot_k) slot_k[at] = slot % top_k;
+        }
+    }
+    // rows that no slot takes
+    for (long long i = (long long)rows + cta * kThreads + tid; i < S; i += (long long)ctas * kThreads) {
+        slot_token[i] = -1;
+        if (slot_k) slot_k[i] = -1;
+    }
+}
+
+// One thread per 8 columns of a token, or per column where rows are not on
+// 16-byte boundaries. Bound: the bytes of y; every rank's load is issued
+// before the first is used.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+    combine_slots_kernel(const T *__restrict__ y, long long ldy, int rows, const int *__restrict__ slot_of,
+                         const float *__restrict__ topk_w, int n, int top_k, int N, const T *residual,
+                         long long ldr, T *out, long long ldo) {
+    constexpr int V = VEC ? 8 : 1;
+    const int groups = (N + V - 1) / V;
+    const long long items = (long long)n * groups;
+    for (long long it = blockIdx.x * 256LL + threadIdx.x; it < items; it += gridDim.x * 256LL) {
+        const int t = (int)(it / groups), c = (int)(it % groups) * V;
+        const bool whole = VEC && c + 8 <= N;
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int j = 0; j < top_k; ++j) {
+            const int s = slot_of[(size_t)t * top_k + j];
+            if (s < 0 || s >= rows) continue;
+            const float w = topk_w[(size_t)t * top_k + j];
+            const T *row = y + (size_t)s * ldy + c;
+            if (whole) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(row);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 f = unpack2<T>(u[i]);
+                    acc[2 * i] += w * f.x;
+                    acc[2 * i + 1] += w * f.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (c + i < N) acc[i] += w * to_f32(row[i]);
+            }
+        }
+        if (residual)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (c + i < N) acc[i] += to_f32(residual[(size_t)t * ldr + c + i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < N) out[(size_t)t * ldo + c + i] = from_f32<T>(acc[i]);
+    }
+}
+
+template <typename T>
+cudaError_t combine(const void *y, long long ldy, int rows, const int *slot_of, const float *topk_w, int n, int top_k,
+                    int N, const void *residual, long long ldr, void *out, long long ldo, cudaStream_t st) {
+    const bool vec = ((uintptr_t)y & 15u) == 0 && ldy % 8 == 0;
+    const long long items = (long long)n * (vec ? (N + 7) / 8 : N);
+    const int grid = (int)min((items + 255) / 256, 1LL << 20);
+    auto k = vec ? combine_slots_kernel<T, true> : combine_slots_kernel<T, false>;
+    k<<<grid, 256, 0, st>>>(static_cast<const T *>(y), ldy, rows, slot_of, topk_w, n, top_k, N,
+                            static_cast<const T *>(residual), ldr, static_cast<T *>(out), ldo);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_group_slots(const int *topk_idx, int n, int top_k, int E, int e_lo, int e_hi, int *offsets,
+                               int *slot_token, int *slot_k, int *slot_of, cudaStream_t st) {
+    const long long S = (long long)n * top_k;
+    const int ctas = S <= 4 * kThreads ? 1 : 8;
+    const int smem = (kWarps + 1) * E * 4;
+    cudaError_t err = cudaFuncSetAttribute(group_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, group_slots_kernel, topk_idx, S, top_k, E, e_lo, e_hi, offsets, slot_token,
+                              slot_k, slot_of);
+}
+
+cudaError_t launch_combine_slots(int dtype, const void *y, long long ldy, int rows, const int *slot_of,
+                                 const float *topk_w, int n, int top_k, int N, const void *residual,
+                                 long long ldr, void *out, long long ldo, cudaStream_t st) {
+    if (dtype == MOE_DTYPE_BF16)
+        return combine<__nv_bfloat16>(y, ldy, rows, slot_of, topk_w, n, top_k, N, residual, ldr, out, ldo, st);
+    return combine<__half>(y, ldy, rows, slot_of, topk_w, n, top_k, N, residual, ldr, out, ldo, st);
+}
+
+}  // namespace ops
+}  // namespace moe

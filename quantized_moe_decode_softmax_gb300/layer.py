@@ -1,5 +1,6 @@
 """Convenience wrappers over the C ABI: resident layer weights and a layer
-object that owns a plan. Argument marshalling only."""
+object that owns a plan, and the 16-bit expert layers that run beside it.
+Argument marshalling only."""
 from __future__ import annotations
 
 from typing import Any, Optional
@@ -7,6 +8,7 @@ from typing import Any, Optional
 import numpy as np
 
 from . import _abi
+from .ops import LinearWeights, moe_combine_slots, moe_group_slots, moe_grouped_linear, moe_linear
 
 _DT = {"f32": _abi.MOE_DTYPE_F32, "bf16": _abi.MOE_DTYPE_BF16}
 
@@ -79,13 +81,19 @@ class MoeDecodeLayer:
         import torch
         return torch.float32 if self.out_dtype == "f32" else torch.bfloat16
 
-    def forward(self, x, w: DeviceLayer, out=None, stream=None):
+    def forward(self, x, w: DeviceLayer, out=None, stream=None, shared=None):
+        """One step. shared: a SharedExpert whose output is added to the routed
+        experts' (16-bit activations and output: its type)."""
         import torch
         n = x.shape[0]
+        if shared is not None and (out.dtype if out is not None else self._out_torch_dtype()) != shared.dtype:
+            raise TypeError(f"the shared expert is {shared.dtype}: the step's output has to be, too")
         if out is None:
             out = torch.empty((n, w.D), dtype=self._out_torch_dtype(), device=x.device)
         _abi.moe_decode_forward(self.plan, x, w.router_w, w.router_bias, w.c_planes, n,
                                 self.cfg.top_k, out, stream)
+        if shared is not None:
+            shared.forward(x, residual=out, out=out, stream=stream)
         return out
 
     def forward_layers(self, steps, stream=None):
@@ -118,3 +126,41 @@ class MoeDecodeLayer:
             self.close()
         except Exception:
             pass
+
+
+class SharedExpert:
+    """A 16-bit expert that every token takes: down(act(x gate^T) * (x up^T)).
+    gate, up [F, D], down [D, F]; two launches (moe_linear)."""
+
+    def __init__(self, gate, up, down, activation: str = "silu", act_limit: float = 0.0):
+        self.gate_up = LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit)
+        self.down = LinearWeights(down)
+        if (self.down.N, self.down.K) != (self.gate_up.K, self.gate_up.N):
+            raise ValueError(f"down {tuple(down.shape)} does not fit gate {tuple(gate.shape)}")
+        self.dtype = self.down.dtype
+
+    def forward(self, x, residual=None, out=None, stream=None):
+        """[n, D] -> [n, D], plus `residual` (which `out` may be)."""
+        h = moe_linear(x, self.gate_up, stream=stream)
+        return moe_linear(h, self.down, residual=residual, out=out, stream=stream)
+
+
+class RoutedExperts:
+    """Experts with 16-bit weights under any router: gate, up [E, F, D], down
+    [E, D, F]. The router's top-k ids and weights are arguments of forward, which
+    groups the slots, runs the two grouped products and combines. experts: (begin,
+    end) of the expert ids whose slots are run (the weights cover all E ids)."""
+
+    def __init__(self, gate, up, down, activation: str = "silu", act_limit: float = 0.0, experts=None):
+        self.gate_up = LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit)
+        self.down = LinearWeights(down)
+        if (self.down.E, self.down.N, self.down.K) != (self.gate_up.E, self.gate_up.K, self.gate_up.N):
+            raise ValueError(f"down {tuple(down.shape)} does not fit gate {tuple(gate.shape)}")
+        self.experts = experts
+
+    def forward(self, x, topk_idx, topk_w, residual=None, out=None, stream=None):
+        """x [n, D], topk_idx [n, k] int32, topk_w [n, k] float32 -> [n, D]."""
+        g = moe_group_slots(topk_idx, self.gate_up.E, experts=self.experts, stream=stream)
+        h = moe_grouped_linear(x, self.gate_up, g.offsets, row_token=g.slot_token, stream=stream)
+        y = moe_grouped_linear(h, self.down, g.offsets, stream=stream)
+        return moe_combine_slots(y, g.slot_of, topk_w, residual=residual, out=out, stream=stream)
