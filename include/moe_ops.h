@@ -26,7 +26,8 @@
  *     call on the device before a capture: it loads the kernels). Calls on
  *     different streams or from several host threads are independent.
  *   - Calls are asynchronous on the stream. Argument errors are returned by the
- *     host checks and nothing is launched.
+ *     host checks and nothing is launched. moe_ops_check reports a device-side
+ *     wait that gave up.
  *   - Results do not depend on timing: the order of every sum is fixed by the
  *     sizes, types and alignment alone.
  *   - Sums run in f32; each result is rounded once, to the output's type. A
@@ -135,6 +136,12 @@ moe_status moe_group_slots(const int32_t *topk_idx, int n, int top_k, int E, int
 moe_status moe_combine_slots(int dtype, const void *y, int64_t ldy, int rows, const int32_t *slot_of,
                              const float *topk_w, int n, int top_k, int N, const void *residual,
                              int64_t ldr, void *out, int64_t ldo, void *stream);
+
+/* Synchronise `stream` and report a device-side wait of these operators on the
+ * current device that gave up (MOE_ERR_TIMEOUT: every wait inside a kernel is
+ * bounded, about 1 s; outputs since the last check are then invalid), then
+ * clear it. Not for a stream that is being captured. */
+moe_status moe_ops_check(void *stream);
 
 #ifdef __cplusplus
 }

@@ -58,7 +58,17 @@ Product product_of(const moe_product *p) {
     return a;
 }
 
-moe_status run(const Product &a, cudaStream_t st) { return of(launch_product_rows(a, st)); }
+// rows of a typical group up to which the weights are streamed (ops_rows.cu)
+constexpr int kStreamRows = 16;
+
+moe_status run(const Product &a, cudaStream_t st) {
+    const int groups = a.offsets ? min(a.E, a.rows) : 1;
+    if (a.rows > (long long)groups * kStreamRows) {
+        const cudaError_t err = launch_product_gemm(a, st);
+        if (err != cudaErrorNotSupported) return of(err);
+    }
+    return of(launch_product_rows(a, st));
+}
 
 }  // namespace
 
@@ -135,6 +145,12 @@ moe_status moe_combine_slots(int dtype, const void *y, int64_t ldy, int rows, co
     if (n == 0) return MOE_OK;
     return of(launch_combine_slots(dtype, y, ldy, rows, slot_of, topk_w, n, top_k, N, residual, ldr, out, ldo,
                                    static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_ops_check(void *stream) {
+    unsigned status = 0;
+    const moe_status st = of(read_ops_status(&status, static_cast<cudaStream_t>(stream)));
+    return st != MOE_OK ? st : status ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 
 }  // extern "C"

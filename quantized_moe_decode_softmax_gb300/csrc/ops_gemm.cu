@@ -1,0 +1,505 @@
+// ops_gemm.cu -- products over many rows (moe_linear, moe_grouped_linear) on the
+// 5th-generation tensor cores.
+//
+//   out[r, c] = act(sum_k x[r, k] w[c, k] + bias[c]) (* the up product) (+ residual[r, c])
+//
+// The tile is transposed: the weights are the M operand (128 output columns per
+// CTA, one per tensor-memory lane) and the rows of x are the N operand, up to 256
+// of them (128 for a gated product, which keeps two accumulators).
+//   - N is any multiple of 16, so a ragged group wastes at most 15 rows of its
+//     last tile, where a 128-row M tile would waste up to 127: the groups of a
+//     prompt hold a few hundred rows each. A group is cut into equal tiles.
+//   - A thread of the epilogue owns one output column: its bias is a register,
+//     a warp's store of one row is 64 adjacent bytes, and neither odd sizes nor
+//     unaligned rows need another path. A gated product finds gate and up of an
+//     output in the same lane.
+//
+// Persistent CTAs (one per SM) walk the work items (group, block of output
+// columns, tile of rows) in a fixed order. Warp 0 loads: per step of 64 inputs
+// the weight boxes and the rows of x (32-row boxes, or tile::gather4 through
+// row_token) by TMA with the 128-byte swizzle into a ring of stages. Warp 1 issues
+// the MMAs. Warps 4..7 run the epilogue of the previous tile meanwhile
+// (two accumulator sets in tensor memory). Inputs past K read as zeros in both
+// operands; rows past the group's end are computed and not stored, and since
+// the rows of a product do not mix, what they hold (even NaN) does not matter.
+//
+// Every wait is bounded (1 s, reported through moe_ops_check); after one gives
+// up, all roles stop and the CTA waits for its copies in flight before it ends.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "ops_common.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace ops {
+namespace {
+
+constexpr int kM = 128;            // output columns per CTA
+constexpr int kK = 64;             // inputs per stage: one 128-byte row of a swizzled tile
+constexpr int kTileA = kM * kK * 2;
+constexpr int kBoxRows = 32;       // rows of x per TMA box
+constexpr int kMaxStages = 8;
+constexpr int kBand = 8;           // row tiles that share their pass over the weights
+constexpr int kThreads = 256;
+constexpr int kTmemCols = 512;
+constexpr unsigned long long kWaitNs = 1000000000ull;
+
+// [0]: set when a wait gave up, until moe_ops_check reads it
+__device__ unsigned g_ops_status[4];
+
+struct Tiling {
+    int tcap;       // rows per tile, a multiple of 32
+    int stages;
+    int stage_bytes;
+    int mblocks;    // blocks of output columns
+};
+
+__device__ __forceinline__ unsigned long long globaltimer() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// wait for an mbarrier phase; false once any role of the CTA gave up
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (ptx::mbar_try_wait_hint(bar, parity, 20000u)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            atomicOr(&g_ops_status[0], 1u);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_3d(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// four rows of a map whose box is one row high
+__device__ __forceinline__ void tma_gather4(void *dst, const void *map, int x, const int (&r)[4], uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+        "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// 32 consecutive f32 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// A group of c rows in equal tiles of at most tcap rows: rows per tile, a multiple of 16
+__device__ __forceinline__ int tile_rows(int c, int tcap) {
+    const int nt = (c + tcap - 1) / tcap;
+    return ((c + nt - 1) / nt + 15) & ~15;
+}
+
+// One work item.
+struct Item {
+    int e;          // expert
+    int r0, rows;   // first row and number of rows to store
+    int T;          // rows of the tile's MMAs
+    int m;          // block of output columns
+};
+
+// The items of all groups, numbered group by group: first[e] is the first of
+// group e (shared memory; null: one group).
+struct Walk {
+    const Product &p;
+    const Tiling &g;
+    const int *first;
+    int total;
+
+    __device__ __forceinline__ bool get(int i, Item &it) const {
+        if (i >= total) return false;
+        int e = 0;
+        if (first) {  // the last group that starts at or before item i
+            int hi = p.E;
+            while (hi - e > 1) {
+                const int mid = (e + hi) >> 1;
+                if (first[mid] <= i) e = mid;
+                else hi = mid;
+            }
+            i -= first[e];
+        }
+        int lo, hi;
+        group_rows(p, e, lo, hi);
+        const int c = hi - lo, T = tile_rows(c, g.tcap), nt = (c + T - 1) / T;
+        // bands of kBand row tiles: the tiles of a band run side by side on one
+        // weight block, then on the next
+        const int per_band = kBand * g.mblocks, band = i / per_band, r = i - band * per_band;
+        const int bh = min(kBand, nt - band * kBand);
+        it.e = e;
+        it.m = r / bh;
+        it.T = T;
+        it.r0 = lo + (band * kBand + r % bh) * T;
+        it.rows = min(T, hi - it.r0);
+        return true;
+    }
+};
+
+template <typename T, int MATS>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_gemm_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling g,
+                        const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
+                        const __grid_constant__ CUtensorMap tmu) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tslot;
+    __shared__ int abort_word, warp_sum[kThreads / 32];
+    volatile int *abort_flag = &abort_word;
+    unsigned char *ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    int *first = reinterpret_cast<int *>(ring + g.stages * g.stage_bytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        abort_word = 0;
+        for (int i = 0; i < g.stages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&acc_full[i], 1);
+            ptx::mbar_init(&acc_empty[i], 4);  // the epilogue's warps
+        }
+        ptx::mbar_fence_init();
+        ptx::prefetch_tensormap(&tmx);
+        ptx::prefetch_tensormap(&tmw);
+        if (MATS == 2) ptx::prefetch_tensormap(&tmu);
+    }
+    if (warp == 2) tc::tmem_alloc(&tslot, kTmemCols);
+    int total;
+    if (p.offsets) {
+        // items per group and their exclusive prefix, 256 groups at a time
+        int base = 0;
+        for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+            const int e = e0 + tid;
+            int items = 0;
+            if (e < p.E) {
+                int lo, hi;
+                group_rows(p, e, lo, hi);
+                if (hi > lo) {
+                    const int t = tile_rows(hi - lo, g.tcap);
+                    items = (hi - lo + t - 1) / t * g.mblocks;
+                }
+            }
+            int scan = items;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, scan, d);
+                if (lane >= d) scan += v;
+            }
+            if (lane == 31) warp_sum[warp] = scan;
+            __syncthreads();
+            int before = base, sum = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) before += warp_sum[w];
+                sum += warp_sum[w];
+            }
+            if (e < p.E) first[e] = before + scan - items;
+            base += sum;
+            __syncthreads();
+        }
+        total = base;
+    } else {
+        const int t = tile_rows(p.rows, g.tcap);
+        total = (p.rows + t - 1) / t * g.mblocks;
+        first = nullptr;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tslot;
+    const Walk walk{p, g, first, total};
+    const int nk = (p.K + kK - 1) / kK;
+
+    if (warp == 0) {
+        // ---- loads ------------------------------------------------------------
+        int s = 0, fills = 0;
+        uint32_t ph = 1;  // a fresh barrier passes the wait for its previous phase
+        Item it;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && walk.get(i, it); i += gridDim.x) {
+            int rows[2][4] = {};
+            if (p.row_token) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // rows past the end repeat the last one
+                        rows[h][j] = input_row(p, min(it.r0 + 4 * (lane + 32 * h) + j, it.r0 + it.rows - 1));
+            }
+            const int boxes = (it.T + kBoxRows - 1) / kBoxRows;
+            const uint32_t bytes = MATS * kTileA + (p.row_token ? it.T : boxes * kBoxRows) * 128;
+            for (int k = 0; k < nk; ++k) {
+                ok = __all_sync(0xffffffffu, wait(&empty[s], ph, abort_flag));
+                if (!ok) break;
+                unsigned char *st = ring + s * g.stage_bytes;
+                unsigned char *xb = st + MATS * kTileA;
+                if (lane == 0) {
+                    tc::arrive_expect_tx(&full[s], bytes);
+                    tma_3d(st, &tmw, k * kK, it.m * kM, it.e, &full[s]);
+                    if (MATS == 2) tma_3d(st + kTileA, &tmu, k * kK, it.m * kM, it.e, &full[s]);
+                }
+                if (p.row_token) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (4 * (lane + 32 * h) < it.T)
+                            tma_gather4(xb + (lane + 32 * h) * 512, &tmx, k * kK, rows[h], &full[s]);
+                } else if (lane < boxes) {
+                    tc::tma_load_2d(xb + lane * kBoxRows * 128, &tmx, k * kK, it.r0 + lane * kBoxRows, &full[s]);
+                }
+                __syncwarp();
+                if (++fills, ++s == g.stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        // every copy has landed before the CTA may end (they have, unless a wait gave up)
+        for (int i = 0; i < min(fills, g.stages); ++i) {
+            const int f = fills - 1 - i;  // the fill with this number
+            const unsigned long long t0 = globaltimer();
+            while (!ptx::mbar_try_wait_hint(&full[f % g.stages], (uint32_t)((f / g.stages) & 1), 20000u) &&
+                   globaltimer() - t0 < kWaitNs) {
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMAs --------------------------------------------------------------
+        int s = 0, n = 0;
+        uint32_t ph = 0;
+        Item it;
+        bool ok = true;
+        const uint32_t base = p.dtype == MOE_DTYPE_BF16 ? tc::idesc_bf16_f32(kM, 0) : tc::idesc_f16_f32(kM, 0);
+        for (int i = blockIdx.x; ok && walk.get(i, it); i += gridDim.x, ++n) {
+            const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
+            const uint32_t acc = tmem + (uint32_t)((n & 1) * MATS * g.tcap);
+            // the epilogue of the tile before last has read this accumulator set
+            ok = __all_sync(0xffffffffu, wait(&acc_empty[n & 1], (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag));
+            if (!ok) break;
+            tc::fence_after_sync();
+            for (int k = 0; k < nk; ++k) {
+                ok = __all_sync(0xffffffffu, wait(&full[s], ph, abort_flag));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t st = tc::smem_u32(ring + s * g.stage_bytes);
+                const uint64_t bd = tc::smem_desc_sw128(st + MATS * kTileA, 1024);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m) {
+                        const uint64_t ad = tc::smem_desc_sw128(st + m * kTileA, 1024);
+#pragma unroll
+                        for (int q = 0; q < kK / 16; ++q)
+                            tc::mma_f16(acc + (uint32_t)(m * g.tcap), ad + 2 * q, bd + 2 * q, idesc, (k | q) ? 1u : 0u);
+                    }
+                    tc::commit(&empty[s]);
+                    if (k == nk - 1) tc::commit(&acc_full[n & 1]);
+                }
+                __syncwarp();
+                if (++s == g.stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
+            __shared__ uint64_t drain;
+            if (tc::elect_one()) {
+                ptx::mbar_init(&drain, 1);
+                ptx::mbar_fence_init();
+                tc::commit(&drain);
+                const unsigned long long t0 = globaltimer();
+                while (!ptx::mbar_try_wait_hint(&drain, 0, 20000u) && globaltimer() - t0 < kWaitNs) {
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue ----------------------------------------------------------
+        const int q = warp & 3;  // the lanes this warp can read
+        const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
+        int n = 0;
+        Item it;
+        for (int i = blockIdx.x; walk.get(i, it); i += gridDim.x, ++n) {
+            const int c = it.m * kM + 32 * q + lane;
+            const bool mine = c < p.N;
+            float b0 = 0.f, b1 = 0.f;
+            if (mine && p.bias) b0 = to_f32(static_cast<const T *>(p.bias)[(size_t)it.e * p.N + c]);
+            if (MATS == 2 && mine && p.bias_up) b1 = to_f32(static_cast<const T *>(p.bias_up)[(size_t)it.e * p.N + c]);
+            if (!__all_sync(0xffffffffu, wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1), abort_flag))) break;
+            tc::fence_after_sync();
+            const uint32_t acc = tlane + (uint32_t)((n & 1) * MATS * g.tcap);
+            const T *res = p.residual ? static_cast<const T *>(p.residual) + (size_t)it.r0 * p.ldr + c : nullptr;
+            T *out = static_cast<T *>(p.out) + (size_t)it.r0 * p.ldo + c;
+            for (int t0 = 0; t0 < it.rows; t0 += 32) {
+                uint32_t v[32], u[MATS == 2 ? 32 : 1];
+                tmem_ld32(acc + t0, v);
+                if constexpr (MATS == 2) tmem_ld32(acc + g.tcap + t0, u);
+                float r[32];
+                if (res) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        r[j] = mine && t0 + j < it.rows ? to_f32(res[(size_t)(t0 + j) * p.ldr]) : 0.f;
+                }
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float o = __uint_as_float(v[j]) + b0;
+                    if constexpr (MATS == 2) o = gated_act(p.act, p.limit, o, __uint_as_float(u[j]) + b1);
+                    else o = unary_act(p.act, o);
+                    if (res) o += r[j];
+                    if (mine && t0 + j < it.rows) out[(size_t)(t0 + j) * p.ldo] = from_f32<T>(o);
+                }
+            }
+            tc::fence_before_sync();
+            if (lane == 0) ptx::mbar_arrive(&acc_empty[n & 1], 1);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// the driver's tensor-map encoder, resolved once; null if there is none
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        PFN_cuTensorMapEncodeTiled_v12000 r = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        cudaGetLastError();
+        return r;
+    }();
+    return fn;
+}
+
+// 16-bit rows of `cols` elements `ld` apart, `planes` of them (rank 3) or one
+// (rank 2), boxes of 64 columns x box_rows rows; what lies outside reads as zeros
+bool encode(CUtensorMap *m, int dtype, const void *base, long long cols, long long rows, long long ld, int planes,
+            long long stride, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const int rank = planes ? 3 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(planes ? planes : 1)};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {(cuuint32_t)kK, (cuuint32_t)box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// what a launch needs to know of a device, looked up once
+struct Device {
+    std::atomic<int> sms{0}, smem{0};
+    std::atomic<unsigned> ready{0};  // kernels whose shared-memory limit is raised
+};
+constexpr int kMaxDevices = 64;
+Device g_devices[kMaxDevices];
+
+template <typename T, int MATS>
+cudaError_t launch(const Product &p, const Tiling &g, int items, int smem, Device &d, int sms, const CUtensorMap &tmx,
+                   const CUtensorMap &tmw, const CUtensorMap &tmu, cudaStream_t st) {
+    auto k = product_gemm_kernel<T, MATS>;
+    const unsigned bit = 1u << (MATS - 1 + (p.dtype == MOE_DTYPE_BF16 ? 2 : 0));
+    if (!(d.ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     d.smem.load(std::memory_order_relaxed));
+        if (err != cudaSuccess) return err;
+        d.ready.fetch_or(bit, std::memory_order_release);
+    }
+    k<<<items < sms ? items : sms, kThreads, smem, st>>>(p, g, tmx, tmw, tmu);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    Device &d = g_devices[dev];
+    int sms = d.sms.load(std::memory_order_acquire);
+    if (sms == 0) {
+        int smem = 0;
+        cudaFuncAttributes fa;
+        if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+            (err = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+            (err = cudaFuncGetAttributes(&fa, product_gemm_kernel<__half, 2>)) != cudaSuccess)
+            return err;
+        d.smem.store(smem - (int)((fa.sharedSizeBytes + 127) / 128 * 128), std::memory_order_relaxed);
+        d.sms.store(sms, std::memory_order_release);
+    }
+    const int mats = p.w_up ? 2 : 1;
+    const int mblocks = (p.N + kM - 1) / kM;
+    // rows per tile: the largest that double-buffers in tensor memory, or fewer
+    // where that leaves SMs without an item
+    const int groups = p.offsets ? min(p.E, p.rows) : 1;
+    const long long mean = (p.rows + groups - 1) / groups;
+    int tcap = mats == 2 ? 128 : 256;
+    while (tcap > 32 && (long long)groups * mblocks * ((mean + tcap - 1) / tcap) < sms) tcap /= 2;
+    Tiling g;
+    g.tcap = tcap;
+    g.stage_bytes = mats * kTileA + tcap * 128;
+    g.mblocks = mblocks;
+    const int table = p.offsets ? p.E * 4 : 0;
+    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table;
+    g.stages = min(kMaxStages, budget / g.stage_bytes);
+    if (g.stages < 2) return cudaErrorNotSupported;
+    const int smem = 1024 + g.stages * g.stage_bytes + table;
+    const long long most = ((p.rows + 15) / 16 + groups) * (long long)mblocks;  // bound of the number of items
+    if (most > 0x7fffffffLL) return cudaErrorNotSupported;
+    alignas(64) CUtensorMap tmx, tmw, tmu;
+    if (!encode(&tmx, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||
+        !encode(&tmw, p.dtype, p.w, p.K, p.N, p.ldw, p.E, p.E > 1 ? p.stride_e : p.ldw * p.N, kM))
+        return cudaErrorNotSupported;
+    tmu = tmw;
+    if (mats == 2 && !encode(&tmu, p.dtype, p.w_up, p.K, p.N, p.ldw, p.E, p.E > 1 ? p.stride_e : p.ldw * p.N, kM))
+        return cudaErrorNotSupported;
+    const int items = (int)min(most, (long long)sms);
+    if (p.dtype == MOE_DTYPE_BF16)
+        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, items, smem, d, sms, tmx, tmw, tmu, st)
+                         : launch<__nv_bfloat16, 1>(p, g, items, smem, d, sms, tmx, tmw, tmu, st);
+    return mats == 2 ? launch<__half, 2>(p, g, items, smem, d, sms, tmx, tmw, tmu, st)
+                     : launch<__half, 1>(p, g, items, smem, d, sms, tmx, tmw, tmu, st);
+}
+
+cudaError_t read_ops_status(unsigned *value, cudaStream_t st) {
+    *value = 0;
+    cudaError_t err = cudaMemcpyFromSymbolAsync(value, g_ops_status, 4, 0, cudaMemcpyDeviceToHost, st);
+    if (err == cudaSuccess) err = cudaStreamSynchronize(st);
+    if (err != cudaSuccess || *value == 0) return err;
+    const unsigned zero = 0;
+    err = cudaMemcpyToSymbolAsync(g_ops_status, &zero, 4, 0, cudaMemcpyHostToDevice, st);
+    return err == cudaSuccess ? cudaStreamSynchronize(st) : err;
+}
+
+}  // namespace ops
+}  // namespace moe

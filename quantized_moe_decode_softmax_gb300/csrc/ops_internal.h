@@ -27,6 +27,11 @@ struct Product {
 
 // few rows per expert: the weights are streamed once per 32 rows (ops_rows.cu)
 cudaError_t launch_product_rows(const Product &p, cudaStream_t st);
+// many rows per expert: tcgen05 (ops_gemm.cu); cudaErrorNotSupported, with nothing
+// launched, where the driver declines a tensor map
+cudaError_t launch_product_gemm(const Product &p, cudaStream_t st);
+// the status word of the current device's operators, cleared if it was set
+cudaError_t read_ops_status(unsigned *value, cudaStream_t st);
 
 cudaError_t launch_group_slots(const int *topk_idx, int n, int top_k, int E, int e_lo, int e_hi, int *offsets,
                                int *slot_token, int *slot_k, int *slot_of, cudaStream_t st);

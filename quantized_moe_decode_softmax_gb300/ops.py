@@ -17,7 +17,7 @@ MOE_DTYPE_F16 = 2
 MOE_EPI_NONE, MOE_EPI_SILU, MOE_EPI_GELU, MOE_EPI_GELU_TANH = range(4)
 ACTIVATIONS = {"none": MOE_EPI_NONE, "silu": MOE_EPI_SILU, "gelu": MOE_EPI_GELU, "gelu_tanh": MOE_EPI_GELU_TANH}
 
-OPS_EXPORTED = ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots")
+OPS_EXPORTED = ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots", "moe_ops_check")
 
 
 class moe_product(ctypes.Structure):
@@ -40,6 +40,7 @@ def _lib():
         L.moe_grouped_linear.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i64, vp]
         L.moe_group_slots.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_combine_slots.argtypes = [i32, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp]
+        L.moe_ops_check.argtypes = [vp]
         for name in OPS_EXPORTED:
             getattr(L, name).restype = i32
         _fns = L
@@ -265,3 +266,9 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
                                                  None if residual is None else residual.data_ptr(), ldr,
                                                  out.data_ptr(), ldo, st), "moe_combine_slots")
     return out
+
+
+def moe_ops_check(stream=None) -> None:
+    """Synchronise `stream` (the current one by default) and raise MoeError for a
+    device-side wait of these operators that gave up since the last check."""
+    _abi._check(_lib().moe_ops_check(_abi._stream(stream)), "moe_ops_check")

@@ -216,7 +216,7 @@ def test_grouped_bounds_offsets_and_tokens(rows):
     out = buf[32:32 + rows]
     check_grouped(x, {"w": w}, [half, rows - half - 2], "none", out[:rows - 2])
     assert bool((buf[:32] == 7).all()) and bool((buf[32 + rows:] == 7).all())
-    q.moe_ops_check() if hasattr(q, "moe_ops_check") else torch.cuda.synchronize()
+    q.moe_ops_check()
 
 
 SLOTS = [(1, 1, 1, 0, 1), (1, 8, 128, 0, 128), (3, 2, 5, 1, 4), (8, 8, 128, 0, 128), (33, 4, 16, 0, 16),
