@@ -3,28 +3,34 @@
 //
 //   out[r, c] = act(sum_k x[r, k] w[c, k] + bias[c]) (* the up product) (+ residual[r, c])
 //
-// The tile is transposed: the weights are the M operand (128 output columns per
-// CTA, one per tensor-memory lane) and the rows of x are the N operand, up to 256
-// of them (128 for a gated product, which keeps two accumulators).
-//   - N is any multiple of 16, so a ragged group wastes at most 15 rows of its
-//     last tile, where a 128-row M tile would waste up to 127: the groups of a
-//     prompt hold a few hundred rows each. A group is cut into equal tiles.
+// A pair of CTAs (one cluster, cta_group::2 MMAs) shares a tile. The tile is
+// transposed: the weights are the M operand (256 output columns, 128 per CTA, one
+// per tensor-memory lane) and the rows of x are the N operand, up to 256 of them
+// (128 for a gated product, which keeps two accumulators).
+//   - N is any multiple of 32, so a ragged group wastes at most 31 rows of its
+//     tiles, where a 128-row M tile would waste up to 127: the groups of a prompt
+//     hold a few hundred rows each. A group is cut into equal tiles.
 //   - A thread of the epilogue owns one output column: its bias is a register,
 //     a warp's store of one row is 64 adjacent bytes, and neither odd sizes nor
 //     unaligned rows need another path. A gated product finds gate and up of an
 //     output in the same lane.
+//   - Each CTA of the pair loads its own weights and half of the rows; the MMA
+//     reads both halves. Per step of 64 inputs a CTA fetches 32 KB (gated: 40 KB)
+//     from L2 for 512 tensor-core cycles; alone it would fetch 48 KB, which the
+//     way from L2 to the SMs cannot sustain.
 //
-// Persistent CTAs (one per SM) walk the work items (group, block of output
-// columns, tile of rows) in a fixed order. Warp 0 loads: per step of 64 inputs
-// the weight boxes and the rows of x (32-row boxes, or tile::gather4 through
-// row_token) by TMA with the 128-byte swizzle into a ring of stages. Warp 1 issues
-// the MMAs. Warps 4..7 run the epilogue of the previous tile meanwhile
+// Persistent pairs walk the work items (group, block of output columns, tile of
+// rows) in a fixed order. Warps 0..3 load, per step of 64 inputs, the weight
+// boxes and the rows of x (32-row boxes, or tile::gather4 through row_token, four
+// warps wide because a warp issues its copies one lane after the other) by TMA
+// with the 128-byte swizzle into a ring of stages. Warp 8 of the first CTA issues
+// the MMAs for both. Warps 4..7 run the epilogue of the previous tile meanwhile
 // (two accumulator sets in tensor memory). Inputs past K read as zeros in both
 // operands; rows past the group's end are computed and not stored, and since
 // the rows of a product do not mix, what they hold (even NaN) does not matter.
 //
 // Every wait is bounded (1 s, reported through moe_ops_check); after one gives
-// up, all roles stop and the CTA waits for its copies in flight before it ends.
+// up, all roles stop and the pair waits for its copies in flight before it ends.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -38,12 +44,15 @@ namespace ops {
 namespace {
 
 constexpr int kM = 128;            // output columns per CTA
+constexpr int kPair = 2;           // CTAs per tile
 constexpr int kK = 64;             // inputs per stage: one 128-byte row of a swizzled tile
 constexpr int kTileA = kM * kK * 2;
 constexpr int kBoxRows = 32;       // rows of x per TMA box
+constexpr int kStepRows = 32;      // rows per tile come in multiples of this
 constexpr int kMaxStages = 8;
 constexpr int kBand = 8;           // row tiles that share their pass over the weights
-constexpr int kThreads = 256;
+constexpr int kLoaders = 4;        // load warps
+constexpr int kThreads = 288;
 constexpr int kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
@@ -51,10 +60,10 @@ constexpr unsigned long long kWaitNs = 1000000000ull;
 __device__ unsigned g_ops_status[4];
 
 struct Tiling {
-    int tcap;       // rows per tile, a multiple of 32
+    int tcap;       // rows per tile, at most: a multiple of kStepRows
     int stages;
     int stage_bytes;
-    int mblocks;    // blocks of output columns
+    int mblocks;    // blocks of kPair * kM output columns
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -63,12 +72,43 @@ __device__ __forceinline__ unsigned long long globaltimer() {
     return t;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// the cluster address of this CTA's barrier `bar` in the pair's first CTA
+__device__ __forceinline__ uint32_t in_first(const void *bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(bar)));
+    return a;
+}
+
+// barrier phases here are completed by either CTA of the pair
+__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(hint_ns)
+        : "memory");
+    return ok != 0;
+}
+
 // wait for an mbarrier phase; false once any role of the CTA gave up
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (try_wait(bar, parity, 1000u)) return true;
     const unsigned long long t0 = globaltimer();
     for (;;) {
-        if (ptx::mbar_try_wait_hint(bar, parity, 20000u)) return true;
+        if (try_wait(bar, parity, 20000u)) return true;
         if (*abort_flag) return false;
         if (globaltimer() - t0 > kWaitNs) {
             *abort_flag = 1;
@@ -78,20 +118,59 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     }
 }
 
-__device__ __forceinline__ void tma_3d(void *dst, const void *map, int x, int y, int z, uint64_t *bar) {
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// TMA loads into this CTA's shared memory, counted by a barrier of the pair's
+// first CTA (a cluster address)
+__device__ __forceinline__ void tma_2d(void *dst, const void *map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_3d(void *dst, const void *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// four rows of a map whose box is one row high
+__device__ __forceinline__ void tma_gather4(void *dst, const void *map, int x, const int (&r)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]),
+        "r"(r[2]), "r"(r[3]), "r"(bar)
         : "memory");
 }
 
-// four rows of a map whose box is one row high
-__device__ __forceinline__ void tma_gather4(void *dst, const void *map, int x, const int (&r)[4], uint64_t *bar) {
+// D[tmem of both CTAs] (+)= A * B^T: each CTA's shared memory holds its 128 rows of A and
+// half of B's rows; issued by one thread of the first CTA
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-        "r"(tc::smem_u32(bar))
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// arrive on both CTAs' barriers once the MMAs issued before have completed
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
 // 32 consecutive f32 columns of this thread's lane
@@ -109,10 +188,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// A group of c rows in equal tiles of at most tcap rows: rows per tile, a multiple of 16
-__device__ __forceinline__ int tile_rows(int c, int tcap) {
+// A group of c rows in equal tiles of at most tcap rows: rows per tile
+__host__ __device__ __forceinline__ int tile_rows(int c, int tcap) {
     const int nt = (c + tcap - 1) / tcap;
-    return ((c + nt - 1) / nt + 15) & ~15;
+    return ((c + nt - 1) / nt + kStepRows - 1) / kStepRows * kStepRows;
 }
 
 // One work item.
@@ -165,13 +244,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
                         const __grid_constant__ CUtensorMap tmu) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    // full and acc_empty are used in the first CTA only, for both
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tslot;
     __shared__ int abort_word, warp_sum[kThreads / 32];
     volatile int *abort_flag = &abort_word;
     unsigned char *ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     int *first = reinterpret_cast<int *>(ring + g.stages * g.stage_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank();
+    const int item0 = blockIdx.x / kPair, item_step = gridDim.x / kPair;
 
     if (tid == 0) {
         abort_word = 0;
@@ -181,17 +263,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 4);  // the epilogue's warps
+            ptx::mbar_init(&acc_empty[i], 4 * kPair);  // the epilogues' warps
         }
+        ptx::mbar_init(&drain, 1);
         ptx::mbar_fence_init();
         ptx::prefetch_tensormap(&tmx);
         ptx::prefetch_tensormap(&tmw);
         if (MATS == 2) ptx::prefetch_tensormap(&tmu);
     }
-    if (warp == 2) tc::tmem_alloc(&tslot, kTmemCols);
+    if (warp == 8) tmem_alloc_pair(&tslot, kTmemCols);
     int total;
     if (p.offsets) {
-        // items per group and their exclusive prefix, 256 groups at a time
+        // items per group and their exclusive prefix, kThreads groups at a time
         int base = 0;
         for (int e0 = 0; e0 < p.E; e0 += kThreads) {
             const int e = e0 + tid;
@@ -230,72 +313,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
+    cluster_sync();  // the peer's barriers are ready
     tc::fence_after_sync();
     const uint32_t tmem = tslot;
     const Walk walk{p, g, first, total};
     const int nk = (p.K + kK - 1) / kK;
 
-    if (warp == 0) {
+    if (warp < kLoaders) {
         // ---- loads ------------------------------------------------------------
+        const bool gather = p.row_token != nullptr;
         int s = 0, fills = 0;
         uint32_t ph = 1;  // a fresh barrier passes the wait for its previous phase
         Item it;
-        bool ok = true;
-        for (int i = blockIdx.x; ok && walk.get(i, it); i += gridDim.x) {
-            int rows[2][4] = {};
-            if (p.row_token) {
+        bool ok = warp == 0 || gather;
+        for (int i = item0; ok && walk.get(i, it); i += item_step) {
+            const int half = it.T / kPair;                 // rows of x that this CTA loads
+            const int r0 = it.r0 + rank * half;
+            const int at = warp + kLoaders * lane;         // gather: the lane's four rows
+            const bool four = gather && 4 * at < half;
+            int rows[4] = {};
+            if (four) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)  // rows past the end repeat the last one
-                        rows[h][j] = input_row(p, min(it.r0 + 4 * (lane + 32 * h) + j, it.r0 + it.rows - 1));
+                for (int j = 0; j < 4; ++j)  // rows past the end repeat the last one
+                    rows[j] = input_row(p, min(r0 + 4 * at + j, it.r0 + it.rows - 1));
             }
-            const int boxes = (it.T + kBoxRows - 1) / kBoxRows;
-            const uint32_t bytes = MATS * kTileA + (p.row_token ? it.T : boxes * kBoxRows) * 128;
+            const int boxes = (half + kBoxRows - 1) / kBoxRows;
+            const uint32_t bytes = kPair * (MATS * kTileA + (gather ? half : boxes * kBoxRows) * 128);
+            const int col = (it.m * kPair + rank) * kM;
             for (int k = 0; k < nk; ++k) {
                 ok = __all_sync(0xffffffffu, wait(&empty[s], ph, abort_flag));
                 if (!ok) break;
                 unsigned char *st = ring + s * g.stage_bytes;
                 unsigned char *xb = st + MATS * kTileA;
-                if (lane == 0) {
-                    tc::arrive_expect_tx(&full[s], bytes);
-                    tma_3d(st, &tmw, k * kK, it.m * kM, it.e, &full[s]);
-                    if (MATS == 2) tma_3d(st + kTileA, &tmu, k * kK, it.m * kM, it.e, &full[s]);
+                const uint32_t bar = in_first(&full[s]);
+                if (warp == 0 && lane == 0) {
+                    if (rank == 0) tc::arrive_expect_tx(&full[s], bytes);
+                    tma_3d(st, &tmw, k * kK, col, it.e, bar);
+                    if (MATS == 2) tma_3d(st + kTileA, &tmu, k * kK, col, it.e, bar);
                 }
-                if (p.row_token) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (4 * (lane + 32 * h) < it.T)
-                            tma_gather4(xb + (lane + 32 * h) * 512, &tmx, k * kK, rows[h], &full[s]);
-                } else if (lane < boxes) {
-                    tc::tma_load_2d(xb + lane * kBoxRows * 128, &tmx, k * kK, it.r0 + lane * kBoxRows, &full[s]);
-                }
+                if (four) tma_gather4(xb + at * 512, &tmx, k * kK, rows, bar);
+                if (!gather && lane < boxes)
+                    tma_2d(xb + lane * kBoxRows * 128, &tmx, k * kK, r0 + lane * kBoxRows, bar);
                 __syncwarp();
-                if (++fills, ++s == g.stages) {
+                ++fills;
+                if (++s == g.stages) {
                     s = 0;
                     ph ^= 1;
                 }
             }
         }
-        // every copy has landed before the CTA may end (they have, unless a wait gave up)
-        for (int i = 0; i < min(fills, g.stages); ++i) {
-            const int f = fills - 1 - i;  // the fill with this number
-            const unsigned long long t0 = globaltimer();
-            while (!ptx::mbar_try_wait_hint(&full[f % g.stages], (uint32_t)((f / g.stages) & 1), 20000u) &&
-                   globaltimer() - t0 < kWaitNs) {
+        // every copy has landed before the pair may end (they have, unless a wait gave up)
+        if (warp == 0 && rank == 0)
+            for (int i = 0; i < min(fills, g.stages); ++i) {
+                const int f = fills - 1 - i;  // the fill with this number
+                const unsigned long long t0 = globaltimer();
+                while (!try_wait(&full[f % g.stages], (uint32_t)((f / g.stages) & 1), 20000u) &&
+                       globaltimer() - t0 < kWaitNs) {
+                }
             }
-        }
-    } else if (warp == 1) {
+    } else if (warp == 8 && rank == 0) {
         // ---- MMAs --------------------------------------------------------------
         int s = 0, n = 0;
         uint32_t ph = 0;
         Item it;
         bool ok = true;
-        const uint32_t base = p.dtype == MOE_DTYPE_BF16 ? tc::idesc_bf16_f32(kM, 0) : tc::idesc_f16_f32(kM, 0);
-        for (int i = blockIdx.x; ok && walk.get(i, it); i += gridDim.x, ++n) {
+        const uint32_t base = p.dtype == MOE_DTYPE_BF16 ? tc::idesc_bf16_f32(kPair * kM, 0)
+                                                        : tc::idesc_f16_f32(kPair * kM, 0);
+        for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
             const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
             const uint32_t acc = tmem + (uint32_t)((n & 1) * MATS * g.tcap);
-            // the epilogue of the tile before last has read this accumulator set
+            // the epilogues of the tile before last have read this accumulator set
             ok = __all_sync(0xffffffffu, wait(&acc_empty[n & 1], (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag));
             if (!ok) break;
             tc::fence_after_sync();
@@ -311,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t ad = tc::smem_desc_sw128(st + m * kTileA, 1024);
 #pragma unroll
                         for (int q = 0; q < kK / 16; ++q)
-                            tc::mma_f16(acc + (uint32_t)(m * g.tcap), ad + 2 * q, bd + 2 * q, idesc, (k | q) ? 1u : 0u);
+                            mma_pair(acc + (uint32_t)(m * g.tcap), ad + 2 * q, bd + 2 * q, idesc, (k | q) ? 1u : 0u);
                     }
-                    tc::commit(&empty[s]);
-                    if (k == nk - 1) tc::commit(&acc_full[n & 1]);
+                    commit_pair(&empty[s]);
+                    if (k == nk - 1) commit_pair(&acc_full[n & 1]);
                 }
                 __syncwarp();
                 if (++s == g.stages) {
@@ -324,25 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
-            __shared__ uint64_t drain;
             if (tc::elect_one()) {
-                ptx::mbar_init(&drain, 1);
-                ptx::mbar_fence_init();
-                tc::commit(&drain);
+                commit_pair(&drain);
                 const unsigned long long t0 = globaltimer();
-                while (!ptx::mbar_try_wait_hint(&drain, 0, 20000u) && globaltimer() - t0 < kWaitNs) {
+                while (!try_wait(&drain, 0, 20000u) && globaltimer() - t0 < kWaitNs) {
                 }
             }
             __syncwarp();
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // ---- epilogue ----------------------------------------------------------
         const int q = warp & 3;  // the lanes this warp can read
         const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
         int n = 0;
         Item it;
-        for (int i = blockIdx.x; walk.get(i, it); i += gridDim.x, ++n) {
-            const int c = it.m * kM + 32 * q + lane;
+        for (int i = item0; walk.get(i, it); i += item_step, ++n) {
+            const int c = (it.m * kPair + rank) * kM + 32 * q + lane;
             const bool mine = c < p.N;
             float b0 = 0.f, b1 = 0.f;
             if (mine && p.bias) b0 = to_f32(static_cast<const T *>(p.bias)[(size_t)it.e * p.N + c]);
@@ -373,13 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc::fence_before_sync();
-            if (lane == 0) ptx::mbar_arrive(&acc_empty[n & 1], 1);
+            if (lane == 0) arrive_cluster(in_first(&acc_empty[n & 1]));
         }
     }
     tc::fence_before_sync();
     __syncthreads();
+    cluster_sync();  // neither CTA ends while the other may still use its memory
     tc::fence_after_sync();
-    if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == 8) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 // the driver's tensor-map encoder, resolved once; null if there is none
@@ -417,14 +502,70 @@ bool encode(CUtensorMap *m, int dtype, const void *base, long long cols, long lo
 
 // what a launch needs to know of a device, looked up once
 struct Device {
-    std::atomic<int> sms{0}, smem{0};
+    std::atomic<int> pairs{0};       // CTA pairs that run at once
+    std::atomic<int> smem{0};        // dynamic shared memory a CTA may ask for
     std::atomic<unsigned> ready{0};  // kernels whose shared-memory limit is raised
 };
 constexpr int kMaxDevices = 64;
 Device g_devices[kMaxDevices];
 
+// Rows per tile: the least time of a simple model, waves of tiles on the pairs,
+// each nk steps of the longer of the MMAs (2 rows a cycle per 64 inputs and
+// matrix) and the loads (about 50 bytes a cycle from L2 per SM), plus 2000 cycles
+// for the fill of the ring and the last epilogue.
+int pick_rows(int mats, int mblocks, int groups, int mean, int nk, int pairs) {
+    int best = kStepRows;
+    long long least = -1;
+    for (int cap = mats == 2 ? 128 : 256; cap >= kStepRows; cap -= kStepRows) {
+        const int t = tile_rows(mean, cap);
+        const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
+        const long long waves = (items + pairs - 1) / pairs;
+        const int mma = 2 * mats * t, loads = (mats * kTileA + t / kPair * 128) / 50;
+        const long long cost = waves * ((long long)nk * (mma > loads ? mma : loads) + 2000);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = cap;
+        }
+    }
+    return best;
+}
+
+cudaLaunchConfig_t pair_launch(cudaLaunchAttribute (&attr)[1], int pairs, int smem, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kPair * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+cudaError_t look_up(int dev, Device &d) {
+    int smem = 0, sms = 0, pairs = 0;
+    cudaFuncAttributes fa;
+    cudaError_t err;
+    auto k = product_gemm_kernel<__half, 2>;
+    if ((err = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (err = cudaFuncGetAttributes(&fa, k)) != cudaSuccess)
+        return err;
+    smem -= (int)((fa.sharedSizeBytes + 127) / 128 * 128);
+    if ((err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pair_launch(attr, sms / kPair, smem, nullptr);
+    if ((err = cudaOccupancyMaxActiveClusters(&pairs, k, &cfg)) != cudaSuccess) return err;
+    if (pairs < 1) return cudaErrorNotSupported;
+    d.smem.store(smem, std::memory_order_relaxed);
+    d.pairs.store(min(pairs, sms / kPair), std::memory_order_release);
+    return cudaSuccess;
+}
+
 template <typename T, int MATS>
-cudaError_t launch(const Product &p, const Tiling &g, int items, int smem, Device &d, int sms, const CUtensorMap &tmx,
+cudaError_t launch(const Product &p, const Tiling &g, int pairs, int smem, Device &d, const CUtensorMap &tmx,
                    const CUtensorMap &tmw, const CUtensorMap &tmu, cudaStream_t st) {
     auto k = product_gemm_kernel<T, MATS>;
     const unsigned bit = 1u << (MATS - 1 + (p.dtype == MOE_DTYPE_BF16 ? 2 : 0));
@@ -434,8 +575,9 @@ cudaError_t launch(const Product &p, const Tiling &g, int items, int smem, Devic
         if (err != cudaSuccess) return err;
         d.ready.fetch_or(bit, std::memory_order_release);
     }
-    k<<<items < sms ? items : sms, kThreads, smem, st>>>(p, g, tmx, tmw, tmu);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pair_launch(attr, pairs, smem, st);
+    return cudaLaunchKernelEx(&cfg, k, p, g, tmx, tmw, tmu);
 }
 
 }  // namespace
@@ -446,35 +588,21 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     Device &d = g_devices[dev];
-    int sms = d.sms.load(std::memory_order_acquire);
-    if (sms == 0) {
-        int smem = 0;
-        cudaFuncAttributes fa;
-        if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-            (err = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
-            (err = cudaFuncGetAttributes(&fa, product_gemm_kernel<__half, 2>)) != cudaSuccess)
-            return err;
-        d.smem.store(smem - (int)((fa.sharedSizeBytes + 127) / 128 * 128), std::memory_order_relaxed);
-        d.sms.store(sms, std::memory_order_release);
-    }
+    if (d.pairs.load(std::memory_order_acquire) == 0 && (err = look_up(dev, d)) != cudaSuccess) return err;
+    const int all = d.pairs.load(std::memory_order_acquire);
     const int mats = p.w_up ? 2 : 1;
-    const int mblocks = (p.N + kM - 1) / kM;
-    // rows per tile: the largest that double-buffers in tensor memory, or fewer
-    // where that leaves SMs without an item
+    const int mblocks = (p.N + kPair * kM - 1) / (kPair * kM);
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
-    const long long mean = (p.rows + groups - 1) / groups;
-    int tcap = mats == 2 ? 128 : 256;
-    while (tcap > 32 && (long long)groups * mblocks * ((mean + tcap - 1) / tcap) < sms) tcap /= 2;
     Tiling g;
-    g.tcap = tcap;
-    g.stage_bytes = mats * kTileA + tcap * 128;
+    g.tcap = pick_rows(mats, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kK - 1) / kK, all);
+    g.stage_bytes = mats * kTileA + (g.tcap / kPair + kBoxRows - 1) / kBoxRows * kBoxRows * 128;
     g.mblocks = mblocks;
     const int table = p.offsets ? p.E * 4 : 0;
     const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table;
     g.stages = min(kMaxStages, budget / g.stage_bytes);
     if (g.stages < 2) return cudaErrorNotSupported;
     const int smem = 1024 + g.stages * g.stage_bytes + table;
-    const long long most = ((p.rows + 15) / 16 + groups) * (long long)mblocks;  // bound of the number of items
+    const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     if (most > 0x7fffffffLL) return cudaErrorNotSupported;
     alignas(64) CUtensorMap tmx, tmw, tmu;
     if (!encode(&tmx, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||
@@ -483,12 +611,12 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     tmu = tmw;
     if (mats == 2 && !encode(&tmu, p.dtype, p.w_up, p.K, p.N, p.ldw, p.E, p.E > 1 ? p.stride_e : p.ldw * p.N, kM))
         return cudaErrorNotSupported;
-    const int items = (int)min(most, (long long)sms);
+    const int n = (int)min(most, (long long)all);
     if (p.dtype == MOE_DTYPE_BF16)
-        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, items, smem, d, sms, tmx, tmw, tmu, st)
-                         : launch<__nv_bfloat16, 1>(p, g, items, smem, d, sms, tmx, tmw, tmu, st);
-    return mats == 2 ? launch<__half, 2>(p, g, items, smem, d, sms, tmx, tmw, tmu, st)
-                     : launch<__half, 1>(p, g, items, smem, d, sms, tmx, tmw, tmu, st);
+        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, n, smem, d, tmx, tmw, tmu, st)
+                         : launch<__nv_bfloat16, 1>(p, g, n, smem, d, tmx, tmw, tmu, st);
+    return mats == 2 ? launch<__half, 2>(p, g, n, smem, d, tmx, tmw, tmu, st)
+                     : launch<__half, 1>(p, g, n, smem, d, tmx, tmw, tmu, st);
 }
 
 cudaError_t read_ops_status(unsigned *value, cudaStream_t st) {
