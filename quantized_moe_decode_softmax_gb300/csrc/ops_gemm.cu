@@ -23,8 +23,8 @@
 // rows) in a fixed order. Warps 0..3 load, per step of 64 inputs, the weight
 // boxes and the rows of x (32-row boxes, or tile::gather4 through row_token, four
 // warps wide because a warp issues its copies one lane after the other) by TMA
-// with the 128-byte swizzle into a ring of stages. Warp 8 of the first CTA issues
-// the MMAs for both. Warps 4..7 run the epilogue of the previous tile meanwhile
+// with the 128-byte swizzle into a ring of stages. One warp of the first CTA issues
+// the MMAs for both. Eight warps run the epilogue of the previous tile meanwhile
 // (two accumulator sets in tensor memory). Inputs past K read as zeros in both
 // operands; rows past the group's end are computed and not stored, and since
 // the rows of a product do not mix, what they hold (even NaN) does not matter.
@@ -47,12 +47,14 @@ constexpr int kM = 128;            // output columns per CTA
 constexpr int kPair = 2;           // CTAs per tile
 constexpr int kK = 64;             // inputs per stage: one 128-byte row of a swizzled tile
 constexpr int kTileA = kM * kK * 2;
-constexpr int kBoxRows = 32;       // rows of x per TMA box
+constexpr int kBoxRows = 64;       // rows of x per TMA box
 constexpr int kStepRows = 32;      // rows per tile come in multiples of this
 constexpr int kMaxStages = 8;
 constexpr int kBand = 8;           // row tiles that share their pass over the weights
 constexpr int kLoaders = 4;        // load warps
-constexpr int kThreads = 288;
+constexpr int kEpilogue = 8;       // epilogue warps, two per quadrant of the tensor-memory lanes
+constexpr int kMmaWarp = kLoaders + kEpilogue;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kTmemCols = 512;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
@@ -90,25 +92,12 @@ __device__ __forceinline__ uint32_t in_first(const void *bar) {
     return a;
 }
 
-// barrier phases here are completed by either CTA of the pair
-__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(hint_ns)
-        : "memory");
-    return ok != 0;
-}
-
 // wait for an mbarrier phase; false once any role of the CTA gave up
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    if (try_wait(bar, parity, 1000u)) return true;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
     for (;;) {
-        if (try_wait(bar, parity, 20000u)) return true;
+        if (ptx::mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer() - t0 > kWaitNs) {
             *abort_flag = 1;
@@ -173,16 +162,13 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t addr, uint32_t cols) 
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
-// 32 consecutive f32 columns of this thread's lane
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+// 16 consecutive f32 columns of this thread's lane, complete after tmem_wait_ld
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(addr)
         : "memory");
 }
@@ -263,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 4 * kPair);  // the epilogues' warps
+            ptx::mbar_init(&acc_empty[i], kEpilogue * kPair);  // the epilogues' warps
         }
         ptx::mbar_init(&drain, 1);
         ptx::mbar_fence_init();
@@ -271,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tensormap(&tmw);
         if (MATS == 2) ptx::prefetch_tensormap(&tmu);
     }
-    if (warp == 8) tmem_alloc_pair(&tslot, kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc_pair(&tslot, kTmemCols);
     int total;
     if (p.offsets) {
         // items per group and their exclusive prefix, kThreads groups at a time
@@ -322,38 +308,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kLoaders) {
         // ---- loads ------------------------------------------------------------
         const bool gather = p.row_token != nullptr;
+        // one thread issues its copies one after the other, and that is what limits
+        // a loader: each warp has one box per step (0: w, 1: x, 2: w_up or x's second
+        // box), or with row_token every fourth copy of four rows beside it
         int s = 0, fills = 0;
         uint32_t ph = 1;  // a fresh barrier passes the wait for its previous phase
         Item it;
-        bool ok = warp == 0 || gather;
+        bool ok = gather || warp < 3;
         for (int i = item0; ok && walk.get(i, it); i += item_step) {
-            const int half = it.T / kPair;                 // rows of x that this CTA loads
+            const int half = it.T / kPair;  // rows of x that this CTA loads
             const int r0 = it.r0 + rank * half;
-            const int at = warp + kLoaders * lane;         // gather: the lane's four rows
-            const bool four = gather && 4 * at < half;
-            int rows[4] = {};
-            if (four) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)  // rows past the end repeat the last one
-                    rows[j] = input_row(p, min(r0 + 4 * at + j, it.r0 + it.rows - 1));
-            }
             const int boxes = (half + kBoxRows - 1) / kBoxRows;
             const uint32_t bytes = kPair * (MATS * kTileA + (gather ? half : boxes * kBoxRows) * 128);
             const int col = (it.m * kPair + rank) * kM;
+            const int box = warp == 1 ? 0 : MATS == 1 && warp == 2 ? 1 : boxes;  // of x, without row_token
+            const int fours = gather ? (half / 4 - warp + kLoaders - 1) / kLoaders : 0;
+            int rows[4] = {};  // gather: lane j's rows are the warp's j-th copy
+            if (lane < fours) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // rows past the end repeat the last one
+                    rows[j] = input_row(p, min(r0 + 4 * (warp + kLoaders * lane) + j, it.r0 + it.rows - 1));
+            }
             for (int k = 0; k < nk; ++k) {
                 ok = __all_sync(0xffffffffu, wait(&empty[s], ph, abort_flag));
                 if (!ok) break;
                 unsigned char *st = ring + s * g.stage_bytes;
                 unsigned char *xb = st + MATS * kTileA;
                 const uint32_t bar = in_first(&full[s]);
-                if (warp == 0 && lane == 0) {
-                    if (rank == 0) tc::arrive_expect_tx(&full[s], bytes);
-                    tma_3d(st, &tmw, k * kK, col, it.e, bar);
-                    if (MATS == 2) tma_3d(st + kTileA, &tmu, k * kK, col, it.e, bar);
+                if (tc::elect_one()) {
+                    if (warp == 0) {
+                        if (rank == 0) tc::arrive_expect_tx(&full[s], bytes);
+                        tma_3d(st, &tmw, k * kK, col, it.e, bar);
+                    }
+                    if (MATS == 2 && warp == 2) tma_3d(st + kTileA, &tmu, k * kK, col, it.e, bar);
+                    if (!gather && box < boxes)
+                        tma_2d(xb + box * kBoxRows * 128, &tmx, k * kK, r0 + box * kBoxRows, bar);
                 }
-                if (four) tma_gather4(xb + at * 512, &tmx, k * kK, rows, bar);
-                if (!gather && lane < boxes)
-                    tma_2d(xb + lane * kBoxRows * 128, &tmx, k * kK, r0 + lane * kBoxRows, bar);
+                if (lane < fours) tma_gather4(xb + (warp + kLoaders * lane) * 512, &tmx, k * kK, rows, bar);
                 __syncwarp();
                 ++fills;
                 if (++s == g.stages) {
@@ -367,32 +358,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < min(fills, g.stages); ++i) {
                 const int f = fills - 1 - i;  // the fill with this number
                 const unsigned long long t0 = globaltimer();
-                while (!try_wait(&full[f % g.stages], (uint32_t)((f / g.stages) & 1), 20000u) &&
+                while (!ptx::mbar_try_wait_hint(&full[f % g.stages], (uint32_t)((f / g.stages) & 1), 20000u) &&
                        globaltimer() - t0 < kWaitNs) {
                 }
             }
-    } else if (warp == 8 && rank == 0) {
+        __syncwarp();
+    } else if (warp == kMmaWarp && rank == 0) {
         // ---- MMAs --------------------------------------------------------------
-        int s = 0, n = 0;
-        uint32_t ph = 0;
-        Item it;
-        bool ok = true;
-        const uint32_t base = p.dtype == MOE_DTYPE_BF16 ? tc::idesc_bf16_f32(kPair * kM, 0)
-                                                        : tc::idesc_f16_f32(kPair * kM, 0);
-        for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
-            const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
-            const uint32_t acc = tmem + (uint32_t)((n & 1) * MATS * g.tcap);
-            // the epilogues of the tile before last have read this accumulator set
-            ok = __all_sync(0xffffffffu, wait(&acc_empty[n & 1], (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag));
-            if (!ok) break;
-            tc::fence_after_sync();
-            for (int k = 0; k < nk; ++k) {
-                ok = __all_sync(0xffffffffu, wait(&full[s], ph, abort_flag));
-                if (!ok) break;
+        if (tc::elect_one()) {
+            int s = 0, n = 0;
+            uint32_t ph = 0;
+            Item it;
+            bool ok = true;
+            const uint32_t base = p.dtype == MOE_DTYPE_BF16 ? tc::idesc_bf16_f32(kPair * kM, 0)
+                                                            : tc::idesc_f16_f32(kPair * kM, 0);
+            for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
+                const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
+                const uint32_t acc = tmem + (uint32_t)((n & 1) * MATS * g.tcap);
+                // the epilogues of the tile before last have read this accumulator set
+                if (!(ok = wait(&acc_empty[n & 1], (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag))) break;
                 tc::fence_after_sync();
-                const uint32_t st = tc::smem_u32(ring + s * g.stage_bytes);
-                const uint64_t bd = tc::smem_desc_sw128(st + MATS * kTileA, 1024);
-                if (tc::elect_one()) {
+                for (int k = 0; k < nk; ++k) {
+                    if (!(ok = wait(&full[s], ph, abort_flag))) break;
+                    tc::fence_after_sync();
+                    const uint32_t st = tc::smem_u32(ring + s * g.stage_bytes);
+                    const uint64_t bd = tc::smem_desc_sw128(st + MATS * kTileA, 1024);
 #pragma unroll
                     for (int m = 0; m < MATS; ++m) {
                         const uint64_t ad = tc::smem_desc_sw128(st + m * kTileA, 1024);
@@ -401,27 +391,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_pair(acc + (uint32_t)(m * g.tcap), ad + 2 * q, bd + 2 * q, idesc, (k | q) ? 1u : 0u);
                     }
                     commit_pair(&empty[s]);
-                    if (k == nk - 1) commit_pair(&acc_full[n & 1]);
+                    if (++s == g.stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
-                __syncwarp();
-                if (++s == g.stages) {
-                    s = 0;
-                    ph ^= 1;
-                }
+                if (ok) commit_pair(&acc_full[n & 1]);
             }
-        }
-        if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
-            if (tc::elect_one()) {
+            if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
                 commit_pair(&drain);
                 const unsigned long long t0 = globaltimer();
-                while (!try_wait(&drain, 0, 20000u) && globaltimer() - t0 < kWaitNs) {
+                while (!ptx::mbar_try_wait_hint(&drain, 0, 20000u) && globaltimer() - t0 < kWaitNs) {
                 }
             }
-            __syncwarp();
         }
-    } else if (warp >= 4 && warp < 8) {
+        __syncwarp();
+    } else if (warp >= kLoaders && warp < kMmaWarp) {
         // ---- epilogue ----------------------------------------------------------
-        const int q = warp & 3;  // the lanes this warp can read
+        const int q = warp & 3;                  // the lanes this warp can read
+        const int part = (warp - kLoaders) >> 2; // its half of the tile's chunks of 16 rows
         const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
         int n = 0;
         Item it;
@@ -431,30 +419,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             float b0 = 0.f, b1 = 0.f;
             if (mine && p.bias) b0 = to_f32(static_cast<const T *>(p.bias)[(size_t)it.e * p.N + c]);
             if (MATS == 2 && mine && p.bias_up) b1 = to_f32(static_cast<const T *>(p.bias_up)[(size_t)it.e * p.N + c]);
+            const int rows = mine ? it.rows : 0;  // rows this thread stores
+            const T *res = static_cast<const T *>(p.residual);
+            if (res) res += (size_t)it.r0 * p.ldr + c;
+            T *out = static_cast<T *>(p.out) + (size_t)it.r0 * p.ldo + c;
+            float r[16], rn[16];
+            // a residual is read one chunk ahead, the first before the tile is done
+            auto load_res = [&](float (&d)[16], int t0) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) d[j] = t0 + j < rows ? to_f32(res[(size_t)(t0 + j) * p.ldr]) : 0.f;
+            };
+            if (res) load_res(rn, 16 * part);
             if (!__all_sync(0xffffffffu, wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1), abort_flag))) break;
             tc::fence_after_sync();
             const uint32_t acc = tlane + (uint32_t)((n & 1) * MATS * g.tcap);
-            const T *res = p.residual ? static_cast<const T *>(p.residual) + (size_t)it.r0 * p.ldr + c : nullptr;
-            T *out = static_cast<T *>(p.out) + (size_t)it.r0 * p.ldo + c;
-            for (int t0 = 0; t0 < it.rows; t0 += 32) {
-                uint32_t v[32], u[MATS == 2 ? 32 : 1];
-                tmem_ld32(acc + t0, v);
-                if constexpr (MATS == 2) tmem_ld32(acc + g.tcap + t0, u);
-                float r[32];
+            for (int t0 = 16 * part; t0 < it.rows; t0 += 32) {
+                float v[16], u[MATS == 2 ? 16 : 1];
+                tmem_ld16(acc + t0, v);
+                if constexpr (MATS == 2) tmem_ld16(acc + g.tcap + t0, u);
                 if (res) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        r[j] = mine && t0 + j < it.rows ? to_f32(res[(size_t)(t0 + j) * p.ldr]) : 0.f;
+                    for (int j = 0; j < 16; ++j) r[j] = rn[j];
+                    load_res(rn, t0 + 32);
                 }
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float o = __uint_as_float(v[j]) + b0;
-                    if constexpr (MATS == 2) o = gated_act(p.act, p.limit, o, __uint_as_float(u[j]) + b1);
-                    else o = unary_act(p.act, o);
-                    if (res) o += r[j];
-                    if (mine && t0 + j < it.rows) out[(size_t)(t0 + j) * p.ldo] = from_f32<T>(o);
+                for (int j = 0; j < 16; ++j) v[j] += b0;
+                if constexpr (MATS == 2) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) u[j] += b1;
+                    if (p.limit > 0.f) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            v[j] = clamp_hi(v[j], p.limit);
+                            u[j] = clamp_lo(clamp_hi(u[j], p.limit), -p.limit);
+                        }
+                    }
                 }
+                unary_act_all(p.act, v);
+                if constexpr (MATS == 2) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] *= u[j];
+                }
+                if (res) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += r[j];
+                }
+                T *o = out + (size_t)t0 * p.ldo;
+#pragma unroll
+                for (int j = 0; j < 16; ++j, o += p.ldo)
+                    if (t0 + j < rows) *o = from_f32<T>(v[j]);
             }
             tc::fence_before_sync();
             if (lane == 0) arrive_cluster(in_first(&acc_empty[n & 1]));
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();  // neither CTA ends while the other may still use its memory
     tc::fence_after_sync();
-    if (warp == 8) tmem_dealloc_pair(tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 // the driver's tensor-map encoder, resolved once; null if there is none
