@@ -47,7 +47,7 @@ constexpr int kM = 128;            // output columns per CTA
 constexpr int kPair = 2;           // CTAs per tile
 constexpr int kK = 64;             // inputs per stage: one 128-byte row of a swizzled tile
 constexpr int kTileA = kM * kK * 2;
-constexpr int kBoxRows = 64;       // rows of x per TMA box
+constexpr int kBoxRows = 64;       // rows of x per TMA box, or half as many for the last one
 constexpr int kStepRows = 32;      // rows per tile come in multiples of this
 constexpr int kMaxStages = 8;
 constexpr int kBand = 8;           // row tiles that share their pass over the weights
@@ -66,6 +66,7 @@ struct Tiling {
     int stages;
     int stage_bytes;
     int mblocks;    // blocks of kPair * kM output columns
+    int bufs;       // accumulator sets in tensor memory, 1 or 2
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -174,6 +175,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// rows that the boxes of `half` rows of x cover
+__host__ __device__ __forceinline__ int box_rows(int half) {
+    return (half + kBoxRows / 2 - 1) / (kBoxRows / 2) * (kBoxRows / 2);
+}
+
 // A group of c rows in equal tiles of at most tcap rows: rows per tile
 __host__ __device__ __forceinline__ int tile_rows(int c, int tcap) {
     const int nt = (c + tcap - 1) / tcap;
@@ -227,8 +233,8 @@ struct Walk {
 template <typename T, int MATS>
 __global__ void __launch_bounds__(kThreads, 1)
     product_gemm_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling g,
-                        const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
-                        const __grid_constant__ CUtensorMap tmu) {
+                        const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmx_half,
+                        const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmu) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     // full and acc_empty are used in the first CTA only, for both
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
@@ -254,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&drain, 1);
         ptx::mbar_fence_init();
         ptx::prefetch_tensormap(&tmx);
+        ptx::prefetch_tensormap(&tmx_half);
         ptx::prefetch_tensormap(&tmw);
         if (MATS == 2) ptx::prefetch_tensormap(&tmu);
     }
@@ -309,19 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- loads ------------------------------------------------------------
         const bool gather = p.row_token != nullptr;
         // one thread issues its copies one after the other, and that is what limits
-        // a loader: each warp has one box per step (0: w, 1: x, 2: w_up or x's second
-        // box), or with row_token every fourth copy of four rows beside it
+        // a loader: each warp has one box per step (0: w, 1 and 3: x, 2: w_up), or
+        // with row_token every fourth copy of four rows beside it
         int s = 0, fills = 0;
         uint32_t ph = 1;  // a fresh barrier passes the wait for its previous phase
         Item it;
-        bool ok = gather || warp < 3;
+        bool ok = true;
         for (int i = item0; ok && walk.get(i, it); i += item_step) {
             const int half = it.T / kPair;  // rows of x that this CTA loads
             const int r0 = it.r0 + rank * half;
-            const int boxes = (half + kBoxRows - 1) / kBoxRows;
-            const uint32_t bytes = kPair * (MATS * kTileA + (gather ? half : boxes * kBoxRows) * 128);
+            const uint32_t bytes = kPair * (MATS * kTileA + (gather ? half : box_rows(half)) * 128);
             const int col = (it.m * kPair + rank) * kM;
-            const int box = warp == 1 ? 0 : MATS == 1 && warp == 2 ? 1 : boxes;  // of x, without row_token
+            // without row_token: the first row and the size of this warp's box of x
+            const int x0 = warp == 1 ? 0 : kBoxRows;
+            const int xn = gather || !(warp & 1) || x0 >= half ? 0 : half - x0 > kBoxRows / 2 ? kBoxRows : kBoxRows / 2;
             const int fours = gather ? (half / 4 - warp + kLoaders - 1) / kLoaders : 0;
             int rows[4] = {};  // gather: lane j's rows are the warp's j-th copy
             if (lane < fours) {
@@ -341,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_3d(st, &tmw, k * kK, col, it.e, bar);
                     }
                     if (MATS == 2 && warp == 2) tma_3d(st + kTileA, &tmu, k * kK, col, it.e, bar);
-                    if (!gather && box < boxes)
-                        tma_2d(xb + box * kBoxRows * 128, &tmx, k * kK, r0 + box * kBoxRows, bar);
+                    if (xn) tma_2d(xb + x0 * 128, xn == kBoxRows ? &tmx : &tmx_half, k * kK, r0 + x0, bar);
                 }
                 if (lane < fours) tma_gather4(xb + (warp + kLoaders * lane) * 512, &tmx, k * kK, rows, bar);
                 __syncwarp();
@@ -374,9 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                             : tc::idesc_f16_f32(kPair * kM, 0);
             for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
                 const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
-                const uint32_t acc = tmem + (uint32_t)((n & 1) * MATS * g.tcap);
-                // the epilogues of the tile before last have read this accumulator set
-                if (!(ok = wait(&acc_empty[n & 1], (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag))) break;
+                const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
+                const uint32_t acc = tmem + (uint32_t)(buf * MATS * g.tcap);
+                // the epilogues have read what this accumulator set held
+                if (!(ok = wait(&acc_empty[buf], (uint32_t)((use & 1) ^ 1), abort_flag))) break;
                 tc::fence_after_sync();
                 for (int k = 0; k < nk; ++k) {
                     if (!(ok = wait(&full[s], ph, abort_flag))) break;
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ph ^= 1;
                     }
                 }
-                if (ok) commit_pair(&acc_full[n & 1]);
+                if (ok) commit_pair(&acc_full[buf]);
             }
             if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
                 commit_pair(&drain);
@@ -423,25 +431,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const T *res = static_cast<const T *>(p.residual);
             if (res) res += (size_t)it.r0 * p.ldr + c;
             T *out = static_cast<T *>(p.out) + (size_t)it.r0 * p.ldo + c;
-            float r[16], rn[16];
-            // a residual is read one chunk ahead, the first before the tile is done
-            auto load_res = [&](float (&d)[16], int t0) {
+            // a residual is read two chunks ahead, the first two before the tile is
+            // done; the values stay as loaded until they are used, so that nothing waits
+            // for them earlier
+            T ra[16], rb[16];
+            auto load_res = [&](T (&d)[16], int t0) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) d[j] = t0 + j < rows ? to_f32(res[(size_t)(t0 + j) * p.ldr]) : 0.f;
+                for (int j = 0; j < 16; ++j)
+                    if (t0 + j < rows) d[j] = res[(size_t)(t0 + j) * p.ldr];
             };
-            if (res) load_res(rn, 16 * part);
-            if (!__all_sync(0xffffffffu, wait(&acc_full[n & 1], (uint32_t)((n >> 1) & 1), abort_flag))) break;
+            if (res) {
+                load_res(ra, 16 * part);
+                load_res(rb, 16 * part + 32);
+            }
+            const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
+            if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)(use & 1), abort_flag))) break;
             tc::fence_after_sync();
-            const uint32_t acc = tlane + (uint32_t)((n & 1) * MATS * g.tcap);
-            for (int t0 = 16 * part; t0 < it.rows; t0 += 32) {
+            const uint32_t acc = tlane + (uint32_t)(buf * MATS * g.tcap);
+            auto chunk = [&](int t0, T (&r)[16]) {
                 float v[16], u[MATS == 2 ? 16 : 1];
                 tmem_ld16(acc + t0, v);
                 if constexpr (MATS == 2) tmem_ld16(acc + g.tcap + t0, u);
-                if (res) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = rn[j];
-                    load_res(rn, t0 + 32);
-                }
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += b0;
@@ -463,15 +473,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (res) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] += r[j];
+                    for (int j = 0; j < 16; ++j) v[j] += to_f32(r[j]);  // unset past the end: not stored
+                    load_res(r, t0 + 64);
                 }
                 T *o = out + (size_t)t0 * p.ldo;
 #pragma unroll
                 for (int j = 0; j < 16; ++j, o += p.ldo)
                     if (t0 + j < rows) *o = from_f32<T>(v[j]);
+            };
+#pragma unroll 1
+            for (int t0 = 16 * part; t0 < it.rows; t0 += 64) {
+                chunk(t0, ra);
+                if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
             }
             tc::fence_before_sync();
-            if (lane == 0) arrive_cluster(in_first(&acc_empty[n & 1]));
+            if (lane == 0) arrive_cluster(in_first(&acc_empty[buf]));
         }
     }
     tc::fence_before_sync();
@@ -523,19 +539,21 @@ struct Device {
 constexpr int kMaxDevices = 64;
 Device g_devices[kMaxDevices];
 
-// Rows per tile: the least time of a simple model, waves of tiles on the pairs,
-// each nk steps of the longer of the MMAs (2 rows a cycle per 64 inputs and
-// matrix) and the loads (about 50 bytes a cycle from L2 per SM), plus 2000 cycles
-// for the fill of the ring and the last epilogue.
+// Rows per tile: the least time of a simple model. Waves of tiles on the pairs, each
+// nk steps of the longer of the MMAs (2 cycles per row and matrix and 64 inputs)
+// and the loads (64 bytes a cycle from L2 into an SM), 2000 cycles for the fill of
+// the ring and the last epilogue, and 12 cycles per row of a tile whose epilogue
+// cannot run beside the next tile's MMAs (one accumulator set).
 int pick_rows(int mats, int mblocks, int groups, int mean, int nk, int pairs) {
     int best = kStepRows;
     long long least = -1;
-    for (int cap = mats == 2 ? 128 : 256; cap >= kStepRows; cap -= kStepRows) {
+    for (int cap = 256; cap >= kStepRows; cap -= kStepRows) {
         const int t = tile_rows(mean, cap);
         const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
         const long long waves = (items + pairs - 1) / pairs;
-        const int mma = 2 * mats * t, loads = (mats * kTileA + t / kPair * 128) / 50;
-        const long long cost = waves * ((long long)nk * (mma > loads ? mma : loads) + 2000);
+        const int mma = 2 * mats * t, loads = (mats * kTileA + box_rows(t / kPair) * 128) / 64;
+        const long long cost = waves * ((long long)nk * (mma > loads ? mma : loads) +
+                                        (2 * mats * cap > kTmemCols ? 12 * t : 0)) + 2000;
         if (least < 0 || cost < least) {
             least = cost;
             best = cap;
@@ -580,7 +598,7 @@ cudaError_t look_up(int dev, Device &d) {
 
 template <typename T, int MATS>
 cudaError_t launch(const Product &p, const Tiling &g, int pairs, int smem, Device &d, const CUtensorMap &tmx,
-                   const CUtensorMap &tmw, const CUtensorMap &tmu, cudaStream_t st) {
+                   const CUtensorMap &tmx_half, const CUtensorMap &tmw, const CUtensorMap &tmu, cudaStream_t st) {
     auto k = product_gemm_kernel<T, MATS>;
     const unsigned bit = 1u << (MATS - 1 + (p.dtype == MOE_DTYPE_BF16 ? 2 : 0));
     if (!(d.ready.load(std::memory_order_acquire) & bit)) {
@@ -591,7 +609,7 @@ cudaError_t launch(const Product &p, const Tiling &g, int pairs, int smem, Devic
     }
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pair_launch(attr, pairs, smem, st);
-    return cudaLaunchKernelEx(&cfg, k, p, g, tmx, tmw, tmu);
+    return cudaLaunchKernelEx(&cfg, k, p, g, tmx, tmx_half, tmw, tmu);
 }
 
 }  // namespace
@@ -609,7 +627,8 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
     Tiling g;
     g.tcap = pick_rows(mats, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kK - 1) / kK, all);
-    g.stage_bytes = mats * kTileA + (g.tcap / kPair + kBoxRows - 1) / kBoxRows * kBoxRows * 128;
+    g.stage_bytes = mats * kTileA + box_rows(g.tcap / kPair) * 128;
+    g.bufs = 2 * mats * g.tcap <= kTmemCols ? 2 : 1;
     g.mblocks = mblocks;
     const int table = p.offsets ? p.E * 4 : 0;
     const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table;
@@ -618,8 +637,9 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     const int smem = 1024 + g.stages * g.stage_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     if (most > 0x7fffffffLL) return cudaErrorNotSupported;
-    alignas(64) CUtensorMap tmx, tmw, tmu;
+    alignas(64) CUtensorMap tmx, tmx_half, tmw, tmu;
     if (!encode(&tmx, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||
+        !encode(&tmx_half, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, kBoxRows / 2) ||
         !encode(&tmw, p.dtype, p.w, p.K, p.N, p.ldw, p.E, p.E > 1 ? p.stride_e : p.ldw * p.N, kM))
         return cudaErrorNotSupported;
     tmu = tmw;
@@ -627,10 +647,10 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
         return cudaErrorNotSupported;
     const int n = (int)min(most, (long long)all);
     if (p.dtype == MOE_DTYPE_BF16)
-        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, n, smem, d, tmx, tmw, tmu, st)
-                         : launch<__nv_bfloat16, 1>(p, g, n, smem, d, tmx, tmw, tmu, st);
-    return mats == 2 ? launch<__half, 2>(p, g, n, smem, d, tmx, tmw, tmu, st)
-                     : launch<__half, 1>(p, g, n, smem, d, tmx, tmw, tmu, st);
+        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
+                         : launch<__nv_bfloat16, 1>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
+    return mats == 2 ? launch<__half, 2>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
+                     : launch<__half, 1>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
 }
 
 cudaError_t read_ops_status(unsigned *value, cudaStream_t st) {
