@@ -18,6 +18,8 @@
 // read and write 2 MB, which 8 SMs do in the time of the steps around it.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "ops_common.cuh"
 
 namespace moe {
@@ -201,8 +203,19 @@ cudaError_t launch_group_slots(const int *topk_idx, int n, int top_k, int E, int
     const long long S = (long long)n * top_k;
     const int ctas = S <= 4 * kThreads ? 1 : 8;
     const int smem = (kWarps + 1) * E * 4;
-    cudaError_t err = cudaFuncSetAttribute(group_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
+    if (smem > 32 << 10) {  // above what a kernel may ask for by itself: raise the limit, once per device
+        static std::atomic<unsigned long long> raised{0};
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (!(raised.load(std::memory_order_acquire) & bit) || !bit) {
+            err = cudaFuncSetAttribute(group_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kWarps + 1) * kThreads * 4);
+            if (err != cudaSuccess) return err;
+            raised.fetch_or(bit, std::memory_order_release);
+        }
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);

@@ -27,28 +27,33 @@ class moe_product(ctypes.Structure):
                 ("activation", ctypes.c_int), ("act_limit", ctypes.c_float)]
 
 
-_fns = None
+torch = None  # bound by _bind: importing the package does not import torch
+_c = None     # the operators' C functions
+
+
+def _bind():
+    """Bind torch and the C functions (first use; raises if the library is not built)."""
+    global torch, _c
+    L = _abi.lib()
+    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+    L.moe_linear.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp]
+    L.moe_grouped_linear.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i64, vp]
+    L.moe_group_slots.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.moe_combine_slots.argtypes = [i32, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp]
+    L.moe_ops_check.argtypes = [vp]
+    for name in OPS_EXPORTED:
+        getattr(L, name).restype = i32
+    import torch as t
+    torch = t
+    _c = L
+    return L
 
 
 def _lib():
-    """The operators' C functions with their argument types."""
-    global _fns
-    if _fns is None:
-        L = _abi.lib()
-        vp, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
-        L.moe_linear.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp]
-        L.moe_grouped_linear.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i64, vp]
-        L.moe_group_slots.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
-        L.moe_combine_slots.argtypes = [i32, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp]
-        L.moe_ops_check.argtypes = [vp]
-        for name in OPS_EXPORTED:
-            getattr(L, name).restype = i32
-        _fns = L
-    return _fns
+    return _c or _bind()
 
 
 def _dtype_code(dtype) -> int:
-    import torch
     if dtype == torch.bfloat16:
         return _abi.MOE_DTYPE_BF16
     if dtype == torch.float16:
@@ -56,49 +61,47 @@ def _dtype_code(dtype) -> int:
     raise TypeError(f"{dtype} is not supported: bfloat16 or float16")
 
 
-def _rows(t, what: str, cols: int, dtype, device, n: Optional[int] = None) -> int:
-    """Check a [n, cols] tensor whose columns are adjacent; the distance of its rows."""
-    if t.dim() != 2 or t.shape[1] != cols or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not [{'n' if n is None else n}, {cols}]")
-    if t.dtype != dtype:
+def _rows(t, what: str, cols: int, dtype, device, n: int = -1) -> int:
+    """Check a [n, cols] tensor (any n: -1) whose columns are adjacent; the distance
+    of its rows. A call spends about as long here as on the GPU for a few tokens,
+    so that each property is asked for once."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (n >= 0 and shape[0] != n):
+        raise ValueError(f"{what} has shape {tuple(shape)}, not [{'n' if n < 0 else n}, {cols}]")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} is {t.dtype}, not {dtype}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
-    if cols > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if col != 1 and cols > 1:
         raise ValueError(f"{what}: the columns of a row have to be adjacent")
-    return t.stride(0) if t.shape[0] > 1 else cols
+    return row if shape[0] > 1 else cols
 
 
 def _ints(t, what: str, shape, device):
-    import torch
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{what} is {t.dtype}, not int32")
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} has to be contiguous and on {device}")
 
 
-class _Launch:
-    """The device and stream of a call: kernels go to `stream`, or to the current
-    stream of the tensors' device, and outputs are allocated for that stream."""
+class _Elsewhere:
+    """The device and stream of a call that names a stream or whose tensors are not
+    on the current device: outputs are allocated there, kernels go there."""
 
     def __init__(self, device, stream):
-        import torch
-        self._on_device = self._on_stream = None
         if device.type != "cuda":
             raise ValueError(f"tensors have to be on a CUDA device, not on {device}")
-        if torch.cuda.current_device() != device.index:
-            self._on_device = torch.cuda.device(device)
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-            self._on_stream = torch.cuda.stream(s)
         self._device = device
+        self._on_device = torch.cuda.device(device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        self._on_stream = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        import torch
-        if self._on_device is not None:
-            self._on_device.__enter__()
+        self._on_device.__enter__()
         if self._on_stream is not None:
             self._on_stream.__enter__()
         return torch.cuda.current_stream(self._device).cuda_stream
@@ -106,8 +109,12 @@ class _Launch:
     def __exit__(self, *exc):
         if self._on_stream is not None:
             self._on_stream.__exit__(*exc)
-        if self._on_device is not None:
-            self._on_device.__exit__(*exc)
+        self._on_device.__exit__(*exc)
+
+
+def _here(device, stream) -> bool:
+    """Whether a call needs neither another device nor another stream."""
+    return stream is None and device.type == "cuda" and torch._C._cuda_getDevice() == device.index
 
 
 class LinearWeights:
@@ -123,6 +130,7 @@ class LinearWeights:
     The tensors are referenced, not copied."""
 
     def __init__(self, w, w_up=None, bias=None, bias_up=None, activation: str = "none", act_limit: float = 0.0):
+        _lib()
         if w.dim() not in (2, 3):
             raise ValueError(f"w has {w.dim()} dimensions, not 2 or 3")
         if activation not in ACTIVATIONS:
@@ -162,28 +170,41 @@ class SlotGroups(NamedTuple):
 
 
 def _no_grad(x):
-    import torch
     if x.requires_grad and torch.is_grad_enabled():
         raise RuntimeError("x requires a gradient: the operators record none (use torch.no_grad())")
 
 
+def _raise(status: int, what: str):
+    raise _abi.MoeError(status, what)
+
+
 def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     """out [n, N] = epilogue(x [n, K]) (+ residual [n, N]); `out` may be `residual`."""
-    import torch
     if weights.grouped:
         raise ValueError("moe_linear takes weights [N, K]; use moe_grouped_linear")
     _no_grad(x)
-    dt, dev, n, N = weights.dtype, weights.device, x.shape[0], weights.N
+    dt, dev, N = weights.dtype, weights.device, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
-    ldr = _rows(residual, "residual", N, dt, dev, n) if residual is not None else 0
-    ldo = _rows(out, "out", N, dt, dev, n) if out is not None else N
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty((n, N), dtype=dt, device=dev)
-        if n:
-            _abi._check(_lib().moe_linear(weights.ref, x.data_ptr(), ldx, n,
-                                          None if residual is None else residual.data_ptr(), ldr,
-                                          out.data_ptr(), ldo, st), "moe_linear")
+    n = x.shape[0]
+    ldr = ldo = N
+    if residual is not None:
+        ldr = _rows(residual, "residual", N, dt, dev, n)
+    if out is not None:
+        ldo = _rows(out, "out", N, dt, dev, n)
+    if _here(dev, stream):
+        return _linear(x, ldx, n, weights, residual, ldr, out, ldo, torch._C._cuda_getCurrentRawStream(dev.index))
+    with _Elsewhere(dev, stream) as st:
+        return _linear(x, ldx, n, weights, residual, ldr, out, ldo, st)
+
+
+def _linear(x, ldx, n, weights, residual, ldr, out, ldo, st):
+    if out is None:
+        out = torch.empty((n, weights.N), dtype=weights.dtype, device=weights.device)
+    if n:
+        status = _c.moe_linear(weights.ref, x.data_ptr(), ldx, n, None if residual is None else residual.data_ptr(),
+                               ldr, out.data_ptr(), ldo, st)
+        if status:
+            _raise(status, "moe_linear")
     return out
 
 
@@ -191,27 +212,35 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     """out [rows, N]: row r of group e (offsets[e] <= r < offsets[e+1]) through
     expert e's matrix. x is [rows, K], or [tokens, K] with row_token [rows]. Rows
     outside every group are left as they were (unset in an `out` made here)."""
-    import torch
     if not weights.grouped:
         raise ValueError("moe_grouped_linear takes weights [E, N, K]; use moe_linear")
     _no_grad(x)
     dt, dev, N = weights.dtype, weights.device, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
-    rows = x.shape[0] if row_token is None else row_token.numel()
+    rows = x.shape[0]
     if row_token is not None:
+        tokens, rows = rows, row_token.numel()
         _ints(row_token, "row_token", (rows,), dev)
-        if rows and not x.shape[0]:
+        if rows and not tokens:
             raise ValueError("x has no rows to take")
     _ints(offsets, "offsets", (weights.E + 1,), dev)
-    ldo = _rows(out, "out", N, dt, dev, rows) if out is not None else N
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty((rows, N), dtype=dt, device=dev)
-        if rows:
-            _abi._check(_lib().moe_grouped_linear(weights.ref, offsets.data_ptr(),
-                                                  None if row_token is None else row_token.data_ptr(),
-                                                  x.data_ptr(), ldx, x.shape[0], rows, out.data_ptr(), ldo, st),
-                        "moe_grouped_linear")
+    ldo = N if out is None else _rows(out, "out", N, dt, dev, rows)
+    if _here(dev, stream):
+        return _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo,
+                        torch._C._cuda_getCurrentRawStream(dev.index))
+    with _Elsewhere(dev, stream) as st:
+        return _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo, st)
+
+
+def _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo, st):
+    if out is None:
+        out = torch.empty((rows, weights.N), dtype=weights.dtype, device=weights.device)
+    if rows:
+        status = _c.moe_grouped_linear(weights.ref, offsets.data_ptr(),
+                                       None if row_token is None else row_token.data_ptr(), x.data_ptr(), ldx,
+                                       x.shape[0], rows, out.data_ptr(), ldo, st)
+        if status:
+            _raise(status, "moe_grouped_linear")
     return out
 
 
@@ -219,52 +248,74 @@ def moe_group_slots(topk_idx, E: int, experts: Optional[Tuple[int, int]] = None,
     """Group the slots of topk_idx [n, top_k] (int32) by expert. experts: (begin,
     end) of the ids that take part, all of them by default; other ids (another
     shard's, -1 for a dropped slot) belong to no group."""
-    import torch
-    if topk_idx.dim() != 2:
-        raise ValueError(f"topk_idx has shape {tuple(topk_idx.shape)}, not [n, top_k]")
-    n, k = topk_idx.shape
-    dev = topk_idx.device
-    _ints(topk_idx, "topk_idx", (n, k), dev)
+    _lib()
+    shape, dev = topk_idx.shape, topk_idx.device
+    if len(shape) != 2:
+        raise ValueError(f"topk_idx has shape {tuple(shape)}, not [n, top_k]")
+    _ints(topk_idx, "topk_idx", shape, dev)
+    if _here(dev, stream):
+        return _slots(topk_idx, shape, E, experts, dev, torch._C._cuda_getCurrentRawStream(dev.index))
+    with _Elsewhere(dev, stream) as st:
+        return _slots(topk_idx, shape, E, experts, dev, st)
+
+
+def _slots(topk_idx, shape, E, experts, dev, st):
+    n, k = shape
     lo, hi = (0, E) if experts is None else experts
-    with _Launch(dev, stream) as st:
-        S = n * k
-        buf = torch.empty(3 * S + E + 1, dtype=torch.int32, device=dev)
-        # views of one allocation: offsets last, the three slot arrays in front
-        token, rank, of, offsets = buf.split((S, S, S, E + 1))
-        p = buf.data_ptr()
-        # an empty tensor has no address: nothing of it is read
-        _abi._check(_lib().moe_group_slots(topk_idx.data_ptr() or p, n, k, E, lo, hi, p + 12 * S, p, p + 4 * S,
-                                           p + 8 * S, st), "moe_group_slots")
-    return SlotGroups(offsets, token, rank, of.view(n, k))
+    int32 = torch.int32
+    # four allocations: views of one cost more time
+    offsets = torch.empty(max(E, 0) + 1, dtype=int32, device=dev)
+    token = torch.empty(n * k, dtype=int32, device=dev)
+    rank = torch.empty(n * k, dtype=int32, device=dev)
+    of = torch.empty(shape, dtype=int32, device=dev)
+    p = offsets.data_ptr()  # stands in for empty tensors, which have no address: nothing of them is used
+    status = _c.moe_group_slots(topk_idx.data_ptr() or p, n, k, E, lo, hi, p, token.data_ptr() or p,
+                                rank.data_ptr() or p, of.data_ptr() or p, st)
+    if status:
+        _raise(status, "moe_group_slots")
+    return SlotGroups(offsets, token, rank, of)
 
 
 def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
     """out [n, N] = sum_j topk_w[t, j] * y[slot_of[t, j]] (+ residual): y [rows, N],
     slot_of [n, top_k] int32 (a slot outside y's rows adds nothing), topk_w
     [n, top_k] float32; `out` may be `residual`."""
-    import torch
+    _lib()
     _no_grad(y)
     dt, dev = y.dtype, y.device
     code = _dtype_code(dt)
-    if y.dim() != 2 or slot_of.dim() != 2:
+    shape, ys = slot_of.shape, y.shape
+    if len(shape) != 2 or len(ys) != 2:
         raise ValueError("y has to be [rows, N] and slot_of [n, top_k]")
-    rows, N = y.shape
-    n, k = slot_of.shape
+    n, N = shape[0], ys[1]
     ldy = _rows(y, "y", N, dt, dev)
-    _ints(slot_of, "slot_of", (n, k), dev)
-    if topk_w.shape != slot_of.shape or topk_w.dtype != torch.float32 or topk_w.device != dev \
+    _ints(slot_of, "slot_of", shape, dev)
+    if topk_w.shape != shape or topk_w.dtype is not torch.float32 or topk_w.device != dev \
             or not topk_w.is_contiguous():
-        raise ValueError(f"topk_w has to be contiguous float32 {tuple(slot_of.shape)} on {dev}")
-    ldr = _rows(residual, "residual", N, dt, dev, n) if residual is not None else 0
-    ldo = _rows(out, "out", N, dt, dev, n) if out is not None else N
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty((n, N), dtype=dt, device=dev)
-        if n:
-            _abi._check(_lib().moe_combine_slots(code, y.data_ptr() or None, ldy, rows, slot_of.data_ptr(),
-                                                 topk_w.data_ptr(), n, k, N,
-                                                 None if residual is None else residual.data_ptr(), ldr,
-                                                 out.data_ptr(), ldo, st), "moe_combine_slots")
+        raise ValueError(f"topk_w has to be contiguous float32 {tuple(shape)} on {dev}")
+    ldr = ldo = N
+    if residual is not None:
+        ldr = _rows(residual, "residual", N, dt, dev, n)
+    if out is not None:
+        ldo = _rows(out, "out", N, dt, dev, n)
+    if _here(dev, stream):
+        return _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo,
+                        torch._C._cuda_getCurrentRawStream(dev.index))
+    with _Elsewhere(dev, stream) as st:
+        return _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st)
+
+
+def _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st):
+    n, k = slot_of.shape
+    rows, N = y.shape
+    if out is None:
+        out = torch.empty((n, N), dtype=y.dtype, device=y.device)
+    if n:
+        status = _c.moe_combine_slots(code, y.data_ptr() or None, ldy, rows, slot_of.data_ptr(), topk_w.data_ptr(), n,
+                                      k, N, None if residual is None else residual.data_ptr(), ldr, out.data_ptr(),
+                                      ldo, st)
+        if status:
+            _raise(status, "moe_combine_slots")
     return out
 
 
