@@ -56,6 +56,7 @@ constexpr int kEpilogue = 8;       // epilogue warps, two per quadrant of the te
 constexpr int kMmaWarp = kLoaders + kEpilogue;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kTmemCols = 512;
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // see tc::smem_desc_sw128
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 // [0]: set when a wait gave up, until moe_ops_check reads it
@@ -87,18 +88,32 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // the cluster address of this CTA's barrier `bar` in the pair's first CTA
-__device__ __forceinline__ uint32_t in_first(const void *bar) {
+__device__ __forceinline__ uint32_t in_first(uint32_t bar) {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(bar)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(bar));
     return a;
 }
 
-// wait for an mbarrier phase; false once any role of the CTA gave up
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+// Barriers and ring stages are held as shared-memory addresses: the loops below
+// are bound by their instruction count.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// wait for an mbarrier phase that a first try did not find complete; false once any
+// role of the CTA gave up
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     const unsigned long long t0 = globaltimer();
     for (;;) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer() - t0 > kWaitNs) {
             *abort_flag = 1;
@@ -108,48 +123,86 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     }
 }
 
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return try_wait(bar, parity) || wait_more(bar, parity, abort_flag);
+}
+
+// the same once the kernel is done with its work: no flag, no report
+__device__ __noinline__ void settle(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer();
+    while (!try_wait(bar, parity) && globaltimer() - t0 < kWaitNs) {
+    }
+}
+
+// the position of a role in the ring of stages
+struct Ring {
+    uint32_t stage, empty, full;  // addresses of the current stage and its barriers
+    uint32_t s, phase;
+    __device__ __forceinline__ void next(uint32_t stages, uint32_t stage_bytes) {
+        stage += stage_bytes;
+        empty += 8;
+        full += 8;
+        if (++s == stages) {
+            stage -= stages * stage_bytes;
+            empty -= stages * 8;
+            full -= stages * 8;
+            s = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // TMA loads into this CTA's shared memory, counted by a barrier of the pair's
 // first CTA (a cluster address)
-__device__ __forceinline__ void tma_2d(void *dst, const void *map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_2d(uint32_t dst, const void *map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-        "%3}], [%4];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+        "%3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_3d(void *dst, const void *map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_3d(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-        "%3, %4}], [%5];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "%3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 // four rows of a map whose box is one row high
-__device__ __forceinline__ void tma_gather4(void *dst, const void *map, int x, const int (&r)[4], uint32_t bar) {
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *map, int x, const int (&r)[4], uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]),
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(map), "r"(x), "r"(r[0]), "r"(r[1]),
         "r"(r[2]), "r"(r[3]), "r"(bar)
         : "memory");
 }
 
 // D[tmem of both CTAs] (+)= A * B^T: each CTA's shared memory holds its 128 rows of A and
 // half of B's rows; issued by one thread of the first CTA
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// a and b are the low words of their descriptors, whose high words are all alike
+// (128-byte swizzle, 8-row atoms of 1024 bytes)
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "mov.b64 ad, {%1, %5};\n\t"
+        "mov.b64 bd, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], ad, bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
 // arrive on both CTAs' barriers once the MMAs issued before have completed
-__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            tc::smem_u32(bar)),
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
 }
@@ -309,72 +362,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();  // the peer's barriers are ready
     tc::fence_after_sync();
     const uint32_t tmem = tslot;
+    const uint32_t ring_addr = tc::smem_u32(ring), full_addr = tc::smem_u32(full), empty_addr = tc::smem_u32(empty);
+    const uint32_t acc_full_addr = tc::smem_u32(acc_full), acc_empty_addr = tc::smem_u32(acc_empty);
     const Walk walk{p, g, first, total};
     const int nk = (p.K + kK - 1) / kK;
 
     if (warp < kLoaders) {
         // ---- loads ------------------------------------------------------------
         const bool gather = p.row_token != nullptr;
-        // one thread issues its copies one after the other, and that is what limits
-        // a loader: each warp has one box per step (0: w, 1 and 3: x, 2: w_up), or
-        // with row_token every fourth copy of four rows beside it
-        int s = 0, fills = 0;
-        uint32_t ph = 1;  // a fresh barrier passes the wait for its previous phase
+        // One thread issues its copies one after the other, and that is what limits a
+        // loader: each warp has one box per step (0: w, 1 and 3: x, 2: w_up), or with
+        // row_token every fourth copy of four rows beside it. A warp without a box
+        // in some tile waits for its stages all the same: parities only tell
+        // neighbouring phases apart.
+        Ring at{ring_addr, empty_addr, in_first(full_addr), 0, 1};  // a fresh barrier passes the wait for phase 1
+        const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
         Item it;
-        bool ok = true;
+        bool ok = gather || MATS == 2 || warp != 2;
         for (int i = item0; ok && walk.get(i, it); i += item_step) {
             const int half = it.T / kPair;  // rows of x that this CTA loads
             const int r0 = it.r0 + rank * half;
             const uint32_t bytes = kPair * (MATS * kTileA + (gather ? half : box_rows(half)) * 128);
             const int col = (it.m * kPair + rank) * kM;
-            // without row_token: the first row and the size of this warp's box of x
-            const int x0 = warp == 1 ? 0 : kBoxRows;
-            const int xn = gather || !(warp & 1) || x0 >= half ? 0 : half - x0 > kBoxRows / 2 ? kBoxRows : kBoxRows / 2;
-            const int fours = gather ? (half / 4 - warp + kLoaders - 1) / kLoaders : 0;
-            int rows[4] = {};  // gather: lane j's rows are the warp's j-th copy
-            if (lane < fours) {
+            const int k_end = nk * kK;
+            if (gather) {
+                // lane j's rows are the warp's j-th copy; rows past the end repeat the last one
+                const int fours = (half / 4 - warp + kLoaders - 1) / kLoaders;
+                int rows[4] = {};
+                if (lane < fours) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)  // rows past the end repeat the last one
-                    rows[j] = input_row(p, min(r0 + 4 * (warp + kLoaders * lane) + j, it.r0 + it.rows - 1));
-            }
-            for (int k = 0; k < nk; ++k) {
-                ok = __all_sync(0xffffffffu, wait(&empty[s], ph, abort_flag));
-                if (!ok) break;
-                unsigned char *st = ring + s * g.stage_bytes;
-                unsigned char *xb = st + MATS * kTileA;
-                const uint32_t bar = in_first(&full[s]);
-                if (tc::elect_one()) {
-                    if (warp == 0) {
-                        if (rank == 0) tc::arrive_expect_tx(&full[s], bytes);
-                        tma_3d(st, &tmw, k * kK, col, it.e, bar);
-                    }
-                    if (MATS == 2 && warp == 2) tma_3d(st + kTileA, &tmu, k * kK, col, it.e, bar);
-                    if (xn) tma_2d(xb + x0 * 128, xn == kBoxRows ? &tmx : &tmx_half, k * kK, r0 + x0, bar);
+                    for (int j = 0; j < 4; ++j)
+                        rows[j] = input_row(p, min(r0 + 4 * (warp + kLoaders * lane) + j, it.r0 + it.rows - 1));
                 }
-                if (lane < fours) tma_gather4(xb + (warp + kLoaders * lane) * 512, &tmx, k * kK, rows, bar);
-                __syncwarp();
-                ++fills;
-                if (++s == g.stages) {
-                    s = 0;
-                    ph ^= 1;
+                const uint32_t dst = MATS * kTileA + (warp + kLoaders * lane) * 512;
+                const CUtensorMap *map = warp == 0 ? &tmw : &tmu;
+                const bool loads_w = warp == 0 || (MATS == 2 && warp == 2), counts = warp == 0 && rank == 0;
+#pragma unroll 1
+                for (int k = 0; k < k_end; k += kK) {
+                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                    if (loads_w && tc::elect_one()) {
+                        if (counts) expect_tx(full_addr + 8 * at.s, bytes);
+                        tma_3d(at.stage + (warp == 0 ? 0 : kTileA), map, k, col, it.e, at.full);
+                    }
+                    if (lane < fours) tma_gather4(at.stage + dst, &tmx, k, rows, at.full);
+                    at.next(stages, stage_bytes);
+                }
+            } else if (warp & 1) {
+                // the size of this warp's box of x, or 0
+                const int x0 = warp == 1 ? 0 : kBoxRows;
+                const int xn = x0 >= half ? 0 : half - x0 > kBoxRows / 2 ? kBoxRows : kBoxRows / 2;
+                const CUtensorMap *map = xn == kBoxRows ? &tmx : &tmx_half;
+                const uint32_t dst = MATS * kTileA + x0 * 128;
+#pragma unroll 1
+                for (int k = 0; k < k_end; k += kK) {
+                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                    if (xn && tc::elect_one()) tma_2d(at.stage + dst, map, k, r0 + x0, at.full);
+                    at.next(stages, stage_bytes);
+                }
+            } else {
+                const CUtensorMap *map = warp == 0 ? &tmw : &tmu;
+                const uint32_t dst = warp == 0 ? 0 : kTileA;
+                const bool counts = warp == 0 && rank == 0;
+#pragma unroll 1
+                for (int k = 0; k < k_end; k += kK) {
+                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                    if (tc::elect_one()) {
+                        if (counts) expect_tx(full_addr + 8 * at.s, bytes);
+                        tma_3d(at.stage + dst, map, k, col, it.e, at.full);
+                    }
+                    at.next(stages, stage_bytes);
                 }
             }
         }
-        // every copy has landed before the pair may end (they have, unless a wait gave up)
+        // every copy has landed before the pair may end (they have, unless a wait gave
+        // up): the stages before `at` were last filled in its lap, the others in the
+        // one before (a fresh barrier passes)
         if (warp == 0 && rank == 0)
-            for (int i = 0; i < min(fills, g.stages); ++i) {
-                const int f = fills - 1 - i;  // the fill with this number
-                const unsigned long long t0 = globaltimer();
-                while (!ptx::mbar_try_wait_hint(&full[f % g.stages], (uint32_t)((f / g.stages) & 1), 20000u) &&
-                       globaltimer() - t0 < kWaitNs) {
-                }
-            }
+            for (uint32_t i = 0; i < stages; ++i) settle(full_addr + 8 * i, i < at.s ? at.phase ^ 1 : at.phase);
         __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
         // ---- MMAs --------------------------------------------------------------
         if (tc::elect_one()) {
-            int s = 0, n = 0;
-            uint32_t ph = 0;
+            Ring at{ring_addr, empty_addr, full_addr, 0, 0};
+            const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
+            int n = 0;
             Item it;
             bool ok = true;
             const uint32_t base = p.dtype == MOE_DTYPE_BF16 ? tc::idesc_bf16_f32(kPair * kM, 0)
@@ -382,35 +453,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
                 const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
                 const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
-                const uint32_t acc = tmem + (uint32_t)(buf * MATS * g.tcap);
+                const uint32_t acc = tmem + (uint32_t)(buf * MATS * g.tcap), acc_up = acc + g.tcap;
                 // the epilogues have read what this accumulator set held
-                if (!(ok = wait(&acc_empty[buf], (uint32_t)((use & 1) ^ 1), abort_flag))) break;
+                if (!(ok = wait(acc_empty_addr + 8 * buf, (uint32_t)((use & 1) ^ 1), abort_flag))) break;
                 tc::fence_after_sync();
+                uint32_t add = 0;  // the first MMA of a tile overwrites
+#pragma unroll 1
                 for (int k = 0; k < nk; ++k) {
-                    if (!(ok = wait(&full[s], ph, abort_flag))) break;
+                    if (!(ok = wait(at.full, at.phase, abort_flag))) break;
                     tc::fence_after_sync();
-                    const uint32_t st = tc::smem_u32(ring + s * g.stage_bytes);
-                    const uint64_t bd = tc::smem_desc_sw128(st + MATS * kTileA, 1024);
+                    const uint32_t a = desc_low(at.stage), b = a + (MATS * kTileA >> 4);
 #pragma unroll
-                    for (int m = 0; m < MATS; ++m) {
-                        const uint64_t ad = tc::smem_desc_sw128(st + m * kTileA, 1024);
-#pragma unroll
-                        for (int q = 0; q < kK / 16; ++q)
-                            mma_pair(acc + (uint32_t)(m * g.tcap), ad + 2 * q, bd + 2 * q, idesc, (k | q) ? 1u : 0u);
+                    for (int q = 0; q < kK / 16; ++q) {
+                        mma_pair(acc, a + 2 * q, b + 2 * q, idesc, add);
+                        if (MATS == 2) mma_pair(acc_up, a + (kTileA >> 4) + 2 * q, b + 2 * q, idesc, add);
+                        add = 1;
                     }
-                    commit_pair(&empty[s]);
-                    if (++s == g.stages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                    commit_pair(at.empty);
+                    at.next(stages, stage_bytes);
                 }
-                if (ok) commit_pair(&acc_full[buf]);
+                if (ok) commit_pair(acc_full_addr + 8 * buf);
             }
             if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
-                commit_pair(&drain);
-                const unsigned long long t0 = globaltimer();
-                while (!ptx::mbar_try_wait_hint(&drain, 0, 20000u) && globaltimer() - t0 < kWaitNs) {
-                }
+                commit_pair(tc::smem_u32(&drain));
+                settle(tc::smem_u32(&drain), 0);
             }
         }
         __syncwarp();
@@ -445,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_res(rb, 16 * part + 32);
             }
             const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
-            if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)(use & 1), abort_flag))) break;
+            if (!__all_sync(0xffffffffu, wait(acc_full_addr + 8 * buf, (uint32_t)(use & 1), abort_flag))) break;
             tc::fence_after_sync();
             const uint32_t acc = tlane + (uint32_t)(buf * MATS * g.tcap);
             auto chunk = [&](int t0, T (&r)[16]) {
@@ -487,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
             }
             tc::fence_before_sync();
-            if (lane == 0) arrive_cluster(in_first(&acc_empty[buf]));
+            if (lane == 0) arrive_cluster(in_first(acc_empty_addr + 8 * buf));
         }
     }
     tc::fence_before_sync();
