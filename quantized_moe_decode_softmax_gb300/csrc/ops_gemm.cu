@@ -370,15 +370,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kLoaders) {
         // ---- loads ------------------------------------------------------------
         const bool gather = p.row_token != nullptr;
-        // One thread issues its copies one after the other, and that is what limits a
-        // loader: each warp has one box per step (0: w, 1 and 3: x, 2: w_up), or with
-        // row_token every fourth copy of four rows beside it. A warp without a box
-        // in some tile waits for its stages all the same: parities only tell
-        // neighbouring phases apart.
+        // A step of a load loop is a chain of about 450 cycles (wait, elect, copy),
+        // whatever it copies, so the steps are dealt to two pairs of warps: warps 0 and 1
+        // take the even ones, 2 and 3 the odd ones; 0 and 2 load the weights, 1 and 3 the
+        // rows of x. With row_token every warp takes part in every step, with every
+        // fourth copy of four rows; warps 0 and 2 load the weights beside it.
+        // (A warp that skips steps stays less than two laps of the ring ahead of the
+        // MMAs all the same, by the waits of the steps that it takes, so that parities
+        // tell the phases of a barrier apart.)
         Ring at{ring_addr, empty_addr, in_first(full_addr), 0, 1};  // a fresh barrier passes the wait for phase 1
         const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
+        const bool odd = warp >= 2;
+        bool skip = odd && !gather;  // the next step belongs to the other pair
         Item it;
-        bool ok = gather || MATS == 2 || warp != 2;
+        bool ok = true;
         for (int i = item0; ok && walk.get(i, it); i += item_step) {
             const int half = it.T / kPair;  // rows of x that this CTA loads
             const int r0 = it.r0 + rank * half;
@@ -408,28 +413,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     at.next(stages, stage_bytes);
                 }
             } else if (warp & 1) {
-                // the size of this warp's box of x, or 0
-                const int x0 = warp == 1 ? 0 : kBoxRows;
-                const int xn = x0 >= half ? 0 : half - x0 > kBoxRows / 2 ? kBoxRows : kBoxRows / 2;
-                const CUtensorMap *map = xn == kBoxRows ? &tmx : &tmx_half;
-                const uint32_t dst = MATS * kTileA + x0 * 128;
+                // two boxes of x at most: the last one is half as high if that is enough
+                const int n1 = half > kBoxRows ? (half - kBoxRows > kBoxRows / 2 ? 2 : 1) : 0;
+                const CUtensorMap *map0 = half > kBoxRows / 2 ? &tmx : &tmx_half, *map1 = n1 == 2 ? &tmx : &tmx_half;
 #pragma unroll 1
                 for (int k = 0; k < k_end; k += kK) {
-                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
-                    if (xn && tc::elect_one()) tma_2d(at.stage + dst, map, k, r0 + x0, at.full);
+                    if (!skip) {
+                        if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                        if (tc::elect_one()) {
+                            tma_2d(at.stage + MATS * kTileA, map0, k, r0, at.full);
+                            if (n1)
+                                tma_2d(at.stage + MATS * kTileA + kBoxRows * 128, map1, k, r0 + kBoxRows, at.full);
+                        }
+                    }
+                    skip = !skip;
                     at.next(stages, stage_bytes);
                 }
             } else {
-                const CUtensorMap *map = warp == 0 ? &tmw : &tmu;
-                const uint32_t dst = warp == 0 ? 0 : kTileA;
-                const bool counts = warp == 0 && rank == 0;
 #pragma unroll 1
                 for (int k = 0; k < k_end; k += kK) {
-                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
-                    if (tc::elect_one()) {
-                        if (counts) expect_tx(full_addr + 8 * at.s, bytes);
-                        tma_3d(at.stage + dst, map, k, col, it.e, at.full);
+                    if (!skip) {
+                        if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                        if (tc::elect_one()) {
+                            if (rank == 0) expect_tx(full_addr + 8 * at.s, bytes);
+                            tma_3d(at.stage, &tmw, k, col, it.e, at.full);
+                            if (MATS == 2) tma_3d(at.stage + kTileA, &tmu, k, col, it.e, at.full);
+                        }
                     }
+                    skip = !skip;
                     at.next(stages, stage_bytes);
                 }
             }
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every copy has landed before the pair may end (they have, unless a wait gave
         // up): the stages before `at` were last filled in its lap, the others in the
         // one before (a fresh barrier passes)
-        if (warp == 0 && rank == 0)
+        if ((warp == 0 || warp == 2) && rank == 0)
             for (uint32_t i = 0; i < stages; ++i) settle(full_addr + 8 * i, i < at.s ? at.phase ^ 1 : at.phase);
         __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
@@ -457,17 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the epilogues have read what this accumulator set held
                 if (!(ok = wait(acc_empty_addr + 8 * buf, (uint32_t)((use & 1) ^ 1), abort_flag))) break;
                 tc::fence_after_sync();
-                uint32_t add = 0;  // the first MMA of a tile overwrites
 #pragma unroll 1
                 for (int k = 0; k < nk; ++k) {
                     if (!(ok = wait(at.full, at.phase, abort_flag))) break;
                     tc::fence_after_sync();
                     const uint32_t a = desc_low(at.stage), b = a + (MATS * kTileA >> 4);
+                    // the first MMA of a tile overwrites
+                    mma_pair(acc, a, b, idesc, k);
+                    if (MATS == 2) mma_pair(acc_up, a + (kTileA >> 4), b, idesc, k);
 #pragma unroll
-                    for (int q = 0; q < kK / 16; ++q) {
-                        mma_pair(acc, a + 2 * q, b + 2 * q, idesc, add);
-                        if (MATS == 2) mma_pair(acc_up, a + (kTileA >> 4) + 2 * q, b + 2 * q, idesc, add);
-                        add = 1;
+                    for (int q = 1; q < kK / 16; ++q) {
+                        mma_pair(acc, a + 2 * q, b + 2 * q, idesc, 1);
+                        if (MATS == 2) mma_pair(acc_up, a + (kTileA >> 4) + 2 * q, b + 2 * q, idesc, 1);
                     }
                     commit_pair(at.empty);
                     at.next(stages, stage_bytes);
@@ -605,12 +617,15 @@ struct Device {
 constexpr int kMaxDevices = 64;
 Device g_devices[kMaxDevices];
 
-// Rows per tile: the least time of a simple model. Waves of tiles on the pairs, each
-// nk steps of the longer of the MMAs (2 cycles per row and matrix and 64 inputs)
-// and the loads (64 bytes a cycle from L2 into an SM), 2000 cycles for the fill of
-// the ring and the last epilogue, and 12 cycles per row of a tile whose epilogue
-// cannot run beside the next tile's MMAs (one accumulator set).
-int pick_rows(int mats, int mblocks, int groups, int mean, int nk, int pairs) {
+// Rows per tile: the least time of a simple model, in cycles. Waves of tiles on the
+// pairs, each nk steps of the longest of the MMAs (2 per row and matrix and 64
+// inputs), the loads (64 bytes a cycle from L2 into an SM) and the issue of a step
+// (350); then the epilogue of the last tile, and a third of it for every tile where
+// it cannot run beside the next tile's MMAs (one accumulator set: 256 gated rows
+// measured 316 us on 8192 tokens, 128 experts, K = 2048, and 128 rows 382 us).
+int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int pairs) {
+    const int mats = p.w_up ? 2 : 1;
+    const int per_row = 20 + 15 * (mats - 1) + (p.act != MOE_EPI_NONE ? 15 : 0) + (p.residual ? 15 : 0);
     int best = kStepRows;
     long long least = -1;
     for (int cap = 256; cap >= kStepRows; cap -= kStepRows) {
@@ -618,8 +633,8 @@ int pick_rows(int mats, int mblocks, int groups, int mean, int nk, int pairs) {
         const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
         const long long waves = (items + pairs - 1) / pairs;
         const int mma = 2 * mats * t, loads = (mats * kTileA + box_rows(t / kPair) * 128) / 64;
-        const long long cost = waves * ((long long)nk * (mma > loads ? mma : loads) +
-                                        (2 * mats * cap > kTmemCols ? 12 * t : 0)) + 2000;
+        const long long step = max(350, max(mma, loads));
+        const long long cost = waves * nk * step + per_row * t + (2 * mats * cap > kTmemCols ? waves * per_row * t / 3 : 0);
         if (least < 0 || cost < least) {
             least = cost;
             best = cap;
@@ -692,7 +707,7 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     const int mblocks = (p.N + kPair * kM - 1) / (kPair * kM);
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
     Tiling g;
-    g.tcap = pick_rows(mats, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kK - 1) / kK, all);
+    g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kK - 1) / kK, all);
     g.stage_bytes = mats * kTileA + box_rows(g.tcap / kPair) * 128;
     g.bufs = 2 * mats * g.tcap <= kTmemCols ? 2 : 1;
     g.mblocks = mblocks;

@@ -5,7 +5,7 @@
 // Bound: the weights' bytes. With 1..32 rows a weight is used at most 32 times,
 // so the kernel is a stream over the weights and everything else has to stay
 // out of its way. A CTA owns 16 output columns of one expert; its 8 warps split
-// K in interleaved slices of 128 inputs, so a small matrix still keeps every SM
+// K in interleaved slices, so a small matrix still keeps every SM
 // loading (N = 2048: 128 CTAs). mma.sync m16n8k16 does the products: its A
 // operand is 16 weight rows and its B operand 8 rows of x, both straight from
 // 16-byte global loads. That works without shuffles because a sum over k may
@@ -13,6 +13,8 @@
 // inputs 8 t .. 8 t + 7 of a 32-input step from weight rows g and g + 8 and from
 // x row g, and feeds them to two MMAs four inputs at a time. The f32 partials of
 // the 8 warps are summed in warp order.
+#include <atomic>
+
 #include "ops_common.cuh"
 #include "ptx.cuh"
 
@@ -22,7 +24,6 @@ namespace {
 
 constexpr int kCols = 16;    // output columns of a CTA
 constexpr int kWarps = 8;
-constexpr int kSlice = 128;  // inputs of a warp's step: four 16-byte loads per weight row
 
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -55,9 +56,18 @@ __device__ __forceinline__ int nth_group(const Product &p, int g) {
     return -1;
 }
 
-// MATS 1 or 2 (gated) weight matrices, TB blocks of 8 rows at a time
-template <typename T, int MATS, int TB>
-__global__ void __launch_bounds__(32 * kWarps) product_rows_kernel(const Product p) {
+// MATS 1 or 2 (gated) weight matrices, TB blocks of 8 rows at a time. AHEAD: the
+// weights of the next slice are loaded while this one's are used, with registers
+// for two CTAs per SM. That is the faster way while the grid fits the SMs at two
+// CTAs each (4096x4096, one row: 5.8 against 9.0 us). A larger grid does better with
+// fewer registers, more CTAs per SM and an even end (128 experts, 8 in use, gated
+// 2048 -> 768: 12.0 against 14.5 us).
+constexpr int min_ctas(int mats, int tb, bool ahead) {
+    return ahead ? 2 : mats * tb == 1 ? 6 : mats * tb == 2 ? 4 : mats * tb == 4 ? 3 : 2;
+}
+
+template <typename T, int MATS, int TB, bool AHEAD>
+__global__ void __launch_bounds__(32 * kWarps, min_ctas(MATS, TB, AHEAD)) product_rows_kernel(const Product p) {
     __shared__ float part[kWarps][MATS][TB * 8][kCols + 1];
     __shared__ int s_e;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -98,14 +108,27 @@ __global__ void __launch_bounds__(32 * kWarps) product_rows_kernel(const Product
             for (int b = 0; b < TB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][b][i] = 0.f;
+        constexpr int kSlice = AHEAD ? 64 : 128;  // inputs of a warp's step
+        uint4 wn[MATS][kSlice / 32][2];
+        auto load_w = [&](int k0) {
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int s = 0; s < kSlice / 32; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) wn[m][s][h] = load8(wrow[m][h], k0 + 32 * s + 8 * t, p.K);
+        };
+        if (AHEAD) load_w(warp * kSlice);
         for (int k0 = warp * kSlice; k0 < p.K; k0 += kWarps * kSlice) {
+            if (!AHEAD) load_w(k0);
             uint4 wv[MATS][kSlice / 32][2];
 #pragma unroll
             for (int m = 0; m < MATS; ++m)
 #pragma unroll
                 for (int s = 0; s < kSlice / 32; ++s)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) wv[m][s][h] = load8(wrow[m][h], k0 + 32 * s + 8 * t, p.K);
+                    for (int h = 0; h < 2; ++h) wv[m][s][h] = wn[m][s][h];
+            if (AHEAD) load_w(k0 + kWarps * kSlice);
 #pragma unroll
             for (int s = 0; s < kSlice / 32; ++s) {
 #pragma unroll
@@ -150,20 +173,40 @@ __global__ void __launch_bounds__(32 * kWarps) product_rows_kernel(const Product
     }
 }
 
+// SMs of the current device, looked up once per device
+cudaError_t sm_count(int &sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms > 0) return cudaSuccess;
+    if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 template <typename T, int MATS, int TB>
-cudaError_t launch(const Product &p, cudaStream_t st) {
+cudaError_t launch(const Product &p, int sms, cudaStream_t st) {
     const dim3 grid((p.N + kCols - 1) / kCols, p.offsets ? min(p.E, p.rows) : 1);
-    product_rows_kernel<T, MATS, TB><<<grid, 32 * kWarps, 0, st>>>(p);
+    if ((long long)grid.x * grid.y <= 2 * sms)
+        product_rows_kernel<T, MATS, TB, true><<<grid, 32 * kWarps, 0, st>>>(p);
+    else
+        product_rows_kernel<T, MATS, TB, false><<<grid, 32 * kWarps, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int MATS>
 cudaError_t pick(const Product &p, cudaStream_t st) {
+    int sms = 0;
+    const cudaError_t err = sm_count(sms);
+    if (err != cudaSuccess) return err;
     // rows of a typical group
-    const int mean = p.offsets ? (p.rows + p.E - 1) / p.E : p.rows;
-    if (mean <= 8) return launch<T, MATS, 1>(p, st);
-    if (mean <= 16) return launch<T, MATS, 2>(p, st);
-    return launch<T, MATS, 4>(p, st);
+    const int groups = p.offsets ? min(p.E, p.rows) : 1;
+    const int mean = (p.rows + groups - 1) / groups;
+    if (mean <= 8) return launch<T, MATS, 1>(p, sms, st);
+    if (mean <= 16) return launch<T, MATS, 2>(p, sms, st);
+    return launch<T, MATS, 4>(p, sms, st);
 }
 
 }  // namespace

@@ -29,6 +29,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kCombineThreads = 128;
 
 // slots [first, last) of warp `warp` of CTA `cta`: runs of a multiple of 32 slots
 __device__ __forceinline__ void warp_run(long long S, int ctas, int cta, int warp, long long &first, long long &last) {
@@ -137,62 +138,87 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// One thread per 8 columns of a token, or per column where rows are not on
-// 16-byte boundaries. Bound: the bytes of y; every rank's load is issued
-// before the first is used.
+// A thread owns 8 columns of a token (one where rows are not on 16-byte
+// boundaries), blockIdx.y the token. Bound: the bytes of y. Eight ranks at a time
+// their rows are looked up, then all their loads are issued before the first is used
+// (8 x 16 bytes in flight per thread); the sum keeps the order of the ranks.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kCombineThreads)
     combine_slots_kernel(const T *__restrict__ y, long long ldy, int rows, const int *__restrict__ slot_of,
                          const float *__restrict__ topk_w, int n, int top_k, int N, const T *residual,
                          long long ldr, T *out, long long ldo) {
-    constexpr int V = VEC ? 8 : 1;
-    const int groups = (N + V - 1) / V;
-    const long long items = (long long)n * groups;
-    for (long long it = blockIdx.x * 256LL + threadIdx.x; it < items; it += gridDim.x * 256LL) {
-        const int t = (int)(it / groups), c = (int)(it % groups) * V;
-        const bool whole = VEC && c + 8 <= N;
+    constexpr int V = VEC ? 8 : 1, R = 8;
+    const int c = (blockIdx.x * kCombineThreads + threadIdx.x) * V;
+    if (c >= N) return;
+    for (int t = blockIdx.y; t < n; t += gridDim.y) {
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        for (int j = 0; j < top_k; ++j) {
-            const int s = slot_of[(size_t)t * top_k + j];
-            if (s < 0 || s >= rows) continue;
-            const float w = topk_w[(size_t)t * top_k + j];
-            const T *row = y + (size_t)s * ldy + c;
-            if (whole) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(row);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int j0 = 0; j0 < top_k; j0 += R) {
+            int s[R];
+            float w[R];
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i) {
-                    const float2 f = unpack2<T>(u[i]);
-                    acc[2 * i] += w * f.x;
-                    acc[2 * i + 1] += w * f.y;
+            for (int j = 0; j < R; ++j) {
+                const bool in = j0 + j < top_k;
+                s[j] = in ? slot_of[(size_t)t * top_k + j0 + j] : -1;
+                w[j] = in ? topk_w[(size_t)t * top_k + j0 + j] : 0.f;
+            }
+            if constexpr (VEC) {
+                uint4 v[R];
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (s[j] >= 0 && s[j] < rows) v[j] = __ldcs(reinterpret_cast<const uint4 *>(y + (size_t)s[j] * ldy + c));
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    if (s[j] < 0 || s[j] >= rows) continue;
+                    const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack2<T>(u[i]);
+                        acc[2 * i] += w[j] * f.x;
+                        acc[2 * i + 1] += w[j] * f.y;
+                    }
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < N) acc[i] += w * to_f32(row[i]);
+                for (int j = 0; j < R; ++j)
+                    if (s[j] >= 0 && s[j] < rows) acc[0] += w[j] * to_f32(y[(size_t)s[j] * ldy + c]);
             }
         }
-        if (residual)
+        T *o = out + (size_t)t * ldo + c;
+        const T *r = residual ? residual + (size_t)t * ldr + c : nullptr;
+        if constexpr (VEC) {
+            if (r) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(r);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (c + i < N) acc[i] += to_f32(residual[(size_t)t * ldr + c + i]);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (c + i < N) out[(size_t)t * ldo + c + i] = from_f32<T>(acc[i]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<T>(u[i]);
+                    acc[2 * i] += f.x;
+                    acc[2 * i + 1] += f.y;
+                }
+            }
+            *reinterpret_cast<uint4 *>(o) = make_uint4(pack2<T>(acc[0], acc[1]), pack2<T>(acc[2], acc[3]),
+                                                       pack2<T>(acc[4], acc[5]), pack2<T>(acc[6], acc[7]));
+        } else {
+            if (r) acc[0] += to_f32(*r);
+            *o = from_f32<T>(acc[0]);
+        }
     }
 }
+
+// whether rows of 16-bit elements start on 16-byte boundaries
+bool rows16(const void *p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0; }
 
 template <typename T>
 cudaError_t combine(const void *y, long long ldy, int rows, const int *slot_of, const float *topk_w, int n, int top_k,
                     int N, const void *residual, long long ldr, void *out, long long ldo, cudaStream_t st) {
-    const bool vec = ((uintptr_t)y & 15u) == 0 && ldy % 8 == 0;
-    const long long items = (long long)n * (vec ? (N + 7) / 8 : N);
-    const int grid = (int)min((items + 255) / 256, 1LL << 20);
+    const bool vec = N % 8 == 0 && rows16(y, ldy) && rows16(out, ldo) && (!residual || rows16(residual, ldr));
+    const int cols = vec ? N / 8 : N;
+    const dim3 grid((cols + kCombineThreads - 1) / kCombineThreads, min(n, 65535));
     auto k = vec ? combine_slots_kernel<T, true> : combine_slots_kernel<T, false>;
-    k<<<grid, 256, 0, st>>>(static_cast<const T *>(y), ldy, rows, slot_of, topk_w, n, top_k, N,
-                            static_cast<const T *>(residual), ldr, static_cast<T *>(out), ldo);
+    k<<<grid, kCombineThreads, 0, st>>>(static_cast<const T *>(y), ldy, rows, slot_of, topk_w, n, top_k, N,
+                                        static_cast<const T *>(residual), ldr, static_cast<T *>(out), ldo);
     return cudaGetLastError();
 }
 
