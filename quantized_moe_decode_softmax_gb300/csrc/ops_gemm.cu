@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MATS == 2) ptx::prefetch_tensormap(&tmu);
     }
     if (warp == kMmaWarp) tmem_alloc_pair(&tslot, kTmemCols);
+    ptx::griddep_wait();
     int total;
     if (p.offsets) {
         // items per group and their exclusive prefix, kThreads groups at a time
@@ -643,20 +644,6 @@ int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int p
     return best;
 }
 
-cudaLaunchConfig_t pair_launch(cudaLaunchAttribute (&attr)[1], int pairs, int smem, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(kPair * pairs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPair;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
 cudaError_t look_up(int dev, Device &d) {
     int smem = 0, sms = 0, pairs = 0;
     cudaFuncAttributes fa;
@@ -668,8 +655,16 @@ cudaError_t look_up(int dev, Device &d) {
         return err;
     smem -= (int)((fa.sharedSizeBytes + 127) / 128 * 128);
     if ((err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms / kPair * kPair);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pair_launch(attr, sms / kPair, smem, nullptr);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if ((err = cudaOccupancyMaxActiveClusters(&pairs, k, &cfg)) != cudaSuccess) return err;
     if (pairs < 1) return cudaErrorNotSupported;
     d.smem.store(smem, std::memory_order_relaxed);
@@ -688,9 +683,7 @@ cudaError_t launch(const Product &p, const Tiling &g, int pairs, int smem, Devic
         if (err != cudaSuccess) return err;
         d.ready.fetch_or(bit, std::memory_order_release);
     }
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pair_launch(attr, pairs, smem, st);
-    return cudaLaunchKernelEx(&cfg, k, p, g, tmx, tmx_half, tmw, tmu);
+    return launch_overlapped(k, dim3(kPair * pairs), kThreads, smem, kPair, st, p, g, tmx, tmx_half, tmw, tmu);
 }
 
 }  // namespace

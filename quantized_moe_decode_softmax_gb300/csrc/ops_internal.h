@@ -25,6 +25,28 @@ struct Product {
     float limit;                 // 0: no clamp
 };
 
+// A kernel launch that may begin before the stream's previous kernel has ended: the
+// kernel calls griddep_wait before its first access to global memory, so only its
+// start-up overlaps the other's end (about 1 us less between two small kernels).
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
+                              A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // few rows per expert: the weights are streamed once per 32 rows (ops_rows.cu)
 cudaError_t launch_product_rows(const Product &p, cudaStream_t st);
 // many rows per expert: tcgen05 (ops_gemm.cu); cudaErrorNotSupported, with nothing

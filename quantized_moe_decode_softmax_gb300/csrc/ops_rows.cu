@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(32 * kWarps, min_ctas(MATS, TB, AHEAD)) produc
     __shared__ int s_e;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     int e = 0;
+    ptx::griddep_wait();
     if (p.offsets) {
         if (warp == 0) {
             const int f = nth_group(p, blockIdx.y);
@@ -189,11 +190,9 @@ cudaError_t sm_count(int &sms) {
 template <typename T, int MATS, int TB>
 cudaError_t launch(const Product &p, int sms, cudaStream_t st) {
     const dim3 grid((p.N + kCols - 1) / kCols, p.offsets ? min(p.E, p.rows) : 1);
-    if ((long long)grid.x * grid.y <= 2 * sms)
-        product_rows_kernel<T, MATS, TB, true><<<grid, 32 * kWarps, 0, st>>>(p);
-    else
-        product_rows_kernel<T, MATS, TB, false><<<grid, 32 * kWarps, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped((long long)grid.x * grid.y <= 2 * sms ? product_rows_kernel<T, MATS, TB, true>
+                                                                   : product_rows_kernel<T, MATS, TB, false>,
+                             grid, 32 * kWarps, 0, 1, st, p);
 }
 
 template <typename T, int MATS>

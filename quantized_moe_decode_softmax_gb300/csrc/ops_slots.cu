@@ -21,6 +21,7 @@
 #include <atomic>
 
 #include "ops_common.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace ops {
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(kThreads)
     const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < kWarps * E; i += kThreads) cnt[i] = 0;
+    ptx::griddep_wait();
     __syncthreads();
     long long first, last;
     warp_run(S, ctas, cta, warp, first, last);
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(kCombineThreads)
                          long long ldr, T *out, long long ldo) {
     constexpr int V = VEC ? 8 : 1, R = 8;
     const int c = (blockIdx.x * kCombineThreads + threadIdx.x) * V;
+    ptx::griddep_wait();
     if (c >= N) return;
     for (int t = blockIdx.y; t < n; t += gridDim.y) {
         float acc[V];
@@ -217,9 +220,8 @@ cudaError_t combine(const void *y, long long ldy, int rows, const int *slot_of, 
     const int cols = vec ? N / 8 : N;
     const dim3 grid((cols + kCombineThreads - 1) / kCombineThreads, min(n, 65535));
     auto k = vec ? combine_slots_kernel<T, true> : combine_slots_kernel<T, false>;
-    k<<<grid, kCombineThreads, 0, st>>>(static_cast<const T *>(y), ldy, rows, slot_of, topk_w, n, top_k, N,
-                                        static_cast<const T *>(residual), ldr, static_cast<T *>(out), ldo);
-    return cudaGetLastError();
+    return launch_overlapped(k, grid, kCombineThreads, 0, 1, st, static_cast<const T *>(y), ldy, rows, slot_of, topk_w,
+                             n, top_k, N, static_cast<const T *>(residual), ldr, static_cast<T *>(out), ldo);
 }
 
 }  // namespace
@@ -242,19 +244,8 @@ cudaError_t launch_group_slots(const int *topk_idx, int n, int top_k, int E, int
             raised.fetch_or(bit, std::memory_order_release);
         }
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, group_slots_kernel, topk_idx, S, top_k, E, e_lo, e_hi, offsets, slot_token,
-                              slot_k, slot_of);
+    return launch_overlapped(group_slots_kernel, dim3(ctas), kThreads, smem, ctas, st, topk_idx, S, top_k, E, e_lo,
+                             e_hi, offsets, slot_token, slot_k, slot_of);
 }
 
 cudaError_t launch_combine_slots(int dtype, const void *y, long long ldy, int rows, const int *slot_of,
