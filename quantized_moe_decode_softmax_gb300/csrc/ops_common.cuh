@@ -62,7 +62,7 @@ __device__ __forceinline__ float unary_act(int act, float z) {
         const float x = fabsf(z) * 0.70710678118654752f, t = rcp_fast(1.0f + 0.3275911f * x);
         const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
         const float c = 0.5f * poly * exp2_fast(-kLog2e * x * x);  // erfc(x) / 2
-        return z > 0.f ? z - z * c : z * c;
+        return z * (z > 0.f ? 1.0f - c : c);
     }
     constexpr float kTwoC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     const float t = act == MOE_EPI_SILU ? -kLog2e * z
@@ -110,7 +110,8 @@ __device__ __forceinline__ void group_rows(const Product &p, int e, int &lo, int
 
 // the row of x that feeds row r, inside 0..x_rows-1 whatever row_token holds
 __device__ __forceinline__ int input_row(const Product &p, int r) {
-    return p.row_token ? min(max(p.row_token[r], 0), p.x_rows - 1) : min(r, p.x_rows - 1);
+    r = min(max(r, 0), p.rows - 1);
+    return min(p.row_token ? max(p.row_token[r], 0) : r, p.x_rows - 1);
 }
 
 }  // namespace ops

@@ -269,11 +269,13 @@ struct Walk {
         }
         int lo, hi;
         group_rows(p, e, lo, hi);
-        const int c = hi - lo, T = tile_rows(c, g.tcap), nt = (c + T - 1) / T;
+        // (offsets that do not ascend number the items wrongly: the bounds below keep
+        // such an item's tile in shape and its rows in range)
+        const int c = max(hi - lo, 1), T = tile_rows(c, g.tcap), nt = (c + T - 1) / T;
         // bands of kBand row tiles: the tiles of a band run side by side on one
         // weight block, then on the next
         const int per_band = kBand * g.mblocks, band = i / per_band, r = i - band * per_band;
-        const int bh = min(kBand, nt - band * kBand);
+        const int bh = max(min(kBand, nt - band * kBand), 1);
         it.e = e;
         it.m = r / bh;
         it.T = T;
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = it.T / kPair;  // rows of x that this CTA loads
             const int r0 = it.r0 + rank * half;
             const uint32_t bytes = kPair * (MATS * kTileA + (gather ? half : box_rows(half)) * 128);
-            const int col = (it.m * kPair + rank) * kM;
+            const int col = (it.m * kPair + rank) * kM, plane = p.stride_e ? it.e : 0;
             const int k_end = nk * kK;
             if (gather) {
                 // lane j's rows are the warp's j-th copy; rows past the end repeat the last one
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
                     if (loads_w && tc::elect_one()) {
                         if (counts) expect_tx(full_addr + 8 * at.s, bytes);
-                        tma_3d(at.stage + (warp == 0 ? 0 : kTileA), map, k, col, it.e, at.full);
+                        tma_3d(at.stage + (warp == 0 ? 0 : kTileA), map, k, col, plane, at.full);
                     }
                     if (lane < fours) tma_gather4(at.stage + dst, &tmx, k, rows, at.full);
                     at.next(stages, stage_bytes);
@@ -437,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
                         if (tc::elect_one()) {
                             if (rank == 0) expect_tx(full_addr + 8 * at.s, bytes);
-                            tma_3d(at.stage, &tmw, k, col, it.e, at.full);
-                            if (MATS == 2) tma_3d(at.stage + kTileA, &tmu, k, col, it.e, at.full);
+                            tma_3d(at.stage, &tmw, k, col, plane, at.full);
+                            if (MATS == 2) tma_3d(at.stage + kTileA, &tmu, k, col, plane, at.full);
                         }
                     }
                     skip = !skip;
@@ -711,13 +713,14 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     const int smem = 1024 + g.stages * g.stage_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     if (most > 0x7fffffffLL) return cudaErrorNotSupported;
+    const int planes = p.stride_e ? p.E : 1;  // experts may share one matrix
     alignas(64) CUtensorMap tmx, tmx_half, tmw, tmu;
     if (!encode(&tmx, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||
         !encode(&tmx_half, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, kBoxRows / 2) ||
-        !encode(&tmw, p.dtype, p.w, p.K, p.N, p.ldw, p.E, p.E > 1 ? p.stride_e : p.ldw * p.N, kM))
+        !encode(&tmw, p.dtype, p.w, p.K, p.N, p.ldw, planes, p.stride_e ? p.stride_e : p.ldw, kM))
         return cudaErrorNotSupported;
     tmu = tmw;
-    if (mats == 2 && !encode(&tmu, p.dtype, p.w_up, p.K, p.N, p.ldw, p.E, p.E > 1 ? p.stride_e : p.ldw * p.N, kM))
+    if (mats == 2 && !encode(&tmu, p.dtype, p.w_up, p.K, p.N, p.ldw, planes, p.stride_e ? p.stride_e : p.ldw, kM))
         return cudaErrorNotSupported;
     const int n = (int)min(most, (long long)all);
     if (p.dtype == MOE_DTYPE_BF16)

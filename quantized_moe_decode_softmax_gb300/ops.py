@@ -62,16 +62,18 @@ def _dtype_code(dtype) -> int:
 
 
 def _rows(t, what: str, cols: int, dtype, device, n: int = -1) -> int:
-    """Check a [n, cols] tensor (any n: -1) whose columns are adjacent; the distance
-    of its rows. A call spends about as long here as on the GPU for a few tokens,
-    so that each property is asked for once."""
+    """Check a [n, cols] tensor (any n: -1) whose columns are adjacent on CUDA device
+    number `device`; the distance of its rows. A call spends about as long here as
+    on the GPU for a few tokens, so that each property is asked for once."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or (n >= 0 and shape[0] != n):
         raise ValueError(f"{what} has shape {tuple(shape)}, not [{'n' if n < 0 else n}, {cols}]")
     if t.dtype is not dtype:
         raise TypeError(f"{what} is {t.dtype}, not {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, not on CUDA device {device}")
+    if t.is_contiguous():
+        return cols
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{what}: the columns of a row have to be adjacent")
@@ -83,17 +85,18 @@ def _ints(t, what: str, shape, device):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype is not torch.int32:
         raise TypeError(f"{what} is {t.dtype}, not int32")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} has to be contiguous and on {device}")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} has to be contiguous and on CUDA device {device}")
 
 
 class _Elsewhere:
-    """The device and stream of a call that names a stream or whose tensors are not
-    on the current device: outputs are allocated there, kernels go there."""
+    """The device (by its number) and stream of a call that names a stream or whose
+    tensors are not on the current device: outputs are allocated there, kernels go
+    there."""
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"tensors have to be on a CUDA device, not on {device}")
+    def __init__(self, device: int, stream):
+        if device < 0:
+            raise ValueError("tensors have to be on a CUDA device")
         self._device = device
         self._on_device = torch.cuda.device(device)
         if isinstance(stream, int):
@@ -112,9 +115,9 @@ class _Elsewhere:
         self._on_device.__exit__(*exc)
 
 
-def _here(device, stream) -> bool:
+def _here(device: int, stream) -> bool:
     """Whether a call needs neither another device nor another stream."""
-    return stream is None and device.type == "cuda" and torch._C._cuda_getDevice() == device.index
+    return stream is None and device >= 0 and torch._C._cuda_getDevice() == device
 
 
 class LinearWeights:
@@ -138,7 +141,7 @@ class LinearWeights:
         self.grouped = w.dim() == 3
         self.E = w.shape[0] if self.grouped else 1
         self.N, self.K = w.shape[-2], w.shape[-1]
-        self.dtype, self.device = w.dtype, w.device
+        self.dtype, self.device, self.device_index = w.dtype, w.device, w.get_device()
         self.tensors = (w, w_up, bias, bias_up)
         if self.E < 1 or self.N < 1 or self.K < 1:
             raise ValueError(f"w is empty: {tuple(w.shape)}")
@@ -169,9 +172,9 @@ class SlotGroups(NamedTuple):
     slot_of: object
 
 
-def _no_grad(x):
-    if x.requires_grad and torch.is_grad_enabled():
-        raise RuntimeError("x requires a gradient: the operators record none (use torch.no_grad())")
+def _no_grad(x, residual=None):
+    if (x.requires_grad or (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
+        raise RuntimeError("an input requires a gradient: the operators record none (use torch.no_grad())")
 
 
 def _raise(status: int, what: str):
@@ -182,8 +185,8 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     """out [n, N] = epilogue(x [n, K]) (+ residual [n, N]); `out` may be `residual`."""
     if weights.grouped:
         raise ValueError("moe_linear takes weights [N, K]; use moe_grouped_linear")
-    _no_grad(x)
-    dt, dev, N = weights.dtype, weights.device, weights.N
+    _no_grad(x, residual)
+    dt, dev, N = weights.dtype, weights.device_index, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
     n = x.shape[0]
     ldr = ldo = N
@@ -192,7 +195,7 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     if out is not None:
         ldo = _rows(out, "out", N, dt, dev, n)
     if _here(dev, stream):
-        return _linear(x, ldx, n, weights, residual, ldr, out, ldo, torch._C._cuda_getCurrentRawStream(dev.index))
+        return _linear(x, ldx, n, weights, residual, ldr, out, ldo, torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
         return _linear(x, ldx, n, weights, residual, ldr, out, ldo, st)
 
@@ -215,7 +218,7 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     if not weights.grouped:
         raise ValueError("moe_grouped_linear takes weights [E, N, K]; use moe_linear")
     _no_grad(x)
-    dt, dev, N = weights.dtype, weights.device, weights.N
+    dt, dev, N = weights.dtype, weights.device_index, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
     rows = x.shape[0]
     if row_token is not None:
@@ -227,7 +230,7 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     ldo = N if out is None else _rows(out, "out", N, dt, dev, rows)
     if _here(dev, stream):
         return _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo,
-                        torch._C._cuda_getCurrentRawStream(dev.index))
+                        torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
         return _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo, st)
 
@@ -249,18 +252,19 @@ def moe_group_slots(topk_idx, E: int, experts: Optional[Tuple[int, int]] = None,
     end) of the ids that take part, all of them by default; other ids (another
     shard's, -1 for a dropped slot) belong to no group."""
     _lib()
-    shape, dev = topk_idx.shape, topk_idx.device
+    shape, dev = topk_idx.shape, topk_idx.get_device()
     if len(shape) != 2:
         raise ValueError(f"topk_idx has shape {tuple(shape)}, not [n, top_k]")
     _ints(topk_idx, "topk_idx", shape, dev)
     if _here(dev, stream):
-        return _slots(topk_idx, shape, E, experts, dev, torch._C._cuda_getCurrentRawStream(dev.index))
+        return _slots(topk_idx, shape, E, experts, torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
-        return _slots(topk_idx, shape, E, experts, dev, st)
+        return _slots(topk_idx, shape, E, experts, st)
 
 
-def _slots(topk_idx, shape, E, experts, dev, st):
+def _slots(topk_idx, shape, E, experts, st):
     n, k = shape
+    dev = topk_idx.device
     lo, hi = (0, E) if experts is None else experts
     int32 = torch.int32
     # four allocations: views of one cost more time
@@ -281,8 +285,8 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
     slot_of [n, top_k] int32 (a slot outside y's rows adds nothing), topk_w
     [n, top_k] float32; `out` may be `residual`."""
     _lib()
-    _no_grad(y)
-    dt, dev = y.dtype, y.device
+    _no_grad(y, residual)
+    dt, dev = y.dtype, y.get_device()
     code = _dtype_code(dt)
     shape, ys = slot_of.shape, y.shape
     if len(shape) != 2 or len(ys) != 2:
@@ -290,9 +294,9 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
     n, N = shape[0], ys[1]
     ldy = _rows(y, "y", N, dt, dev)
     _ints(slot_of, "slot_of", shape, dev)
-    if topk_w.shape != shape or topk_w.dtype is not torch.float32 or topk_w.device != dev \
+    if topk_w.shape != shape or topk_w.dtype is not torch.float32 or topk_w.get_device() != dev \
             or not topk_w.is_contiguous():
-        raise ValueError(f"topk_w has to be contiguous float32 {tuple(shape)} on {dev}")
+        raise ValueError(f"topk_w has to be contiguous float32 {tuple(shape)} on CUDA device {dev}")
     ldr = ldo = N
     if residual is not None:
         ldr = _rows(residual, "residual", N, dt, dev, n)
@@ -300,7 +304,7 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
         ldo = _rows(out, "out", N, dt, dev, n)
     if _here(dev, stream):
         return _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo,
-                        torch._C._cuda_getCurrentRawStream(dev.index))
+                        torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
         return _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st)
 

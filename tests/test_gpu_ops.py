@@ -109,6 +109,64 @@ def test_linear_extreme_values():
     assert bool(torch.isinf(out).all())
 
 
+@pytest.mark.parametrize("n", [2, 90])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh"])
+def test_activations_over_the_whole_range(act, gated, n):
+    """Each activation from -inf to inf through an identity product: the values and
+    signs of infinities and NaN as the formula gives them."""
+    z = torch.cat([torch.linspace(-30, 30, 400), torch.tensor([0.0, -0.0, 1e-6, -1e-6, 90.0, -90.0, 1e4, -1e4])]).cuda()
+    for dtype, far in ((BF16, 3e38), (F16, 6e4)):
+        v = torch.cat([z, torch.tensor([far, -far], device="cuda")]).to(dtype)
+        w = torch.zeros(8, 8, dtype=dtype, device="cuda")
+        w[0, 0] = 1
+        one = torch.zeros(8, dtype=dtype, device="cuda")
+        one[0] = 1
+        for start in range(0, v.numel(), n):
+            part = v[start:start + n]
+            x = torch.zeros(part.numel(), 8, dtype=dtype, device="cuda")
+            x[:, 0] = part
+            lw = q.LinearWeights(w, w_up=torch.zeros_like(w) if gated else None, bias_up=one if gated else None,
+                                 activation=act)
+            d = part.double()
+            r = ref.act64(act, d)
+            r = torch.where(d < -1e3, torch.zeros_like(r) if act != "none" else r, r)  # exp overflows f64 there
+            ref.check(q.moe_linear(x, lw)[:, 0], r, d.abs() * 2.0 ** -19 + 2.0 ** -22)
+    # an infinite sum: bias of the type's infinity
+    x, w = torch.zeros(n, 8, dtype=BF16, device="cuda"), torch.zeros(2, 8, dtype=BF16, device="cuda")
+    b = torch.tensor([float("inf"), float("nan")], dtype=BF16, device="cuda")
+    out = q.moe_linear(x, q.LinearWeights(w, bias=b, activation=act))
+    assert bool((out[:, 0] == float("inf")).all()) and bool(torch.isnan(out[:, 1]).all())
+    out = q.moe_linear(x, q.LinearWeights(w, bias=b, w_up=w, bias_up=torch.ones_like(b), activation=act, act_limit=2.0))
+    r = ref.act64(act, torch.tensor(2.0, dtype=torch.float64))
+    assert float((out[:, 0].double() - r.cuda()).abs().max()) <= 2.0 * 2.0 ** -8
+    assert bool(torch.isnan(out[:, 1]).all())  # a clamp keeps a NaN
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("n,N,K", [(100, 7, 8), (70, 1, 24), (333, 300, 16), (5000, 9, 72), (90, 2050, 1000)])
+def test_linear_thin_products(n, N, K, gated):
+    """Many rows with a few columns or inputs, far below a tile."""
+    g = gen(n)
+    t = weights(g, (), N, K, BF16, gated, True)
+    x = normal(g, (n, K))
+    ref.check(q.moe_linear(x, q.LinearWeights(**t, activation="silu")), *ref.product(x, act="silu", **t))
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_grouped_weights_in_other_layouts(rows):
+    """One matrix for all experts, and experts inside the rows ([N, E, K])."""
+    g = gen(rows)
+    E, N, K = 3, 72, 136
+    counts = [rows, 0, rows + 1]
+    x = normal(g, (sum(counts), K))
+    one = normal(g, (1, N, K), K ** -0.5).expand(E, N, K)
+    mixed = normal(g, (N, E, K), K ** -0.5).transpose(0, 1)
+    for w in (one, mixed):
+        out = q.moe_grouped_linear(x, q.LinearWeights(w), offsets_of(counts))
+        check_grouped(x, {"w": w}, counts, "none", out)
+
+
 def test_empty_calls():
     lw = q.LinearWeights(torch.zeros(16, 24, dtype=BF16, device="cuda"))
     assert q.moe_linear(torch.zeros(0, 24, dtype=BF16, device="cuda"), lw).shape == (0, 16)
@@ -209,6 +267,11 @@ def test_grouped_bounds_offsets_and_tokens(rows):
     x = normal(g, (rows, K))
     buf = torch.full((rows + 64, N), 7.0, dtype=BF16, device="cuda")
     half = rows // 2
+    if rows > 100:  # offsets that go back and forth: nothing is promised but that nothing else is touched
+        wild = torch.tensor([rows, -9, 1 << 30, 5], dtype=torch.int32, device="cuda")
+        q.moe_grouped_linear(x, q.LinearWeights(w), wild, out=buf[32:32 + rows])
+        q.moe_ops_check()
+        assert bool((buf[:32] == 7).all()) and bool((buf[32 + rows:] == 7).all())
     off = torch.tensor([-5, half, 1 << 30, -7], dtype=torch.int32, device="cuda")
     token = torch.arange(rows, dtype=torch.int32, device="cuda")
     token[-1], token[-2] = 1 << 30, -3
