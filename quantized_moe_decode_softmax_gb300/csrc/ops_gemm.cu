@@ -157,8 +157,11 @@ __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
                  : "memory");
 }
 
+// Relaxed: what it orders is tensor-memory reads that have completed (wait::ld). A
+// release at cluster scope would first wait for the warp's stores to reach L2: about a
+// microsecond per tile, in which a tile with one accumulator set cannot begin.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // TMA loads into this CTA's shared memory, counted by a barrier of the pair's
@@ -529,11 +532,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, wait(acc_full_addr + 8 * buf, (uint32_t)(use & 1), abort_flag))) break;
             tc::fence_after_sync();
             const uint32_t acc = tlane + (uint32_t)(buf * MATS * g.tcap);
+            // the next tile's MMAs may overwrite this accumulator set
+            auto done_reading = [&] {
+                tc::fence_before_sync();
+                if (lane == 0) arrive_cluster(in_first(acc_empty_addr + 8 * buf));
+            };
             auto chunk = [&](int t0, T (&r)[16]) {
                 float v[16], u[MATS == 2 ? 16 : 1];
                 tmem_ld16(acc + t0, v);
                 if constexpr (MATS == 2) tmem_ld16(acc + g.tcap + t0, u);
                 tmem_wait_ld();
+                if (t0 + 32 >= it.rows) done_reading();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += b0;
                 if constexpr (MATS == 2) {
@@ -567,8 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 chunk(t0, ra);
                 if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
             }
-            tc::fence_before_sync();
-            if (lane == 0) arrive_cluster(in_first(acc_empty_addr + 8 * buf));
+            if (16 * part >= it.rows) done_reading();  // a tile of at most 16 rows has no chunk for the other half
         }
     }
     tc::fence_before_sync();
