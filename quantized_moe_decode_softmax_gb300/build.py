@@ -2,7 +2,9 @@
 
 Each .cu file under csrc/ is compiled to an object in parallel, then linked
 into one shared library next to this file. The CUDA runtime is linked
-statically, so the library needs only the driver at run time.
+statically, so the library needs only the driver at run time. A second, small
+module (torch_calls.cpp) takes torch tensors to the operators' entry points; it
+is built where torch is installed, for that version of it.
 """
 from __future__ import annotations
 
@@ -50,9 +52,46 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def calls_path():
+    """Where the torch_calls module for the installed torch is built; None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    version = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(PKG, f"_torch_calls_{version}.so")
+
+
+def build_calls(force: bool = False):
+    """Compile torch_calls.cpp with the host compiler; returns its path or None."""
+    path = calls_path()
+    if path is None:
+        return None
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    deps = [src, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+        return path
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    inc = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{d}" for d in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    return path
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile and link; returns the library path. Skips work when up to date."""
     if not force and up_to_date():
+        build_calls()
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -74,8 +113,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        calls = ex.submit(build_calls, force)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

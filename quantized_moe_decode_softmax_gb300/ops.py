@@ -5,13 +5,20 @@ C names; LinearWeights holds the weights and the epilogue of a product. As in
 the rest of the binding nothing is computed here: the functions check the
 tensors, pass pointers and sizes to libmoe_decode.so, and turn status codes into
 MoeError. Inference only: no gradients are recorded.
+
+A usual call goes through the torch_calls module (csrc/torch_calls.cpp), which does
+the same checks in less time and returns None for whatever is not usual; the
+functions here then take over, with their messages.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 from typing import NamedTuple, Optional, Tuple
 
-from . import _abi
+from . import _abi, build
 
 MOE_DTYPE_F16 = 2
 MOE_EPI_NONE, MOE_EPI_SILU, MOE_EPI_GELU, MOE_EPI_GELU_TANH = range(4)
@@ -27,13 +34,14 @@ class moe_product(ctypes.Structure):
                 ("activation", ctypes.c_int), ("act_limit", ctypes.c_float)]
 
 
-torch = None  # bound by _bind: importing the package does not import torch
-_c = None     # the operators' C functions
+torch = None   # bound by _bind: importing the package does not import torch
+_c = None      # the operators' C functions
+_calls = None  # the torch_calls module, where it has been built for this torch
 
 
 def _bind():
     """Bind torch and the C functions (first use; raises if the library is not built)."""
-    global torch, _c
+    global torch, _c, _calls
     L = _abi.lib()
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
     L.moe_linear.argtypes = [vp, vp, i64, i32, vp, i64, vp, i64, vp]
@@ -45,6 +53,13 @@ def _bind():
         getattr(L, name).restype = i32
     import torch as t
     torch = t
+    path = build.calls_path()
+    if path is not None and os.path.exists(path):
+        loader = importlib.machinery.ExtensionFileLoader("_torch_calls", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_torch_calls", path, loader=loader))
+        m.bind(*[ctypes.cast(getattr(L, f), vp).value for f in
+                 ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots")])
+        _calls = m
     _c = L
     return L
 
@@ -183,6 +198,10 @@ def _raise(status: int, what: str):
 
 def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     """out [n, N] = epilogue(x [n, K]) (+ residual [n, N]); `out` may be `residual`."""
+    if stream is None and _calls is not None and not weights.grouped:
+        r = _calls.linear(weights.ref, weights.device_index, x, residual, out)
+        if r is not None:
+            return r if r.__class__ is not int else _raise(r, "moe_linear")
     if weights.grouped:
         raise ValueError("moe_linear takes weights [N, K]; use moe_grouped_linear")
     _no_grad(x, residual)
@@ -215,6 +234,10 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     """out [rows, N]: row r of group e (offsets[e] <= r < offsets[e+1]) through
     expert e's matrix. x is [rows, K], or [tokens, K] with row_token [rows]. Rows
     outside every group are left as they were (unset in an `out` made here)."""
+    if stream is None and _calls is not None and weights.grouped:
+        r = _calls.grouped(weights.ref, weights.device_index, x, offsets, row_token, out)
+        if r is not None:
+            return r if r.__class__ is not int else _raise(r, "moe_grouped_linear")
     if not weights.grouped:
         raise ValueError("moe_grouped_linear takes weights [E, N, K]; use moe_linear")
     _no_grad(x)
@@ -252,20 +275,24 @@ def moe_group_slots(topk_idx, E: int, experts: Optional[Tuple[int, int]] = None,
     end) of the ids that take part, all of them by default; other ids (another
     shard's, -1 for a dropped slot) belong to no group."""
     _lib()
+    lo, hi = (0, E) if experts is None else experts
+    if stream is None and _calls is not None:
+        r = _calls.slots(topk_idx, E, lo, hi)
+        if r is not None:
+            return SlotGroups._make(r) if r.__class__ is not int else _raise(r, "moe_group_slots")
     shape, dev = topk_idx.shape, topk_idx.get_device()
     if len(shape) != 2:
         raise ValueError(f"topk_idx has shape {tuple(shape)}, not [n, top_k]")
     _ints(topk_idx, "topk_idx", shape, dev)
     if _here(dev, stream):
-        return _slots(topk_idx, shape, E, experts, torch._C._cuda_getCurrentRawStream(dev))
+        return _slots(topk_idx, shape, E, lo, hi, torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
-        return _slots(topk_idx, shape, E, experts, st)
+        return _slots(topk_idx, shape, E, lo, hi, st)
 
 
-def _slots(topk_idx, shape, E, experts, st):
+def _slots(topk_idx, shape, E, lo, hi, st):
     n, k = shape
     dev = topk_idx.device
-    lo, hi = (0, E) if experts is None else experts
     int32 = torch.int32
     # four allocations: views of one cost more time
     offsets = torch.empty(max(E, 0) + 1, dtype=int32, device=dev)
@@ -285,6 +312,10 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
     slot_of [n, top_k] int32 (a slot outside y's rows adds nothing), topk_w
     [n, top_k] float32; `out` may be `residual`."""
     _lib()
+    if stream is None and _calls is not None:
+        r = _calls.combine(y, slot_of, topk_w, residual, out)
+        if r is not None:
+            return r if r.__class__ is not int else _raise(r, "moe_combine_slots")
     _no_grad(y, residual)
     dt, dev = y.dtype, y.get_device()
     code = _dtype_code(dt)

@@ -468,6 +468,55 @@ def test_graphs_streams_and_repeats(n):
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n", [1, 90])
+def test_calls_with_and_without_the_torch_module(n, monkeypatch):
+    """The same bits and the same refusals with the torch_calls module and without."""
+    g = gen(n)
+    t = q.LinearWeights(normal(g, (72, 136), 0.1), activation="silu")
+    tg = q.LinearWeights(normal(g, (6, 72, 136), 0.1))
+    x, res = normal(g, (n, 136)), normal(g, (n, 72))
+    idx, w = route(g, n, 2, 6)
+
+    def every():
+        out = normal(gen(1), (n, 80))[:, 3:75]
+        yield q.moe_linear(x, t, residual=res)
+        yield q.moe_linear(x, t, residual=out, out=out)
+        s = q.moe_group_slots(idx, 6, experts=(1, 5))
+        yield from s
+        y = torch.zeros(2 * n, 72, dtype=BF16, device="cuda")
+        yield q.moe_grouped_linear(x, tg, s.offsets, row_token=s.slot_token, out=y)
+        yield q.moe_combine_slots(y, s.slot_of, w, residual=res)
+        yield q.moe_combine_slots(y[:, 1:], s.slot_of, w)
+
+    def refused():
+        for call in (lambda: q.moe_linear(x[:, :128], t), lambda: q.moe_linear(x.half(), t),
+                     lambda: q.moe_linear(x, tg), lambda: q.moe_linear(x.cpu(), t),
+                     lambda: q.moe_linear(x.t().contiguous().t() if n > 1 else x[:, ::2], t),
+                     lambda: q.moe_linear(x, t, residual=res[:, :71]), lambda: q.moe_linear(x, t, out=x),
+                     lambda: q.moe_linear(x.clone().requires_grad_(), t),
+                     lambda: q.moe_linear(x, t, residual=res.clone().requires_grad_()),
+                     lambda: q.moe_linear(x[:1].expand(9, 136), t), lambda: q.moe_linear(None, t),
+                     lambda: q.moe_grouped_linear(x, tg, torch.zeros(6, dtype=torch.int32, device="cuda")),
+                     lambda: q.moe_grouped_linear(x, tg, torch.zeros(7, device="cuda")),
+                     lambda: q.moe_grouped_linear(x, t, torch.zeros(2, dtype=torch.int32, device="cuda")),
+                     lambda: q.moe_group_slots(idx, 2000), lambda: q.moe_group_slots(idx, 6, experts=(4, 2)),
+                     lambda: q.moe_group_slots(idx.long(), 6), lambda: q.moe_group_slots(idx, 0),
+                     lambda: q.moe_combine_slots(x, idx, w.double()), lambda: q.moe_combine_slots(x.float(), idx, w),
+                     lambda: q.moe_combine_slots(x, idx[:, :1], w)):
+            try:
+                call()
+                yield "nothing"
+            except Exception as e:
+                yield type(e).__name__
+
+    assert q.ops._calls is not None
+    with_module, refusals = [v.clone() for v in every()], list(refused())
+    monkeypatch.setattr(q.ops, "_calls", None)
+    for a, b in zip(with_module, every()):
+        assert torch.equal(a, b)
+    assert list(refused()) == refusals and "nothing" not in refusals
+
+
 def test_two_streams_at_once():
     """Independent calls that overlap on the device do not disturb one another."""
     g = gen(21)

@@ -112,6 +112,25 @@ def test_slots_and_combine_refuse_bad_calls(lib):
         assert st == status, over
 
 
+def test_torch_calls_module_leaves_what_is_not_usual(lib):
+    """The module is built with the library, and answers None (never an exception)
+    to a call that its caller has to look at."""
+    c = ops._calls
+    assert c is not None and os.path.samefile(c.__file__, qbuild.calls_path())
+    w = torch.zeros(16, 24, dtype=torch.bfloat16)
+    lw, x, i = q.LinearWeights(w), torch.zeros(2, 24, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32)
+    assert c.linear(lw.ref, lw.device_index, x, None, None) is None  # not on a GPU
+    assert c.linear(lw.ref, 0, x, None, None) is None
+    assert c.linear(lw.ref, 0, None, None, None) is None
+    assert c.linear(lw.ref, 0, "x", None, None) is None
+    assert c.linear(lw.ref, 0, torch.nn.Parameter(x), None, None) is None
+    assert c.linear(lw.ref, 0, x.to_sparse(), None, None) is None
+    assert c.linear(1, 2) is None
+    assert c.grouped(lw.ref, 0, x, i, None, None) is None and c.grouped(lw.ref, 0, x, None, None, None) is None
+    assert c.slots(i, 4, 0, 4) is None and c.slots(i, "4", 0, 4) is None and c.slots(i, 1 << 70, 0, 4) is None
+    assert c.combine(x, i, i, None, None) is None and c.combine(x, None, i, None, None) is None
+
+
 def test_python_checks():
     w = torch.zeros(16, 24, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
