@@ -32,43 +32,54 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kCombineThreads = 128;
 
-// slots [first, last) of warp `warp` of CTA `cta`: runs of a multiple of 32 slots
-__device__ __forceinline__ void warp_run(long long S, int ctas, int cta, int warp, long long &first, long long &last) {
-    const long long rounds = (S + 32LL * ctas * kWarps - 1) / (32LL * ctas * kWarps);
-    first = min((long long)(cta * kWarps + warp) * rounds * 32, S);
-    last = min(first + rounds * 32, S);
-}
+constexpr int kAhead = 8;  // rounds whose ids are loaded together
 
 __global__ void __launch_bounds__(kThreads)
     group_slots_kernel(const int *__restrict__ topk_idx, long long S, int top_k, int E, int e_lo, int e_hi,
                        int *__restrict__ offsets, int *__restrict__ slot_token, int *__restrict__ slot_k,
                        int *__restrict__ slot_of) {
     extern __shared__ int sm[];
-    int *cnt = sm;                 // [kWarps][E] counters, then each warp's next row per expert
-    int *total = sm + kWarps * E;  // [E] this CTA's counts (read by the cluster)
+    int *cnt = sm;                 // [kWarps][E] counters, then the rows of the earlier warps per expert
+    int *total = sm + kWarps * E;  // [E] this CTA's counts (read by the cluster), then its first rows
     __shared__ int warp_sum[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < kWarps * E; i += kThreads) cnt[i] = 0;
+    const long long rounds = (S + 32LL * ctas * kWarps - 1) / (32LL * ctas * kWarps);
+    // slots [first, last) are this warp's; later warps than `used` of a CTA have none
+    const long long first = min((long long)(cta * kWarps + warp) * rounds * 32, S), last = min(first + rounds * 32, S);
+    const int used = rounds ? (int)min((S + 32 * rounds - 1) / (32 * rounds), (long long)kWarps) : 0;
+    for (int i = tid; i < used * E; i += kThreads) cnt[i] = 0;
     ptx::griddep_wait();
     __syncthreads();
-    long long first, last;
-    warp_run(S, ctas, cta, warp, first, last);
     int *mine = cnt + warp * E;
-    for (long long i = first; i < last; i += 32) {
-        const int id = i + lane < last ? topk_idx[i + lane] : -1;
-        const bool in = id >= e_lo && id < e_hi;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? id : -1);
-        if (in && (same & ((1u << lane) - 1)) == 0) mine[id] += __popc(same);
-        __syncwarp();
+    // the ids of kAhead rounds; -1 outside the experts and the run
+    int ids[kAhead];
+    auto load = [&](long long i) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const long long at = i + 32 * a + lane;
+            const int id = at < last ? topk_idx[at] : -1;
+            ids[a] = id >= e_lo && id < e_hi ? id : -1;
+        }
+    };
+    for (long long i = first; i < last; i += 32 * kAhead) {
+        load(i);
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            if (i + 32 * a >= last) break;
+            const int id = ids[a];
+            const unsigned same = __match_any_sync(0xffffffffu, id);
+            if (id >= 0 && (same & ((1u << lane) - 1)) == 0) mine[id] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // thread e: prefix over the CTA's warps (E <= kThreads)
     int sum = 0;
     if (tid < E) {
 #pragma unroll 8
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < used; ++w) {
             const int c = cnt[w * E + tid];
             cnt[w * E + tid] = sum;
             sum += c;
@@ -86,7 +97,7 @@ __global__ void __launch_bounds__(kThreads)
             all += v;
         }
     }
-    if (ctas > 1) cluster.sync();  // no CTA leaves while another reads its counts
+    if (ctas > 1) cluster.sync();  // no CTA leaves, or reuses its counts, while another reads them
     // exclusive scan of the counts over the experts
     int scan = all;
 #pragma unroll
@@ -113,24 +124,28 @@ __global__ void __launch_bounds__(kThreads)
             offsets[tid] = base;
             if (tid == E - 1) offsets[E] = rows;
         }
-        for (int w = 0; w < kWarps; ++w) cnt[w * E + tid] += base + before;
+        total[tid] = base + before;
     }
     __syncthreads();
-    for (long long i = first; i < last; i += 32) {
-        const bool live = i + lane < last;
-        const int id = live ? topk_idx[i + lane] : -1;
-        const bool in = id >= e_lo && id < e_hi;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? id : -1);
-        const unsigned lower = same & ((1u << lane) - 1);
-        const int at = in ? mine[id] + __popc(lower) : -1;
-        __syncwarp();
-        if (in && lower == 0) mine[id] += __popc(same);
-        __syncwarp();
-        if (live) slot_of[i + lane] = at;
-        if (in) {
-            const int slot = (int)(i + lane);
-            slot_token[at] = slot / top_k;
-            if (slot_k) slot_k[at] = slot % top_k;
+    for (long long i = first; i < last; i += 32 * kAhead) {
+        if (rounds > kAhead) load(i);  // a shorter run's ids are still there
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            if (i + 32 * a >= last) break;
+            const int id = ids[a];
+            const unsigned same = __match_any_sync(0xffffffffu, id);
+            const unsigned lower = same & ((1u << lane) - 1);
+            const int at = id >= 0 ? total[id] + mine[id] + __popc(lower) : -1;
+            __syncwarp();
+            if (id >= 0 && lower == 0) mine[id] += __popc(same);
+            __syncwarp();
+            const long long slot = i + 32 * a + lane;
+            if (slot < last) slot_of[slot] = at;
+            if (id >= 0) {
+                const int t = (int)slot / top_k;
+                slot_token[at] = t;
+                if (slot_k) slot_k[at] = (int)slot - t * top_k;
+            }
         }
     }
     // rows that no slot takes
