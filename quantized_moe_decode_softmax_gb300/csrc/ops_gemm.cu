@@ -68,6 +68,7 @@ struct Tiling {
     int stage_bytes;
     int mblocks;    // blocks of kPair * kM output columns
     int bufs;       // accumulator sets in tensor memory, 1 or 2
+    bool paired;    // columns of out (and residual) come in aligned pairs
 };
 
 __device__ __forceinline__ unsigned long long globaltimer() {
@@ -512,17 +513,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine && p.bias) b0 = to_f32(static_cast<const T *>(p.bias)[(size_t)it.e * p.N + c]);
             if (MATS == 2 && mine && p.bias_up) b1 = to_f32(static_cast<const T *>(p.bias_up)[(size_t)it.e * p.N + c]);
             const int rows = mine ? it.rows : 0;  // rows this thread stores
-            const T *res = static_cast<const T *>(p.residual);
-            if (res) res += (size_t)it.r0 * p.ldr + c;
-            T *out = static_cast<T *>(p.out) + (size_t)it.r0 * p.ldo + c;
-            // a residual is read two chunks ahead, the first two before the tile is
-            // done; the values stay as loaded until they are used, so that nothing waits
-            // for them earlier
-            T ra[16], rb[16];
-            auto load_res = [&](T (&d)[16], int t0) {
+            // Two lanes that own neighbouring columns trade rows, so that each moves two
+            // columns of every other row in one 4-byte access: an access takes the same
+            // time whatever its width. g.paired: columns and addresses allow it.
+            const int odd = lane & 1;
+            const uint32_t trade = odd ? 0x3276u : 0x5410u;  // (theirs.hi, mine.hi) or (mine.lo, theirs.lo)
+            const size_t rstep = (g.paired ? 4 : 2) * p.ldr, ostep = (g.paired ? 4 : 2) * p.ldo;  // bytes
+            const char *res = static_cast<const char *>(p.residual);
+            char *out = static_cast<char *>(p.out);
+            const long long c_first = g.paired ? c - odd : c, r_first = it.r0 + (g.paired ? odd : 0);
+            if (res) res += 2 * (r_first * p.ldr + c_first);
+            out += 2 * (r_first * p.ldo + c_first);
+            // a residual is read two chunks ahead, the first two before the tile is done;
+            // the values stay as loaded until they are used, so that nothing waits for
+            // them earlier
+            uint32_t ra[16], rb[16];
+            auto load_res = [&](uint32_t (&d)[16], int t0) {
+                const char *s = res + 2 * (size_t)t0 * p.ldr;
+                if (g.paired) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (t0 + j < rows) d[j] = res[(size_t)(t0 + j) * p.ldr];
+                    for (int j = 0; j < 8; ++j, s += rstep)
+                        if (t0 + 2 * j + odd < rows) d[j] = *reinterpret_cast<const uint32_t *>(s);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, s += rstep)
+                        if (t0 + j < rows) d[j] = *reinterpret_cast<const uint16_t *>(s);
+                }
             };
             if (res) {
                 load_res(ra, 16 * part);
@@ -537,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 if (lane == 0) arrive_cluster(in_first(acc_empty_addr + 8 * buf));
             };
-            auto chunk = [&](int t0, T (&r)[16]) {
+            auto chunk = [&](int t0, uint32_t (&r)[16]) {
                 float v[16], u[MATS == 2 ? 16 : 1];
                 tmem_ld16(acc + t0, v);
                 if constexpr (MATS == 2) tmem_ld16(acc + g.tcap + t0, u);
@@ -556,20 +572,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                unary_act_all(p.act, v);
+                if (p.act != MOE_EPI_NONE) unary_act_all(p.act, v);
                 if constexpr (MATS == 2) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] *= u[j];
                 }
-                if (res) {
+                if (res) {  // (unset past the end of the tile, where nothing is stored)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] += to_f32(r[j]);  // unset past the end: not stored
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t w = g.paired ? __byte_perm(r[j], __shfl_xor_sync(0xffffffffu, r[j], 1), trade)
+                                                    : __byte_perm(r[2 * j], r[2 * j + 1], 0x5410u);
+                        const float2 f = unpack2<T>(w);
+                        v[2 * j] += f.x;
+                        v[2 * j + 1] += f.y;
+                    }
                     load_res(r, t0 + 64);
                 }
-                T *o = out + (size_t)t0 * p.ldo;
+                char *o = out + 2 * (size_t)t0 * p.ldo;
+                if (g.paired) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j, o += p.ldo)
-                    if (t0 + j < rows) *o = from_f32<T>(v[j]);
+                    for (int j = 0; j < 8; ++j, o += ostep) {
+                        const uint32_t w = pack2<T>(v[2 * j], v[2 * j + 1]);
+                        const uint32_t x = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), trade);
+                        if (t0 + 2 * j + odd < rows) *reinterpret_cast<uint32_t *>(o) = x;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, o += ostep)
+                        if (t0 + j < rows) *reinterpret_cast<T *>(o) = from_f32<T>(v[j]);
+                }
             };
 #pragma unroll 1
             for (int t0 = 16 * part; t0 < it.rows; t0 += 64) {
@@ -714,6 +745,8 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     g.stage_bytes = mats * kTileA + box_rows(g.tcap / kPair) * 128;
     g.bufs = 2 * mats * g.tcap <= kTmemCols ? 2 : 1;
     g.mblocks = mblocks;
+    auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
+    g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
     const int table = p.offsets ? p.E * 4 : 0;
     const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table;
     g.stages = min(kMaxStages, budget / g.stage_bytes);
