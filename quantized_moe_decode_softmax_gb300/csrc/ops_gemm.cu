@@ -5,29 +5,41 @@
 //
 // A pair of CTAs (one cluster, cta_group::2 MMAs) shares a tile. The tile is
 // transposed: the weights are the M operand (256 output columns, 128 per CTA, one
-// per tensor-memory lane) and the rows of x are the N operand, up to 256 of them
-// (128 for a gated product, which keeps two accumulators).
+// per tensor-memory lane) and the rows of x are the N operand, up to 256 of them.
 //   - N is any multiple of 32, so a ragged group wastes at most 31 rows of its
 //     tiles, where a 128-row M tile would waste up to 127: the groups of a prompt
 //     hold a few hundred rows each. A group is cut into equal tiles.
 //   - A thread of the epilogue owns one output column: its bias is a register,
-//     a warp's store of one row is 64 adjacent bytes, and neither odd sizes nor
-//     unaligned rows need another path. A gated product finds gate and up of an
-//     output in the same lane.
+//     and odd sizes need no other path. A gated product finds gate and up of an output
+//     in the same lane.
 //   - Each CTA of the pair loads its own weights and half of the rows; the MMA
-//     reads both halves. Per step of 64 inputs a CTA fetches 32 KB (gated: 40 KB)
-//     from L2 for 512 tensor-core cycles; alone it would fetch 48 KB, which the
-//     way from L2 to the SMs cannot sustain.
+//     reads both halves. Per step of 64 inputs at 256 rows a CTA fetches 32 KB from L2
+//     for 512 tensor-core cycles (gated: 48 KB for 1024). The way from L2 into an SM
+//     takes about 64 bytes a cycle: a CTA by itself would need 48 KB for 512 cycles.
+//   - Two accumulator sets fit tensor memory up to 256 rows (gated: 128), and the
+//     epilogue of a tile then runs beside the MMAs of the next. A gated product may
+//     still take tiles of 256 rows and one set: it gives the overlap away and halves
+//     the weights' traffic.
 //
 // Persistent pairs walk the work items (group, block of output columns, tile of
 // rows) in a fixed order. Warps 0..3 load, per step of 64 inputs, the weight
-// boxes and the rows of x (32-row boxes, or tile::gather4 through row_token, four
-// warps wide because a warp issues its copies one lane after the other) by TMA
+// boxes and the rows of x (boxes, or tile::gather4 through row_token) by TMA
 // with the 128-byte swizzle into a ring of stages. One warp of the first CTA issues
-// the MMAs for both. Eight warps run the epilogue of the previous tile meanwhile
-// (two accumulator sets in tensor memory). Inputs past K read as zeros in both
-// operands; rows past the group's end are computed and not stored, and since
+// the MMAs for both. Eight warps run the epilogue. Inputs past K read as zeros in
+// both operands; rows past the group's end are computed and not stored, and since
 // the rows of a product do not mix, what they hold (even NaN) does not matter.
+//
+// Bound: the tensor cores for long products, the weights' bytes for groups of few
+// rows. Measured (GB300, bf16, clocks as they come, 2.0 GHz at best):
+//   65536 x 4096 x 4096                          1146 us  1918 TFLOP/s
+//   8192 x 4096 x 4096                            145 us  1900 TFLOP/s (library 138)
+//   8192 x 4096 x 2 x 2048 gated, SiLU        148..167 us  1860..1650 TFLOP/s
+//   8192 tokens x 8 of 128 experts, 2048 -> 2 x 768, gathered  289 us  1427 TFLOP/s
+//   64 tokens x 8 of 128 experts, 768 -> 2048     64.6 us  6.2 TB/s
+// (The range is the clock under the power limit: short runs and long ones.)
+// Dealing each pair one contiguous run of rows, for an even end, was slower on the
+// grouped product (455 against 300 us): pairs then no longer share a weight block
+// while it is in L2.
 //
 // Every wait is bounded (1 s, reported through moe_ops_check); after one gives
 // up, all roles stop and the pair waits for its copies in flight before it ends.
@@ -50,7 +62,8 @@ constexpr int kTileA = kM * kK * 2;
 constexpr int kBoxRows = 64;       // rows of x per TMA box, or half as many for the last one
 constexpr int kStepRows = 32;      // rows per tile come in multiples of this
 constexpr int kMaxStages = 8;
-constexpr int kBand = 8;           // row tiles that share their pass over the weights
+constexpr int kBand = 8;           // row tiles that share their pass over the weights: 65536 x 4096 x 4096 takes
+                                   // 1146 us in bands of 8, 1421 us without (x is then read once per block)
 constexpr int kLoaders = 4;        // load warps
 constexpr int kEpilogue = 8;       // epilogue warps, two per quadrant of the tensor-memory lanes
 constexpr int kMmaWarp = kLoaders + kEpilogue;

@@ -13,6 +13,11 @@
 // inputs 8 t .. 8 t + 7 of a 32-input step from weight rows g and g + 8 and from
 // x row g, and feeds them to two MMAs four inputs at a time. The f32 partials of
 // the 8 warps are summed in warp order.
+//
+// Measured (GB300, bf16, us back to back in a graph): 2048x2048, one row 2.8; 4096x4096
+// 6.0 (5.6 TB/s); 4096x8192 13.6 (4.9 TB/s); 8 of 128 experts, gated 2048 -> 768, one
+// row each 11.2 (4.5 TB/s). Up to about 10 MB the time is launch, one load latency per
+// slice and the reduction; above, the weights' bytes.
 #include <atomic>
 
 #include "ops_common.cuh"
