@@ -53,10 +53,13 @@ def up_to_date() -> bool:
 
 
 def calls_path():
-    """Where the torch_calls module for the installed torch is built; None without torch."""
+    """Where the torch_calls module for the installed torch is built; None without a
+    torch that has CUDA."""
     try:
         import torch
     except ImportError:
+        return None
+    if torch.version.cuda is None:
         return None
     version = "".join(c if c.isalnum() else "_" for c in torch.__version__)
     return os.path.join(PKG, f"_torch_calls_{version}.so")

@@ -293,6 +293,7 @@ def moe_group_slots(topk_idx, E: int, experts: Optional[Tuple[int, int]] = None,
 def _slots(topk_idx, shape, E, lo, hi, st):
     n, k = shape
     dev = topk_idx.device
+    E, lo, hi = int(E), int(lo), int(hi)
     int32 = torch.int32
     # four allocations: views of one cost more time
     offsets = torch.empty(max(E, 0) + 1, dtype=int32, device=dev)

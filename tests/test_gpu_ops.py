@@ -99,12 +99,15 @@ def test_linear_keeps_nan_and_inf_to_their_rows_and_columns(n):
     ref.check(out[clean], r[clean], d[clean])
 
 
-def test_linear_extreme_values():
-    """The largest and smallest 16-bit values; f16 overflows to infinity as a cast does."""
-    x = torch.tensor([[3.0e38, 1e-38], [1e-20, 1e-20]], device="cuda").to(BF16).repeat(1, 4)
-    w = torch.eye(8, device="cuda").to(BF16)
-    assert torch.equal(q.moe_linear(x, q.LinearWeights(w)), x)
-    x = torch.full((40, 64), 60000.0, device="cuda").to(F16)
+@pytest.mark.parametrize("n", [2, 40, 100])
+def test_linear_extreme_values(n):
+    """The largest and smallest 16-bit values, subnormals among them, pass through an
+    identity product; f16 overflows to infinity as a cast does."""
+    for dtype, values in ((BF16, [3.0e38, 1e-38, 1e-40, -1e-20]), (F16, [65504.0, 6e-5, 6e-8, -1e-7])):
+        x = torch.tensor(values, device="cuda").to(dtype).repeat(n, 2)
+        assert bool((x != 0).all())
+        assert torch.equal(q.moe_linear(x, q.LinearWeights(torch.eye(8, device="cuda").to(dtype))), x)
+    x = torch.full((n, 64), 60000.0, device="cuda").to(F16)
     out = q.moe_linear(x, q.LinearWeights(torch.ones(16, 64, dtype=F16, device="cuda")))
     assert bool(torch.isinf(out).all())
 
