@@ -65,15 +65,17 @@ Product product_of(const moe_product *p) {
 //   4096x4096             32 rows 11.0 / 15.6   48 rows 16.5 / 14.8
 //   8192x4096             16 rows 14.6 / 17.6   24 rows 24.2 / 17.7
 //   768x2048 gated        32 rows  6.6 / 10.3   48 rows 11.1 / 10.3
-//   8 experts, 1024x1024  16 rows  7.0 / 8.0    24 rows  9.1 / 8.0
 //   8 of 128 experts, 768x2048 gated, one row each  11.9 / 16.4 (50 MB)
 //   6 of 256 experts, 2048x4096 gated, one row each 40.1 / 35.7 (201 MB)
+// Groups besides stream only up to 64 rows in all, because only the device knows how
+// they fall: 64 experts of 256x512, 64 rows 5.4 / 7.1 one on each and 11.5 / 6.8 all on
+// one; 256 rows 5.6 / 7.0 and 41.0 / 9.1.
 bool streams(const Product &a) {
     const int groups = a.offsets ? min(a.E, a.rows) : 1;
     const int mean = (a.rows + groups - 1) / groups;
     const double mb = 2e-6 * groups * a.N * (double)a.K * (a.w_up ? 2 : 1);
     const double work = mb * ((mean + 7) / 8);  // rows cost in blocks of 8
-    if (a.offsets) return mean <= 16 && work <= 60.0;
+    if (a.offsets) return a.rows <= 64 && work <= 60.0;
     return mean <= 32 ? work <= 150.0 : mean <= 64 && !a.w_up && work <= 70.0;
 }
 
