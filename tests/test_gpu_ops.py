@@ -147,6 +147,23 @@ def test_activations_over_the_whole_range(act, gated, n):
 
 
 @pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("n,N,K", [(70, 256, 4096), (100, 300, 1000), (128, 128, 8192), (257, 512, 2056), (300, 40, 16384),
+                                   (640, 768, 2048), (1500, 256, 8000)])
+def test_linear_long_inputs_and_few_tiles(n, N, K, dtype, gated):
+    """Fewer tiles than the GPU has SMs to run them, each over a long K."""
+    g = gen(n + K)
+    t = weights(g, (), N, K, dtype, gated, True)
+    x, res = normal(g, (n, K), 1.0, dtype), normal(g, (n, N), 1.0, dtype)
+    lw = q.LinearWeights(**t, activation="gelu")
+    out = q.moe_linear(x, lw, residual=res)
+    ref.check(out, *ref.product(x, act="gelu", residual=res, **t))
+    for _ in range(5):
+        assert torch.equal(q.moe_linear(x, lw, residual=res), out)
+    q.moe_ops_check()
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
 @pytest.mark.parametrize("n,N,K", [(100, 7, 8), (70, 1, 24), (333, 300, 16), (5000, 9, 72), (90, 2050, 1000)])
 def test_linear_thin_products(n, N, K, gated):
     """Many rows with a few columns or inputs, far below a tile."""
