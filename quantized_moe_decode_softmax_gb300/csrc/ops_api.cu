@@ -61,8 +61,8 @@ Product product_of(const moe_product *p) {
 // Which kernel. Streaming (ops_rows.cu) has the shorter way from launch to result,
 // tcgen05 (ops_gemm.cu) the higher rate once a product is long enough to fill it. By
 // the rows of a typical group and the bytes of weights read (us, streamed / tcgen05):
-//   2048x2048             64 rows  8.1 / 9.3    96 rows 11.2 / 9.4
-//   4096x4096             32 rows 11.0 / 15.6   48 rows 16.5 / 14.8
+//   2048x2048             48 rows  7.5 / 7.6    64 rows  8.1 / 7.6
+//   4096x4096             32 rows 11.0 / 13.7   48 rows 16.5 / 13.7
 //   8192x4096             16 rows 14.6 / 17.6   24 rows 24.2 / 17.7
 //   768x2048 gated        32 rows  6.6 / 10.3   48 rows 11.1 / 10.3
 //   8 of 128 experts, 768x2048 gated, one row each  11.9 / 16.4 (50 MB)
@@ -76,7 +76,7 @@ bool streams(const Product &a) {
     const double mb = 2e-6 * groups * a.N * (double)a.K * (a.w_up ? 2 : 1);
     const double work = mb * ((mean + 7) / 8);  // rows cost in blocks of 8
     if (a.offsets) return a.rows <= 64 && work <= 60.0;
-    return mean <= 32 ? work <= 150.0 : mean <= 64 && !a.w_up && work <= 70.0;
+    return mean <= 32 ? work <= 150.0 : mean <= 64 && !a.w_up && work <= 55.0;
 }
 
 moe_status run(const Product &a, cudaStream_t st) {
