@@ -143,9 +143,8 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     return try_wait(bar, parity) || wait_more(bar, parity, abort_flag);
 }
 
-// the same once the kernel is done with its work: no flag, no report
-__device__ __noinline__ void settle(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer();
+// the same at the end of a role: up to time t0 + kWaitNs, no flag, no report
+__device__ __noinline__ void settle(uint32_t bar, uint32_t parity, unsigned long long t0) {
     while (!try_wait(bar, parity) && globaltimer() - t0 < kWaitNs) {
     }
 }
@@ -475,11 +474,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        // every copy has landed before the pair may end (they have, unless a wait gave
-        // up): the stages before `at` were last filled in its lap, the others in the
-        // one before (a fresh barrier passes)
-        if ((warp == 0 || warp == 2) && rank == 0)
-            for (uint32_t i = 0; i < stages; ++i) settle(full_addr + 8 * i, i < at.s ? at.phase ^ 1 : at.phase);
+        // Before the pair may end, every copy has landed and every stage has been handed
+        // back (both have, or are about to, unless a wait gave up). The stages before
+        // `at` were last filled in its lap, the others in the one before; a fresh
+        // barrier passes.
+        if (warp == 0) {
+            const unsigned long long t0 = globaltimer();
+            for (uint32_t i = 0; i < stages; ++i) {
+                const uint32_t next = i < at.s ? at.phase ^ 1 : at.phase;  // the parity that its next fill would wait for
+                if (rank == 0) settle(full_addr + 8 * i, next, t0);
+                settle(empty_addr + 8 * i, next, t0);
+            }
+        }
         __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
         // ---- MMAs --------------------------------------------------------------
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
                 commit_pair(tc::smem_u32(&drain));
-                settle(tc::smem_u32(&drain), 0);
+                settle(tc::smem_u32(&drain), 0, globaltimer());
             }
         }
         __syncwarp();
@@ -783,7 +789,7 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     if (g.stages < 2) return cudaErrorNotSupported;
     const int smem = 1024 + g.stages * g.stage_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
-    if (most > 0x7fffffffLL) return cudaErrorNotSupported;
+    if (most > 0x3fffffffLL) return cudaErrorNotSupported;
     const int planes = p.stride_e ? p.E : 1;  // experts may share one matrix
     alignas(64) CUtensorMap tmx, tmx_half, tmw, tmu;
     if (!encode(&tmx, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||

@@ -28,6 +28,8 @@ struct Product {
 // A kernel launch that may begin before the stream's previous kernel has ended: the
 // kernel calls griddep_wait before its first access to global memory, so only its
 // start-up overlaps the other's end (about 1 us less between two small kernels).
+// What the other wrote must not be read through the non-coherent cache, which may
+// have been filled meanwhile: no __ldg and no __restrict__ inputs in these kernels.
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
                               A... args) {

@@ -41,10 +41,15 @@ __device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4
     ptx::mma_f16_16816(d, a, b0, b1);
 }
 
-// 16 bytes of a row's inputs k.., zeros from K on or for an absent row
+// 16 bytes of a row's inputs k.., zeros from K on or for an absent row. (volatile keeps
+// the loads of a slice together, ahead of the MMAs.)
 __device__ __forceinline__ uint4 load8(const void *row, int k, int K) {
     if (!row || k >= K) return make_uint4(0, 0, 0, 0);
-    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + 2 * (size_t)k));
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(static_cast<const char *>(row) + 2 * (size_t)k));
+    return v;
 }
 
 // the g-th group that holds rows, or -1 (one warp; E <= 1024)

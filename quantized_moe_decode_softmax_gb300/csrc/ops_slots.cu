@@ -36,9 +36,9 @@ constexpr int kCombineThreads = 128;
 constexpr int kAhead = 8;  // rounds whose ids are loaded together
 
 __global__ void __launch_bounds__(kThreads)
-    group_slots_kernel(const int *__restrict__ topk_idx, long long S, int top_k, int E, int e_lo, int e_hi,
-                       int *__restrict__ offsets, int *__restrict__ slot_token, int *__restrict__ slot_k,
-                       int *__restrict__ slot_of) {
+    group_slots_kernel(const int *topk_idx, long long S, int top_k, int E, int e_lo, int e_hi,
+                       int *offsets, int *slot_token, int *slot_k,
+                       int *slot_of) {
     extern __shared__ int sm[];
     int *cnt = sm;                 // [kWarps][E] counters, then the rows of the earlier warps per expert
     int *total = sm + kWarps * E;  // [E] this CTA's counts (read by the cluster), then its first rows
@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(kThreads)
 // (8 x 16 bytes in flight per thread); the sum keeps the order of the ranks.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_slots_kernel(const T *__restrict__ y, long long ldy, int rows, const int *__restrict__ slot_of,
-                         const float *__restrict__ topk_w, int n, int top_k, int N, const T *residual,
+    combine_slots_kernel(const T *y, long long ldy, int rows, const int *slot_of,
+                         const float *topk_w, int n, int top_k, int N, const T *residual,
                          long long ldr, T *out, long long ldo) {
     constexpr int V = VEC ? 8 : 1, R = 8;
     const int c = (blockIdx.x * kCombineThreads + threadIdx.x) * V;

@@ -537,6 +537,46 @@ def test_calls_with_and_without_the_torch_module(n, monkeypatch):
     assert list(refused()) == refusals and "nothing" not in refusals
 
 
+@pytest.mark.parametrize("n", [1, 8, 40, 130])
+def test_back_to_back_calls_see_each_other(n):
+    """A chain that reads what the call before has just written, in place and out of
+    place, the kernels overlapping at their ends: the same bits as with a wait after
+    every call."""
+    g = gen(n)
+    D, F, E, k = 512, 264, 8, 2
+    up, down = q.LinearWeights(normal(g, (F, D), D ** -0.5)), q.LinearWeights(normal(g, (D, F), F ** -0.5))
+    tg = q.LinearWeights(normal(g, (E, D, D), D ** -0.5), activation="silu")
+    start, ids = normal(g, (n, D)), [route(g, n, k, E) for _ in range(4)]
+
+    def chain(wait):
+        x, h = start.clone(), torch.empty((n, F), dtype=BF16, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(40):
+            calls = [lambda: q.moe_linear(x, up, out=h), lambda: q.moe_linear(h, down, residual=x, out=x)]
+            for c in calls:
+                c()
+                if wait:
+                    torch.cuda.synchronize()
+            idx, w = ids[i % 4]
+            s = q.moe_group_slots(idx, E)
+            if wait:
+                torch.cuda.synchronize()
+            y = q.moe_grouped_linear(x, tg, s.offsets, row_token=s.slot_token)
+            if wait:
+                torch.cuda.synchronize()
+            q.moe_combine_slots(y, s.slot_of, w, residual=x, out=x)
+            x.mul_(0.5)  # another library's kernel in between
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x
+
+    want = chain(True)
+    assert bool(torch.isfinite(want).all())
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
+
+
 def test_two_streams_at_once():
     """Independent calls that overlap on the device do not disturb one another."""
     g = gen(21)
