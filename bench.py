@@ -86,8 +86,8 @@ SEEDS = {"qwen3": 1, "e256": 3, "tiny": 0}
 # timed steps' mean unique-expert count (traffic grows with it).
 KERNEL_SOURCES = ("decode_step.cu", "ptx.cuh", "routing.cuh", "moe_internal.h")
 TRAFFIC = {
-    ("qwen3", 1): {"bytes": 21859328 + 0, "unique": 8, "src": "941f32f5a6607795"},
-    ("qwen3", 8): {"bytes": 138673920 + 2810624, "unique": 52, "src": "941f32f5a6607795"},
+    ("qwen3", 1): {"bytes": 21856768 + 0, "unique": 8, "src": "52d03b1766fea0d0"},
+    ("qwen3", 8): {"bytes": 138672128 + 2948352, "unique": 52, "src": "52d03b1766fea0d0"},
 }
 
 

@@ -382,7 +382,8 @@ __device__ __forceinline__ void warp_topk_tagged(const unsigned long long *lt, u
             }
         }
         if (__all_sync(0xffffffffu, need == 0u)) break;
-        if (*abort_flag || globaltimer() - t0 > kWaitNs) {
+        // one decision for the warp: the collectives below need all its lanes
+        if (__any_sync(0xffffffffu, *abort_flag || globaltimer() - t0 > kWaitNs)) {
             if (lane == 0) set_timeout(abort_flag, status);
             break;
         }
@@ -676,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_step_kernel(const __grid_c
                 for (int i = 0; i < 8; ++i)
                     if (((need >> i) & 1u) && (uint32_t)(ptx::ld_relaxed_gpu_u64(lt + lane + 32 * i) >> 32) == tag)
                         need &= ~(1u << i);
-                if (__all_sync(0xffffffffu, need == 0u) || *abort_flag || globaltimer() - t0 > kWaitNs) break;
+                if (__all_sync(0xffffffffu, need == 0u)) break;
+                if (__any_sync(0xffffffffu, *abort_flag || globaltimer() - t0 > kWaitNs)) break;
                 __nanosleep(200);
             }
             // gave up: report it now, so the token warps below stop at once
@@ -982,6 +984,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_step_kernel(const __grid_c
     const int r0 = 2 * g, r1 = 2 * g + 1;  // tile rows of MMA rows g and g + 8
     unsigned long long ta_wait = 0, ta_comp = 0, tb_wait = 0, tb_comp = 0;
     int slot = 0, par = 0;                 // ring position of the current stage
+    // A warp whose wait for a stage failed (timeout or abort) consumes no later
+    // stage either: a later lap's parity would read as landed on a barrier that is
+    // still in an earlier phase, and the releases would let the producer refill,
+    // and arm a second time, a stage whose copies are in flight.
+    bool alive = true;
 
     // ---- phase A: gate/up ---------------------------------------------------------
     // A warp owns at most one pair of input groups per K chunk, the same pair in
@@ -1014,7 +1021,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_step_kernel(const __grid_c
 #pragma unroll
         for (int kc = 0; kc < NKC; ++kc) {
             const unsigned long long tw0 = timing ? globaltimer() : 0ull;
-            const bool ok = __shfl_sync(0xffffffffu, (int)wait_phase(&S.full[slot], par, abort_flag, W.status), 0) != 0;
+            const bool ok = alive &&
+                __shfl_sync(0xffffffffu, (int)wait_phase(&S.full[slot], par, abort_flag, W.status), 0) != 0;
+            alive = ok;
             const unsigned long long tw1 = timing ? globaltimer() : 0ull;
             if (ok) {
                 if (pw[kc] >= 0) {
@@ -1165,7 +1174,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_step_kernel(const __grid_c
         const int jb = (st - nA) * L.P;
         const int nu = min(L.P, nU - jb);
         const unsigned long long tw0 = timing ? globaltimer() : 0ull;
-        const bool ok = __shfl_sync(0xffffffffu, (int)wait_phase(&S.full[slot], par, abort_flag, W.status), 0) != 0;
+        const bool ok = alive &&
+            __shfl_sync(0xffffffffu, (int)wait_phase(&S.full[slot], par, abort_flag, W.status), 0) != 0;
+        alive = ok;
         const unsigned long long tw1 = timing ? globaltimer() : 0ull;
         const unsigned char *buf = S.ring + (size_t)slot * L.stage_bytes;
         if (ok) {
