@@ -180,7 +180,8 @@ class LinearWeights:
 
 class SlotGroups(NamedTuple):
     """Rows grouped by expert (moe_group_slots): offsets [E + 1], slot_token and
-    slot_k [n * top_k], slot_of [n, top_k]; all int32 on the device."""
+    slot_k [n * top_k], slot_of [n, top_k]; all int32 on the device, and parts of
+    one allocation: they are not to be resized in place."""
     offsets: object
     slot_token: object
     slot_k: object
@@ -295,7 +296,7 @@ def _slots(topk_idx, shape, E, lo, hi, st):
     dev = topk_idx.device
     E, lo, hi = int(E), int(lo), int(hi)
     int32 = torch.int32
-    # four allocations: views of one cost more time
+    # four allocations: from Python, views of one cost more time
     offsets = torch.empty(max(E, 0) + 1, dtype=int32, device=dev)
     token = torch.empty(n * k, dtype=int32, device=dev)
     rank = torch.empty(n * k, dtype=int32, device=dev)

@@ -324,6 +324,23 @@ def test_group_slots(n, k, E, lo, hi):
         assert getattr(got, name).cpu().tolist() == w, name
 
 
+@pytest.mark.parametrize("n,k,E", [(1, 1, 1), (3, 3, 5), (8, 8, 128)])
+def test_group_slots_outputs_stand_alone(n, k, E):
+    """Each of the four tensors can be written, moved to another type and outlive
+    the others without a change in them; a call within inference mode gives the same."""
+    idx = torch.randint(0, E, (n, k), device="cuda", generator=gen(n)).to(torch.int32)
+    want = [t.tolist() for t in q.moe_group_slots(idx, E)]
+    with torch.inference_mode():
+        assert [t.tolist() for t in q.moe_group_slots(idx, E)] == want
+    for i in range(4):
+        got = list(q.moe_group_slots(idx, E))
+        got[i].fill_(-77)
+        assert [t.tolist() for j, t in enumerate(got) if j != i] == [w for j, w in enumerate(want) if j != i]
+        last, got = got[3 - i], None
+        other = torch.full((4096,), 5, dtype=torch.int32, device="cuda")  # may take freed memory
+        assert last.add(0).tolist() == want[3 - i] and last.is_contiguous() and int(other[0]) == 5
+
+
 def test_group_slots_without_ranks_and_long():
     """slot_k left out; a million slots, against a stable sort."""
     n, k, E = 131072, 8, 1000
