@@ -48,26 +48,37 @@ __device__ __forceinline__ float rcp_fast(float v) {
     return r;
 }
 
-// act(z), to about 2^-20 relative (the results are rounded to 16 bits). SiLU and the
-// tanh form of GELU are both z / (1 + exp(-a)): a = z, or twice the tanh's argument,
-// which also avoids the cancellation of 1 + tanh for negative z. With the bare
-// instructions this is 6 (9) operations; exp and the division cost the epilogue of
-// a gated product a third more time. The exact GELU is z erfc(-z / sqrt 2) / 2 with
-// erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + p x), x >= 0 (Abramowitz and
-// Stegun, formula 7.1.26: off by at most 1.5e-7): 15 operations; erff takes about 40.
+// act(z), with a bounded relative error over every z whose result a 16-bit type holds:
+//   SiLU       2^-19 + |z| 2^-23
+//   tanh GELU  2^-19 + |t| 2^-22, t = log2(e) times twice the tanh's argument
+//   GELU       2^-18 + z^2 2^-23
+// (the second terms are the rounding of the exponent; half a step of f16 is 2^-11).
+// SiLU and the tanh form of GELU are both z / (1 + 2^t), which also avoids the
+// cancellation of 1 + tanh for negative z. It is computed as z (k / (k + k 2^t)) with
+// k = 2^-16: the reciprocal of 1 + 2^t by itself would be flushed to zero from t = 126
+// on, where z 2^-t is still a normal bf16 number (SiLU below -87.3); with k that comes
+// after the smallest subnormal of bf16. The exact GELU is z Phi(z), with
+// Phi(-x) = exp(-x^2 / 2) t (a1 + t (a2 + ...)), t = 1 / (1 + p x), x >= 0: a minimax fit
+// of the relative error (1e-6) of exp(x^2 / 2) Phi(-x) over 0 <= x <= 14.5, so that the
+// tail keeps its digits; the exponential is the square of half its exponent's, again
+// for numbers below 2^-126. 6 (8, 17) operations; exp and the division cost the epilogue
+// of a gated product a third more time than the bare instructions, erff takes about 40.
 __device__ __forceinline__ float unary_act(int act, float z) {
     if (act == MOE_EPI_NONE) return z;
     constexpr float kLog2e = 1.4426950408889634f;
     if (act == MOE_EPI_GELU) {
-        const float x = fabsf(z) * 0.70710678118654752f, t = rcp_fast(1.0f + 0.3275911f * x);
-        const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-        const float c = 0.5f * poly * exp2_fast(-kLog2e * x * x);  // erfc(x) / 2
+        const float x = fabsf(z), t = rcp_fast(1.0f + 0.36f * x);
+        const float poly =
+            t * (0.14370854f + t * (0.14183695f + t * (0.1393632f + t * (0.027526388f + t * (0.17953743f +
+            t * (-0.17872778f + t * 0.04675479f))))));
+        const float h = exp2_fast((-0.25f * kLog2e) * x * x), c = poly * h * h;  // Phi(-x)
         return z * (z > 0.f ? 1.0f - c : c);
     }
     constexpr float kTwoC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float t = act == MOE_EPI_SILU ? -kLog2e * z
-                                        : z * (-kLog2e * kTwoC - kLog2e * kTwoC * 0.044715f * (z * z));
-    return z * rcp_fast(1.0f + exp2_fast(t));
+    const float t = act == MOE_EPI_SILU ? fmaf(-kLog2e, z, -16.0f)
+                                        : fmaf(z, fmaf(-kLog2e * kTwoC * 0.044715f, z * z, -kLog2e * kTwoC), -16.0f);
+    constexpr float k = 0x1p-16f;
+    return z * (rcp_fast(k + exp2_fast(t)) * k);
 }
 
 // the same on 16 values, branching once
