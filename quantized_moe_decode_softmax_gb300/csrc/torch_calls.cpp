@@ -13,6 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -29,13 +30,29 @@ decltype(&moe_combine_slots) fn_combine;
 
 PyObject *other() { Py_RETURN_NONE; }
 
+// whether autograd would have to record a call on this tensor, backwards or forwards
+bool differentiated(const at::Tensor &t) {
+    return (t.requires_grad() && c10::GradMode::is_enabled()) || t._fw_grad(0).defined();
+}
+
 // the tensor of a plain torch.Tensor argument (a null pointer for None), or false
 bool tensor(PyObject *o, const at::Tensor **t) {
     *t = nullptr;
     if (o == Py_None) return true;
     if (!THPVariable_CheckExact(o)) return false;
     *t = &THPVariable_Unpack(o);
-    return (*t)->defined() && (*t)->layout() == at::kStrided && !(*t)->requires_grad();
+    return (*t)->defined() && (*t)->layout() == at::kStrided && !differentiated(**t);
+}
+
+// whether a product's weights (w, w_up, bias, bias_up: tensors or None) can be used as they are
+bool weights(PyObject *o) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) return false;
+    for (int i = 0; i < 4; ++i) {
+        PyObject *w = PyTuple_GET_ITEM(o, i);
+        if (w == Py_None) continue;
+        if (!THPVariable_Check(w) || differentiated(THPVariable_Unpack(w))) return false;
+    }
+    return true;
 }
 
 // [n, cols] (n < 0: any) of type dt on CUDA device dev with adjacent columns
@@ -64,10 +81,10 @@ PyObject *result(moe_status st, const at::Tensor &out, PyObject *given) {
 
 at::ScalarType type_of(int dtype) { return dtype == MOE_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
 
-// linear(product address, device, x, residual, out)
+// linear(product address, device, x, residual, out, weights)
 PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 5) return other();
+    if (n_args != 6 || !weights(a[5])) return other();
     const auto *p = static_cast<const moe_product *>(PyLong_AsVoidPtr(a[0]));
     const int dev = (int)PyLong_AsLong(a[1]);
     const at::Tensor *x, *res, *given;
@@ -86,10 +103,10 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
-// grouped(product address, device, x, offsets, row_token, out)
+// grouped(product address, device, x, offsets, row_token, out, weights)
 PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 6) return other();
+    if (n_args != 7 || !weights(a[6])) return other();
     const auto *p = static_cast<const moe_product *>(PyLong_AsVoidPtr(a[0]));
     const int dev = (int)PyLong_AsLong(a[1]);
     const at::Tensor *x, *off, *token, *given;

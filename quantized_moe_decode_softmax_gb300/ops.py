@@ -4,7 +4,7 @@ moe_linear, moe_grouped_linear, moe_group_slots and moe_combine_slots keep the
 C names; LinearWeights holds the weights and the epilogue of a product. As in
 the rest of the binding nothing is computed here: the functions check the
 tensors, pass pointers and sizes to libmoe_decode.so, and turn status codes into
-MoeError. Inference only: no gradients are recorded.
+MoeError. Inference only: a call that autograd would have to record is refused.
 
 A usual call goes through the torch_calls module (csrc/torch_calls.cpp), which does
 the same checks in less time and returns None for whatever is not usual; the
@@ -188,9 +188,14 @@ class SlotGroups(NamedTuple):
     slot_of: object
 
 
-def _no_grad(x, residual=None):
-    if (x.requires_grad or (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
+def _no_grad(*tensors):
+    """Refuse a call that autograd would have to record: every floating-point input, the
+    weights and the output count."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise RuntimeError("an input requires a gradient: the operators record none (use torch.no_grad())")
+    fw = torch.autograd.forward_ad
+    if fw._current_level >= 0 and any(t is not None and fw.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError("an input carries a forward-mode tangent: the operators propagate none")
 
 
 def _raise(status: int, what: str):
@@ -200,12 +205,12 @@ def _raise(status: int, what: str):
 def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     """out [n, N] = epilogue(x [n, K]) (+ residual [n, N]); `out` may be `residual`."""
     if stream is None and _calls is not None and not weights.grouped:
-        r = _calls.linear(weights.ref, weights.device_index, x, residual, out)
+        r = _calls.linear(weights.ref, weights.device_index, x, residual, out, weights.tensors)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_linear")
     if weights.grouped:
         raise ValueError("moe_linear takes weights [N, K]; use moe_grouped_linear")
-    _no_grad(x, residual)
+    _no_grad(x, residual, out, *weights.tensors)
     dt, dev, N = weights.dtype, weights.device_index, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
     n = x.shape[0]
@@ -236,12 +241,12 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     expert e's matrix. x is [rows, K], or [tokens, K] with row_token [rows]. Rows
     outside every group are left as they were (unset in an `out` made here)."""
     if stream is None and _calls is not None and weights.grouped:
-        r = _calls.grouped(weights.ref, weights.device_index, x, offsets, row_token, out)
+        r = _calls.grouped(weights.ref, weights.device_index, x, offsets, row_token, out, weights.tensors)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_grouped_linear")
     if not weights.grouped:
         raise ValueError("moe_grouped_linear takes weights [E, N, K]; use moe_linear")
-    _no_grad(x)
+    _no_grad(x, out, *weights.tensors)
     dt, dev, N = weights.dtype, weights.device_index, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
     rows = x.shape[0]
@@ -318,7 +323,7 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
         r = _calls.combine(y, slot_of, topk_w, residual, out)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_combine_slots")
-    _no_grad(y, residual)
+    _no_grad(y, topk_w, residual, out)
     dt, dev = y.dtype, y.get_device()
     code = _dtype_code(dt)
     shape, ys = slot_of.shape, y.shape
