@@ -44,17 +44,6 @@ bool tensor(PyObject *o, const at::Tensor **t) {
     return (*t)->defined() && (*t)->layout() == at::kStrided && !differentiated(**t);
 }
 
-// whether a product's weights (w, w_up, bias, bias_up: tensors or None) can be used as they are
-bool weights(PyObject *o) {
-    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) return false;
-    for (int i = 0; i < 4; ++i) {
-        PyObject *w = PyTuple_GET_ITEM(o, i);
-        if (w == Py_None) continue;
-        if (!THPVariable_Check(w) || differentiated(THPVariable_Unpack(w))) return false;
-    }
-    return true;
-}
-
 // [n, cols] (n < 0: any) of type dt on CUDA device dev with adjacent columns
 bool rows(const at::Tensor &t, int64_t n, int64_t cols, at::ScalarType dt, int dev, int64_t *ld) {
     if (t.dim() != 2 || t.size(1) != cols || (n >= 0 && t.size(0) != n)) return false;
@@ -81,14 +70,46 @@ PyObject *result(moe_status st, const at::Tensor &out, PyObject *given) {
 
 at::ScalarType type_of(int dtype) { return dtype == MOE_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
 
+// Whether a product's weights (w, w_up, bias, bias_up: tensors or None) are still what
+// *p says of them: a tensor may have been given another storage, shape or device.
+bool weights(PyObject *o, const moe_product *p, int dev) {
+    if (!p || !PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) return false;
+    const void *at[4] = {p->w, p->w_up, p->bias, p->bias_up};
+    const at::ScalarType dt = type_of(p->dtype);
+    for (int i = 0; i < 4; ++i) {
+        PyObject *w = PyTuple_GET_ITEM(o, i);
+        if (w == Py_None) {
+            if (at[i]) return false;
+            continue;
+        }
+        if (!THPVariable_Check(w)) return false;
+        const at::Tensor &t = THPVariable_Unpack(w);
+        if (!t.defined() || t.layout() != at::kStrided || differentiated(t) || t.scalar_type() != dt || !t.is_cuda() ||
+            t.get_device() != dev || t.const_data_ptr() != at[i])
+            return false;
+        const int64_t d = t.dim();
+        if (i < 2) {
+            if ((d != 2 && d != 3) || t.size(d - 1) != p->K || t.size(d - 2) != p->N || (d == 3 ? t.size(0) : 1) != p->E)
+                return false;
+            if ((t.stride(d - 1) != 1 && p->K > 1) || (p->N > 1 && t.stride(d - 2) != p->ldw) ||
+                (p->E > 1 && t.stride(0) != p->stride_e))
+                return false;
+        } else if (t.numel() != (int64_t)p->E * p->N || !t.is_contiguous()) {
+            return false;
+        }
+    }
+    return true;
+}
+
 // linear(product address, device, x, residual, out, weights)
 PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 6 || !weights(a[5])) return other();
+    if (n_args != 6) return other();
     const auto *p = static_cast<const moe_product *>(PyLong_AsVoidPtr(a[0]));
     const int dev = (int)PyLong_AsLong(a[1]);
+    if (dev < 0 || !weights(a[5], p, dev)) return other();
     const at::Tensor *x, *res, *given;
-    if (!p || dev < 0 || !tensor(a[2], &x) || !x || !tensor(a[3], &res) || !tensor(a[4], &given)) return other();
+    if (!tensor(a[2], &x) || !x || !tensor(a[3], &res) || !tensor(a[4], &given)) return other();
     const at::ScalarType dt = type_of(p->dtype);
     int64_t ldx, ldr = 0, ldo = p->N;
     if (!rows(*x, -1, p->K, dt, dev, &ldx)) return other();
@@ -106,11 +127,12 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
 // grouped(product address, device, x, offsets, row_token, out, weights)
 PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 7 || !weights(a[6])) return other();
+    if (n_args != 7) return other();
     const auto *p = static_cast<const moe_product *>(PyLong_AsVoidPtr(a[0]));
     const int dev = (int)PyLong_AsLong(a[1]);
+    if (dev < 0 || !weights(a[6], p, dev)) return other();
     const at::Tensor *x, *off, *token, *given;
-    if (!p || dev < 0 || !tensor(a[2], &x) || !x || !tensor(a[3], &off) || !off || !tensor(a[4], &token) ||
+    if (!tensor(a[2], &x) || !x || !tensor(a[3], &off) || !off || !tensor(a[4], &token) ||
         !tensor(a[5], &given))
         return other();
     const at::ScalarType dt = type_of(p->dtype);

@@ -145,7 +145,9 @@ class LinearWeights:
     them). bias, bias_up: [N] or [E, N]. activation: "none", "silu", "gelu" or
     "gelu_tanh". act_limit: the clamp bound of a gated product, 0 for none.
 
-    The tensors are referenced, not copied."""
+    The tensors are referenced, not copied. One that is given another storage (`w.data =
+    other`, as offloading does) is followed: a call goes by the tensors as they are then.
+    Their shapes and type have to stay."""
 
     def __init__(self, w, w_up=None, bias=None, bias_up=None, activation: str = "none", act_limit: float = 0.0):
         _lib()
@@ -156,26 +158,51 @@ class LinearWeights:
         self.grouped = w.dim() == 3
         self.E = w.shape[0] if self.grouped else 1
         self.N, self.K = w.shape[-2], w.shape[-1]
-        self.dtype, self.device, self.device_index = w.dtype, w.device, w.get_device()
+        self.dtype = w.dtype
         self.tensors = (w, w_up, bias, bias_up)
         if self.E < 1 or self.N < 1 or self.K < 1:
             raise ValueError(f"w is empty: {tuple(w.shape)}")
+        self._epilogue = ACTIVATIONS[activation], float(act_limit)
+        self.c = moe_product()
+        self.ref = ctypes.addressof(self.c)
+        self._bind()
+
+    def _layout(self):
+        return [None if t is None else (t.data_ptr(), t.shape, t.stride(), t.dtype, t.device) for t in self.tensors]
+
+    def _bind(self):
+        """Check the tensors and write their addresses and strides into the struct."""
+        w, w_up, bias, bias_up = self.tensors
+        layout = self._layout()
+        lead = (self.E,) if self.grouped else ()
+        if tuple(w.shape) != lead + (self.N, self.K) or w.dtype != self.dtype:
+            raise ValueError(f"w has become {tuple(w.shape)} of {w.dtype}: it was {lead + (self.N, self.K)} of {self.dtype}")
         if w.stride(-1) != 1 and self.K > 1:
             raise ValueError("w: the inputs of a row have to be adjacent")
         if w_up is not None and (w_up.shape != w.shape or w_up.stride() != w.stride() or w_up.dtype != w.dtype
                                  or w_up.device != w.device):
             raise ValueError("w_up needs the shape, strides, type and device of w")
-        want = (self.E, self.N) if self.grouped else (self.N,)
+        want = lead + (self.N,)
         for name, b in (("bias", bias), ("bias_up", bias_up)):
             if b is not None and (tuple(b.shape) != want or b.dtype != w.dtype or b.device != w.device
                                   or not b.is_contiguous()):
                 raise ValueError(f"{name} has to be contiguous {want} of {w.dtype} on {w.device}")
         ptr = _abi._ptr
-        self.c = moe_product(_dtype_code(w.dtype), self.E, self.N, self.K, ptr(w), ptr(w_up),
-                             w.stride(-2) if self.N > 1 else self.K,
-                             w.stride(0) if self.grouped and self.E > 1 else 0, ptr(bias), ptr(bias_up),
-                             ACTIVATIONS[activation], float(act_limit))
-        self.ref = ctypes.addressof(self.c)
+        if w.is_cuda and not all(t is None or ptr(t) for t in self.tensors):
+            raise ValueError("the storage of a weight has been freed")
+        c = moe_product(_dtype_code(w.dtype), self.E, self.N, self.K, ptr(w), ptr(w_up),
+                        w.stride(-2) if self.N > 1 else self.K,
+                        w.stride(0) if self.grouped and self.E > 1 else 0, ptr(bias), ptr(bias_up), *self._epilogue)
+        # in one piece and in place: a call of another thread has read `ref`, or copies `c`
+        (ctypes.c_char * ctypes.sizeof(c)).from_buffer(self.c).raw = bytes(c)
+        self.device, self.device_index = w.device, w.get_device()
+        self._bound = layout
+
+    def current(self) -> moe_product:
+        """A copy of the struct that describes the tensors as they are now."""
+        if self._layout() != self._bound:
+            self._bind()
+        return moe_product.from_buffer_copy(self.c)
 
 
 class SlotGroups(NamedTuple):
@@ -211,6 +238,7 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     if weights.grouped:
         raise ValueError("moe_linear takes weights [N, K]; use moe_grouped_linear")
     _no_grad(x, residual, out, *weights.tensors)
+    c = weights.current()
     dt, dev, N = weights.dtype, weights.device_index, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
     n = x.shape[0]
@@ -220,16 +248,16 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
     if out is not None:
         ldo = _rows(out, "out", N, dt, dev, n)
     if _here(dev, stream):
-        return _linear(x, ldx, n, weights, residual, ldr, out, ldo, torch._C._cuda_getCurrentRawStream(dev))
+        return _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
-        return _linear(x, ldx, n, weights, residual, ldr, out, ldo, st)
+        return _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, st)
 
 
-def _linear(x, ldx, n, weights, residual, ldr, out, ldo, st):
+def _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, st):
     if out is None:
         out = torch.empty((n, weights.N), dtype=weights.dtype, device=weights.device)
     if n:
-        status = _c.moe_linear(weights.ref, x.data_ptr(), ldx, n, None if residual is None else residual.data_ptr(),
+        status = _c.moe_linear(ctypes.addressof(c), x.data_ptr(), ldx, n, None if residual is None else residual.data_ptr(),
                                ldr, out.data_ptr(), ldo, st)
         if status:
             _raise(status, "moe_linear")
@@ -247,6 +275,7 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     if not weights.grouped:
         raise ValueError("moe_grouped_linear takes weights [E, N, K]; use moe_linear")
     _no_grad(x, out, *weights.tensors)
+    c = weights.current()
     dt, dev, N = weights.dtype, weights.device_index, weights.N
     ldx = _rows(x, "x", weights.K, dt, dev)
     rows = x.shape[0]
@@ -258,17 +287,17 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     _ints(offsets, "offsets", (weights.E + 1,), dev)
     ldo = N if out is None else _rows(out, "out", N, dt, dev, rows)
     if _here(dev, stream):
-        return _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo,
+        return _grouped(c, x, ldx, rows, weights, offsets, row_token, out, ldo,
                         torch._C._cuda_getCurrentRawStream(dev))
     with _Elsewhere(dev, stream) as st:
-        return _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo, st)
+        return _grouped(c, x, ldx, rows, weights, offsets, row_token, out, ldo, st)
 
 
-def _grouped(x, ldx, rows, weights, offsets, row_token, out, ldo, st):
+def _grouped(c, x, ldx, rows, weights, offsets, row_token, out, ldo, st):
     if out is None:
         out = torch.empty((rows, weights.N), dtype=weights.dtype, device=weights.device)
     if rows:
-        status = _c.moe_grouped_linear(weights.ref, offsets.data_ptr(),
+        status = _c.moe_grouped_linear(ctypes.addressof(c), offsets.data_ptr(),
                                        None if row_token is None else row_token.data_ptr(), x.data_ptr(), ldx,
                                        x.shape[0], rows, out.data_ptr(), ldo, st)
         if status:
