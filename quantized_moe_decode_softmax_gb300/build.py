@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -53,16 +54,16 @@ def up_to_date() -> bool:
 
 
 def calls_path():
-    """Where the torch_calls module for the installed torch is built; None without a
-    torch that has CUDA."""
+    """Where the torch_calls module for this interpreter and the installed torch is built
+    (it is tied to both); None without a torch that has CUDA."""
     try:
         import torch
-    except ImportError:
+    except (ImportError, OSError):
         return None
     if torch.version.cuda is None:
         return None
     version = "".join(c if c.isalnum() else "_" for c in torch.__version__)
-    return os.path.join(PKG, f"_torch_calls_{version}.so")
+    return os.path.join(PKG, f"_torch_calls_{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_calls(force: bool = False):
@@ -74,8 +75,6 @@ def build_calls(force: bool = False):
     deps = [src, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
         return path
-    import sysconfig
-
     import torch
     base = os.path.dirname(os.path.abspath(torch.__file__))
     inc = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),

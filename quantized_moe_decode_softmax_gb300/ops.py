@@ -16,6 +16,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from typing import NamedTuple, Optional, Tuple
 
 from . import _abi, build
@@ -56,10 +57,14 @@ def _bind():
     path = build.calls_path()
     if path is not None and os.path.exists(path):
         loader = importlib.machinery.ExtensionFileLoader("_torch_calls", path)
-        m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_torch_calls", path, loader=loader))
-        m.bind(*[ctypes.cast(getattr(L, f), vp).value for f in
-                 ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots")])
-        _calls = m
+        try:
+            m = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_torch_calls", path, loader=loader))
+            m.bind(*[ctypes.cast(getattr(L, f), vp).value for f in
+                     ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots")])
+            _calls = m
+        except (ImportError, OSError) as e:  # every call has its way through ctypes
+            warnings.warn(f"{path} cannot be loaded ({e}): calls of the operators go through ctypes")
     _c = L
     return L
 
