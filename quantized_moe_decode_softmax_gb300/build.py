@@ -15,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -35,6 +36,15 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _cuda_include() -> str:
+    """The CUDA headers: nvcc's, or where the toolkit usually is."""
+    try:
+        home = os.path.dirname(os.path.dirname(_nvcc()))
+    except RuntimeError:
+        home = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return os.path.join(home, "include")
 
 
 def _sources():
@@ -67,7 +77,8 @@ def calls_path():
 
 
 def build_calls(force: bool = False):
-    """Compile torch_calls.cpp with the host compiler; returns its path or None."""
+    """Compile torch_calls.cpp with the host compiler; returns its path, or None where that
+    is not possible (no C++ compiler, no Python headers): calls then go through ctypes."""
     path = calls_path()
     if path is None:
         return None
@@ -78,14 +89,21 @@ def build_calls(force: bool = False):
     import torch
     base = os.path.dirname(os.path.abspath(torch.__file__))
     inc = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+           sysconfig.get_paths()["include"], _cuda_include()]
     tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{d}" for d in inc],
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.returncode and f"{cmd[0]} failed:\n{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        why = str(e)
+    if why:
+        if os.path.exists(path):  # of older sources
+            os.remove(path)
+        warnings.warn(f"{src} is not built, calls of the operators go through ctypes: {why}")
+        return None
     os.replace(tmp, path)
     return path
 
