@@ -8,7 +8,7 @@ from typing import Any, Optional
 import numpy as np
 
 from . import _abi
-from .ops import LinearWeights, moe_combine_slots, moe_group_slots, moe_grouped_linear, moe_linear
+from .ops import LinearWeights, moe_combine_slots, moe_group_slots, moe_grouped_linear, moe_linear, moe_ops_check
 
 _DT = {"f32": _abi.MOE_DTYPE_F32, "bf16": _abi.MOE_DTYPE_BF16}
 
@@ -76,6 +76,7 @@ class MoeDecodeLayer:
         self.act_dtype = act_dtype
         self.out_dtype = out_dtype or act_dtype
         self.plan = _abi.moe_plan_create(self.cfg)
+        self._shared_stream = None  # of the last step with a shared expert
 
     def _out_torch_dtype(self):
         import torch
@@ -93,6 +94,7 @@ class MoeDecodeLayer:
         _abi.moe_decode_forward(self.plan, x, w.router_w, w.router_bias, w.c_planes, n,
                                 self.cfg.top_k, out, stream)
         if shared is not None:
+            self._shared_stream = torch.cuda.current_stream() if stream is None else stream
             shared.forward(x, residual=out, out=out, stream=stream)
         return out
 
@@ -114,7 +116,11 @@ class MoeDecodeLayer:
         return _abi.moe_get_routing(self.plan, n_tokens, self.cfg.E, self.cfg.top_k)
 
     def check(self):
+        """Raise MoeError for a device-side wait that gave up: of the plan's steps, and of
+        the shared experts that ran beside them."""
         _abi.moe_plan_check(self.plan)
+        if self._shared_stream is not None:
+            moe_ops_check(self._shared_stream)
 
     def close(self):
         if getattr(self, "plan", None):
@@ -144,6 +150,10 @@ class SharedExpert:
         h = moe_linear(x, self.gate_up, stream=stream)
         return moe_linear(h, self.down, residual=residual, out=out, stream=stream)
 
+    def check(self, stream=None):
+        """moe_ops_check: raise MoeError for a device-side wait that gave up."""
+        moe_ops_check(stream)
+
 
 class RoutedExperts:
     """Experts with 16-bit weights under any router: gate, up [E, F, D], down
@@ -164,3 +174,7 @@ class RoutedExperts:
         h = moe_grouped_linear(x, self.gate_up, g.offsets, row_token=g.slot_token, stream=stream)
         y = moe_grouped_linear(h, self.down, g.offsets, stream=stream)
         return moe_combine_slots(y, g.slot_of, topk_w, residual=residual, out=out, stream=stream)
+
+    def check(self, stream=None):
+        """moe_ops_check: raise MoeError for a device-side wait that gave up."""
+        moe_ops_check(stream)

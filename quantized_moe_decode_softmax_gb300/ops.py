@@ -397,5 +397,10 @@ def _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st):
 
 def moe_ops_check(stream=None) -> None:
     """Synchronise `stream` (the current one by default) and raise MoeError for a
-    device-side wait of these operators that gave up since the last check."""
-    _abi._check(_lib().moe_ops_check(_abi._stream(stream)), "moe_ops_check")
+    device-side wait of these operators on its device (a stream given as a number: on the
+    current device) that gave up since the last check, on any stream."""
+    lib = _lib()
+    if stream is None or isinstance(stream, int):
+        return _abi._check(lib.moe_ops_check(_abi._stream(stream)), "moe_ops_check")
+    with torch.cuda.device(stream.device):
+        _abi._check(lib.moe_ops_check(stream.cuda_stream), "moe_ops_check")
