@@ -170,6 +170,8 @@ class RoutedExperts:
 
     def forward(self, x, topk_idx, topk_w, residual=None, out=None, stream=None):
         """x [n, D], topk_idx [n, k] int32, topk_w [n, k] float32 -> [n, D]."""
+        if x.dim() != 2 or topk_idx.dim() != 2 or x.shape[0] != topk_idx.shape[0]:
+            raise ValueError(f"x {tuple(x.shape)} and topk_idx {tuple(topk_idx.shape)} have to be [n, D] and [n, k]")
         g = moe_group_slots(topk_idx, self.gate_up.E, experts=self.experts, stream=stream)
         h = moe_grouped_linear(x, self.gate_up, g.offsets, row_token=g.slot_token, stream=stream)
         y = moe_grouped_linear(h, self.down, g.offsets, stream=stream)

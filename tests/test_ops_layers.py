@@ -65,6 +65,19 @@ def test_experts_have_a_check(monkeypatch):
             e.check(stream=5)
 
 
+def test_routed_experts_refuse_ids_of_other_tokens(monkeypatch):
+    """One row of ids per token: ids of more tokens would be read as ids of the last one."""
+    ops._lib()
+    g, d = torch.zeros(3, 16, 24, dtype=BF16), torch.zeros(3, 24, 16, dtype=BF16)
+    e = q.RoutedExperts(g, g, d)
+    monkeypatch.setattr(layer, "moe_group_slots", lambda *a, **k: pytest.fail("launched"))
+    ids = lambda n: torch.zeros(n, 2, dtype=torch.int32)  # noqa: E731
+    for x, idx in ((torch.zeros(4, 24, dtype=BF16), ids(5)), (torch.zeros(4, 24, dtype=BF16), ids(3)),
+                   (torch.zeros(24, dtype=BF16), ids(1)), (torch.zeros(4, 24, dtype=BF16), ids(4)[:, 0])):
+        with pytest.raises(ValueError, match="topk_idx"):
+            e.forward(x, idx, torch.zeros(idx.shape))
+
+
 @pytest.mark.gpu
 def test_checks_on_the_gpu(monkeypatch):
     """The same on a device and a stream: nothing to report, then a status from a fake of
