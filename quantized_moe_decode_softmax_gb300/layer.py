@@ -89,6 +89,8 @@ class MoeDecodeLayer:
         n = x.shape[0]
         if shared is not None and {x.dtype, out.dtype if out is not None else self._out_torch_dtype()} != {shared.dtype}:
             raise TypeError(f"the shared expert is {shared.dtype}: x and the step's output have to be, too")
+        if shared is not None and shared.down.N != w.D:
+            raise ValueError(f"the shared expert is {shared.down.N} wide, the step {w.D}")
         if out is None:
             out = torch.empty((n, w.D), dtype=self._out_torch_dtype(), device=x.device)
         _abi.moe_decode_forward(self.plan, x, w.router_w, w.router_bias, w.c_planes, n,

@@ -22,6 +22,9 @@ class FakeLib:
 class FakeShared:
     dtype = BF16
 
+    class down:
+        N = 512
+
     def forward(self, x, residual, out, stream):
         return out.add_(1)
 
@@ -63,6 +66,18 @@ def test_experts_have_a_check(monkeypatch):
         e.check(stream=5)
         with pytest.raises(q.MoeError):
             e.check(stream=5)
+
+
+def test_shared_expert_of_another_width_is_refused_before_the_step(monkeypatch):
+    ops._lib()
+    lay = step_layer(monkeypatch)
+    weights = layer.DeviceLayer.__new__(layer.DeviceLayer)
+    weights.D, weights.router_w, weights.router_bias, weights.c_planes = 512, None, None, None
+    monkeypatch.setattr(_abi, "moe_decode_forward", lambda *a: pytest.fail("launched"))
+    g, d = torch.zeros(16, 256, dtype=BF16), torch.zeros(256, 16, dtype=BF16)
+    x, out = torch.zeros(2, 512, dtype=BF16), torch.zeros(2, 512, dtype=BF16)
+    with pytest.raises(ValueError, match="wide"):
+        lay.forward(x, weights, out=out, stream=77, shared=q.SharedExpert(g, g, d))
 
 
 def test_routed_experts_refuse_ids_of_other_tokens(monkeypatch):
