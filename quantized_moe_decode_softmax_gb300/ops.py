@@ -6,6 +6,10 @@ the rest of the binding nothing is computed here: the functions check the
 tensors, pass pointers and sizes to libmoe_decode.so, and turn status codes into
 MoeError. Inference only: a call that autograd would have to record is refused.
 
+`stream` is the stream that a call runs on (a torch stream, or a cudaStream_t as a
+number), the current one by default. As everywhere in torch, another stream waits for
+nothing by itself: what wrote the inputs is the caller's to order before it.
+
 A usual call goes through the torch_calls module (csrc/torch_calls.cpp), which does
 the same checks in less time and returns None for whatever is not usual; the
 functions here then take over, with their messages.
@@ -112,15 +116,22 @@ def _ints(t, what: str, shape, device):
 class _Elsewhere:
     """The device (by its number) and stream of a call that names a stream or whose
     tensors are not on the current device: outputs are allocated there, kernels go
-    there."""
+    there. The tensors of the call are recorded on a named stream, so that memory that the
+    caller lets go of right afterwards is not given out again before the call has run
+    there. (Not on a stream that torch does not own: it may be destroyed first. Its
+    caller keeps the tensors.)"""
 
-    def __init__(self, device: int, stream):
+    def __init__(self, device: int, stream, tensors=()):
         if device < 0:
             raise ValueError("tensors have to be on a CUDA device")
         self._device = device
         self._on_device = torch.cuda.device(device)
+        self._recorded = ()
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        elif stream is not None and not isinstance(stream, torch.cuda.ExternalStream):
+            self._recorded = tensors
+        self._stream = stream
         self._on_stream = None if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
@@ -130,6 +141,9 @@ class _Elsewhere:
         return torch.cuda.current_stream(self._device).cuda_stream
 
     def __exit__(self, *exc):
+        for t in self._recorded:
+            if t is not None:
+                t.record_stream(self._stream)
         if self._on_stream is not None:
             self._on_stream.__exit__(*exc)
         self._on_device.__exit__(*exc)
@@ -254,7 +268,7 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
         ldo = _rows(out, "out", N, dt, dev, n)
     if _here(dev, stream):
         return _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, torch._C._cuda_getCurrentRawStream(dev))
-    with _Elsewhere(dev, stream) as st:
+    with _Elsewhere(dev, stream, (x, residual, out, *weights.tensors)) as st:
         return _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, st)
 
 
@@ -294,7 +308,7 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
     if _here(dev, stream):
         return _grouped(c, x, ldx, rows, weights, offsets, row_token, out, ldo,
                         torch._C._cuda_getCurrentRawStream(dev))
-    with _Elsewhere(dev, stream) as st:
+    with _Elsewhere(dev, stream, (x, offsets, row_token, out, *weights.tensors)) as st:
         return _grouped(c, x, ldx, rows, weights, offsets, row_token, out, ldo, st)
 
 
@@ -326,7 +340,7 @@ def moe_group_slots(topk_idx, E: int, experts: Optional[Tuple[int, int]] = None,
     _ints(topk_idx, "topk_idx", shape, dev)
     if _here(dev, stream):
         return _slots(topk_idx, shape, E, lo, hi, torch._C._cuda_getCurrentRawStream(dev))
-    with _Elsewhere(dev, stream) as st:
+    with _Elsewhere(dev, stream, (topk_idx,)) as st:
         return _slots(topk_idx, shape, E, lo, hi, st)
 
 
@@ -377,7 +391,7 @@ def moe_combine_slots(y, slot_of, topk_w, residual=None, out=None, stream=None):
     if _here(dev, stream):
         return _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo,
                         torch._C._cuda_getCurrentRawStream(dev))
-    with _Elsewhere(dev, stream) as st:
+    with _Elsewhere(dev, stream, (y, slot_of, topk_w, residual, out)) as st:
         return _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st)
 
 

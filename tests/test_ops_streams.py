@@ -1,0 +1,46 @@
+"""Calls of the operators on another stream than the tensors' own."""
+import pytest
+import torch
+
+import quantized_moe_decode_softmax_gb300 as q
+
+BF16 = torch.bfloat16
+
+
+def operands(op, g):
+    """The tensors of a call, none of which anything else holds, and the call."""
+    n, N, K, E, k = 256, 512, 256, 8, 2
+    t = lambda *s: torch.empty(s, dtype=BF16, device="cuda").normal_(generator=g)  # noqa: E731
+    idx = torch.randint(0, E, (n, k), device="cuda", generator=g).to(torch.int32)
+    if op == "linear":
+        return [t(n, K), t(N, K), t(n, N)], lambda a, st: q.moe_linear(a[0], q.LinearWeights(a[1]), residual=a[2], stream=st)
+    if op == "grouped":
+        s = q.moe_group_slots(idx, E)
+        return ([t(n, K), t(E, N, K), s.offsets.clone(), s.slot_token.clone()],
+                lambda a, st: q.moe_grouped_linear(a[0], q.LinearWeights(a[1]), a[2], row_token=a[3], stream=st))
+    if op == "slots":
+        return [idx], lambda a, st: q.moe_group_slots(a[0], E, stream=st).slot_of
+    of = torch.arange(n * k, dtype=torch.int32, device="cuda").reshape(n, k)
+    return [t(n * k, N), of, torch.rand(n, k, device="cuda", generator=g)], \
+        lambda a, st: q.moe_combine_slots(a[0], a[1], a[2], stream=st)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", ["linear", "grouped", "slots", "combine"])
+def test_memory_let_go_of_after_the_call_is_not_reused_before_it_ran(op):
+    """The inputs of a call on a busy side stream are dropped right after it, and their
+    memory asked for again and overwritten at once from the current stream."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tensors, call = operands(op, g)
+    want = call(tensors, None).clone()
+    shapes = [(t.shape, t.dtype) for t in tensors]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # about 50 ms: the call below waits behind it
+    got = call(tensors, side)
+    del tensors
+    again = [torch.zeros(s, dtype=d, device="cuda") for s, d in shapes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del again
