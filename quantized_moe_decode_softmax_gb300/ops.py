@@ -129,8 +129,11 @@ class _Elsewhere:
         self._recorded = ()
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
-        elif stream is not None and not isinstance(stream, torch.cuda.ExternalStream):
-            self._recorded = tensors
+        elif stream is not None:
+            if stream.device.index != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on CUDA device {device}")
+            if not isinstance(stream, torch.cuda.ExternalStream):
+                self._recorded = tensors
         self._stream = stream
         self._on_stream = None if stream is None else torch.cuda.stream(stream)
 

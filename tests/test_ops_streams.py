@@ -1,10 +1,19 @@
 """Calls of the operators on another stream than the tensors' own."""
+import types
+
 import pytest
 import torch
 
 import quantized_moe_decode_softmax_gb300 as q
+from quantized_moe_decode_softmax_gb300 import ops
 
 BF16 = torch.bfloat16
+
+
+def test_a_stream_of_another_device_is_refused():
+    ops._lib()
+    with pytest.raises(ValueError, match="cuda:1"):
+        ops._Elsewhere(0, types.SimpleNamespace(device=torch.device("cuda:1")))
 
 
 def operands(op, g):
