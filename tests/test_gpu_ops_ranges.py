@@ -6,6 +6,7 @@ import torch
 
 import ops_reference as ref
 import quantized_moe_decode_softmax_gb300 as q
+from test_gpu_ops import check_grouped, combine_ref, gen, normal, offsets_of, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +65,66 @@ def test_activations_keep_their_relative_error(act, dtype, up, n):
     assert torch.equal(out[over].double(), r[over].sign() * math.inf)
     # below 2^-135, half the smallest subnormal of bf16, the activation may be zero
     ref.check(out[~over], r[~over], (r.abs() * relative_error(act, d) + 2.0 ** -135 * (up or 1.0))[~over])
+
+
+def many(E, sizes):
+    """Rows per expert: `sizes` in turn at both ends and around every 416th expert (the
+    tcgen05 products number their work for so many experts at a time), none elsewhere."""
+    counts, at = [0] * E, 0
+    for e in sorted({e for b in range(0, E + 1, 416) for e in range(b - 2, b + 2) if e != b - 1} | {7, E // 2, E - 1}):
+        if 0 <= e < E:
+            counts[e] = sizes[at % len(sizes)]
+            at += 1
+    return counts
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gather"])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("sizes", [(1, 2, 3), (40, 1, 150, 9)], ids=["streamed", "tcgen05"])
+@pytest.mark.parametrize("E", [415, 416, 417, 832, 833, 1024])
+def test_grouped_over_many_experts(E, sizes, gated, gather):
+    counts = many(E, sizes)
+    rows, (N, K) = sum(counts), (40, 72)
+    assert (rows <= 64) == (sizes[0] == 1)
+    g = gen(E + gated)
+    t = weights(g, (E,), N, K, BF16, gated, True)
+    x = normal(g, (rows, K))
+    token = torch.randperm(rows, device="cuda", generator=g).to(torch.int32) if gather else None
+    out = q.moe_grouped_linear(x, q.LinearWeights(**t, activation="silu"), offsets_of(counts), row_token=token)
+    check_grouped(x, t, counts, "silu", out, token)
+    q.moe_ops_check()
+
+
+@pytest.mark.parametrize("n", [5, 300])
+def test_grouped_with_every_expert_in_use(n):
+    """1024 experts that all hold rows, or nearly all, in the order that the grouping gives."""
+    E, k, N, K = 1024, 8, 24, 64
+    g = gen(n)
+    idx = torch.randint(0, E, (n, k), device="cuda", generator=g).to(torch.int32)
+    t = weights(g, (E,), N, K, F16, False, False)
+    x = normal(g, (n, K), 1.0, F16)
+    s = q.moe_group_slots(idx, E)
+    counts = torch.bincount(idx.reshape(-1).long(), minlength=E).tolist()
+    check_grouped(x, t, counts, "none", q.moe_grouped_linear(x, q.LinearWeights(**t), s.offsets, row_token=s.slot_token),
+                  s.slot_token)
+
+
+# the widest, the longest and the most rows, through both kernels
+@pytest.mark.parametrize("n,N,K", [(1, 150001, 512), (66, 150001, 64), (1, 1 << 20, 8), (66, 1 << 20, 8), (3, 24, 65536),
+                                   (70, 24, 65536), (100000, 16, 16), (70001, 7, 8)])
+def test_linear_far_sizes(n, N, K):
+    g = gen(n + N)
+    t = weights(g, (), N, K, BF16, False, True)
+    x = normal(g, (n, K))
+    ref.check(q.moe_linear(x, q.LinearWeights(**t)), *ref.product(x, **t))
+
+
+@pytest.mark.parametrize("N", [8, 5])
+def test_combine_more_tokens_than_a_grid_has_rows(N):
+    n, k = 70001, 2
+    g = gen(N)
+    y = normal(g, (n, N))
+    of = torch.randint(-1, n, (n, k), device="cuda", generator=g).to(torch.int32)
+    w = torch.rand((n, k), device="cuda", generator=g)
+    res = normal(g, (n, N))
+    ref.check(q.moe_combine_slots(y, of, w, residual=res), *combine_ref(y, of, w, res))
