@@ -789,7 +789,10 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st) {
     if (g.stages < 2) return cudaErrorNotSupported;
     const int smem = 1024 + g.stages * g.stage_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
-    if (most > 0x3fffffffLL) return cudaErrorNotSupported;
+    // items are numbered in 32 bits, also where offsets that do not ascend give every
+    // expert all rows
+    if ((p.offsets ? p.E : 1) * ((p.rows + g.tcap - 1) / g.tcap) * (long long)mblocks > 0x7fff0000LL)
+        return cudaErrorNotSupported;
     const int planes = p.stride_e ? p.E : 1;  // experts may share one matrix
     alignas(64) CUtensorMap tmx, tmx_half, tmw, tmu;
     if (!encode(&tmx, p.dtype, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||
