@@ -58,10 +58,12 @@ bool dense(const at::Tensor &t, at::ScalarType dt, int dev) {
     return t.scalar_type() == dt && t.is_cuda() && t.get_device() == dev && t.is_contiguous();
 }
 
-// the result of a call: the tensor, or the status as a number
+// the result of a call: the tensor, or the status as a number. (An output that was given
+// counts as written, for whoever keeps it for a backward pass.)
 PyObject *result(moe_status st, const at::Tensor &out, PyObject *given) {
     if (st != MOE_OK) return PyLong_FromLong(st);
     if (given != Py_None) {
+        if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
         Py_INCREF(given);
         return given;
     }

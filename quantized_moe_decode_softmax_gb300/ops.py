@@ -275,9 +275,17 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
         return _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, st)
 
 
+def _written(out):
+    """An output that was given counts as written, for whoever keeps it for a backward pass."""
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+
+
 def _linear(c, x, ldx, n, weights, residual, ldr, out, ldo, st):
     if out is None:
         out = torch.empty((n, weights.N), dtype=weights.dtype, device=weights.device)
+    else:
+        _written(out)
     if n:
         status = _c.moe_linear(ctypes.addressof(c), x.data_ptr(), ldx, n, None if residual is None else residual.data_ptr(),
                                ldr, out.data_ptr(), ldo, st)
@@ -318,6 +326,8 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
 def _grouped(c, x, ldx, rows, weights, offsets, row_token, out, ldo, st):
     if out is None:
         out = torch.empty((rows, weights.N), dtype=weights.dtype, device=weights.device)
+    else:
+        _written(out)
     if rows:
         status = _c.moe_grouped_linear(ctypes.addressof(c), offsets.data_ptr(),
                                        None if row_token is None else row_token.data_ptr(), x.data_ptr(), ldx,
@@ -403,6 +413,8 @@ def _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st):
     rows, N = y.shape
     if out is None:
         out = torch.empty((n, N), dtype=y.dtype, device=y.device)
+    else:
+        _written(out)
     if n:
         status = _c.moe_combine_slots(code, y.data_ptr() or None, ldy, rows, slot_of.data_ptr(), topk_w.data_ptr(), n,
                                       k, N, None if residual is None else residual.data_ptr(), ldr, out.data_ptr(),

@@ -53,3 +53,29 @@ def test_memory_let_go_of_after_the_call_is_not_reused_before_it_ran(op):
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     del again
+
+
+@pytest.mark.gpu
+def test_an_output_counts_as_written():
+    """Autograd notices that a buffer which it keeps for a backward pass was the output of
+    a call, as after an in-place operation of torch, with and without the module."""
+    t = lambda *s: torch.ones(s, dtype=BF16, device="cuda")  # noqa: E731
+    lw, lg, off = q.LinearWeights(t(16, 24)), q.LinearWeights(t(1, 16, 24)), torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    of, w = torch.zeros(4, 1, dtype=torch.int32, device="cuda"), torch.ones(4, 1, device="cuda")
+    keep = q.ops._calls
+    try:
+        for module in (keep, None):
+            q.ops._calls = module
+            for call in (lambda o: q.moe_linear(t(4, 24), lw, out=o), lambda o: q.moe_grouped_linear(t(4, 24), lg, off, out=o),
+                         lambda o: q.moe_combine_slots(t(4, 16), of, w, out=o)):
+                p, out = torch.nn.Parameter(t(16)), t(4, 16)
+                loss = (p * out).sum()
+                call(out)
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    loss.backward()
+                with torch.inference_mode():
+                    inner = t(4, 16)
+                    call(inner)
+                call(inner)
+    finally:
+        q.ops._calls = keep
