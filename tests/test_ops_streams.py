@@ -56,6 +56,54 @@ def test_memory_let_go_of_after_the_call_is_not_reused_before_it_ran(op):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 200])
+@pytest.mark.parametrize("before", ["nothing", "copy", "memset", "join", "join_of_operators", "fork"])
+def test_captured_behind_every_kind_of_node(before, n):
+    """A captured call whose dependencies are no kernel, several nodes or none; replayed
+    on new inputs it gives the bits of the eager call."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    t = lambda *s: torch.empty(s, dtype=BF16, device="cuda").normal_(generator=g)  # noqa: E731
+    lw, x, src, y = q.LinearWeights(t(256, 128), activation="silu"), t(n, 128), t(n, 128), t(n, 128)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    q.moe_linear(x, lw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        if before == "copy":
+            x.copy_(src)
+        elif before == "memset":
+            x.zero_()
+        elif before.startswith("join"):
+            for st, buf in ((side, x), (other, y)):
+                st.wait_stream(main)
+                with torch.cuda.stream(st):
+                    if before == "join":
+                        buf.copy_(src)
+                    else:
+                        buf.copy_(q.moe_linear(src, lw)[:, :128])
+            main.wait_stream(side)
+            main.wait_stream(other)
+        if before == "fork":
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                b = q.moe_linear(y, lw)
+            a = q.moe_linear(x, lw)
+            main.wait_stream(side)
+            out = torch.cat([a, b, q.moe_linear(x, lw)])
+        else:
+            out = torch.cat([q.moe_linear(x, lw), q.moe_linear(y, lw)])
+    for _ in range(3):
+        for buf in (src, x, y):
+            buf.copy_(t(n, 128))
+        graph.replay()
+        torch.cuda.synchronize()
+        tail = [x] if before == "fork" else []
+        assert torch.equal(out, torch.cat([q.moe_linear(v, lw) for v in [x, y] + tail]))
+    q.moe_ops_check()
+
+
+@pytest.mark.gpu
 def test_an_output_counts_as_written():
     """Autograd notices that a buffer which it keeps for a backward pass was the output of
     a call, as after an in-place operation of torch, with and without the module."""
