@@ -34,10 +34,10 @@
 // rows. Measured (GB300, bf16, clocks as they come, 2.0 GHz at best):
 //   65536 x 4096 x 4096                          1146 us  1918 TFLOP/s
 //   8192 x 4096 x 4096                            145 us  1900 TFLOP/s (library 138)
-//   8192 x 4096 x 2 x 2048 gated, SiLU        148..167 us  1860..1650 TFLOP/s
-//   8192 tokens x 8 of 128 experts, 2048 -> 2 x 768, gathered  289 us  1427 TFLOP/s
-//   64 tokens x 8 of 128 experts, 768 -> 2048     64.6 us  6.2 TB/s
-// (The range is the clock under the power limit: short runs and long ones.)
+//   8192 x 4096 x 2 x 2048 gated, SiLU        146..171 us  1880..1610 TFLOP/s
+//   8192 tokens x 8 of 128 experts, 2048 -> 2 x 768, gathered  277..325 us  1490..1270 TFLOP/s
+//   64 tokens x 8 of 128 experts, 768 -> 2048     65.3 us  6.1 TB/s
+// (The ranges are the clock under the power limit: short runs and long ones, several boards.)
 // Dealing each pair one contiguous run of rows, for an even end, was slower on the
 // grouped product (455 against 300 us): pairs then no longer share a weight block
 // while it is in L2.

@@ -3,8 +3,8 @@
 //
 // A call on a few tokens is as long on the host as on the GPU, and most of that is
 // the interpreter asking each tensor for its properties and allocating the output.
-// Here the same checks and the allocation are C++ (one-token linear: 9.4 to 6 us on
-// a Grace core). Whatever is not the usual call (another device or stream, a tensor
+// Here the same checks and the allocation are C++ (host time of a one-token linear on
+// a Grace core: 3.6 us, 11 through ctypes). Whatever is not the usual call (another device or stream, a tensor
 // subclass, an input that asks for a gradient, any argument that does not fit)
 // returns None, and ops.py goes on from there with its own checks and messages.
 // Compiled against the installed torch, without the CUDA library: ops.py passes in

@@ -168,8 +168,8 @@ class LinearWeights:
     "gelu_tanh". act_limit: the clamp bound of a gated product, 0 for none.
 
     The tensors are referenced, not copied. One that is given another storage (`w.data =
-    other`, as offloading does) is followed: a call goes by the tensors as they are then.
-    Their shapes and type have to stay."""
+    other`, as offloading does) is followed: a call goes by the tensors as they are then (a
+    captured graph by what they were at its capture). Their shapes and type have to stay."""
 
     def __init__(self, w, w_up=None, bias=None, bias_up=None, activation: str = "none", act_limit: float = 0.0):
         _lib()
