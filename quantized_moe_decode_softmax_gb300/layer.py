@@ -8,7 +8,8 @@ from typing import Any, Optional
 import numpy as np
 
 from . import _abi
-from .ops import LinearWeights, moe_combine_slots, moe_group_slots, moe_grouped_linear, moe_linear, moe_ops_check
+from .ops import (LinearWeights, _no_grad, moe_combine_slots, moe_group_slots, moe_grouped_linear, moe_linear,
+                  moe_ops_check)
 
 _DT = {"f32": _abi.MOE_DTYPE_F32, "bf16": _abi.MOE_DTYPE_BF16}
 
@@ -89,8 +90,8 @@ class MoeDecodeLayer:
         n = x.shape[0]
         if shared is not None and {x.dtype, out.dtype if out is not None else self._out_torch_dtype()} != {shared.dtype}:
             raise TypeError(f"the shared expert is {shared.dtype}: x and the step's output have to be, too")
-        if shared is not None and shared.down.N != w.D:
-            raise ValueError(f"the shared expert is {shared.down.N} wide, the step {w.D}")
+        if shared is not None:
+            shared.refuse(x, out, w.D)
         if out is None:
             out = torch.empty((n, w.D), dtype=self._out_torch_dtype(), device=x.device)
         _abi.moe_decode_forward(self.plan, x, w.router_w, w.router_bias, w.c_planes, n,
@@ -146,6 +147,12 @@ class SharedExpert:
         if (self.down.N, self.down.K) != (self.gate_up.K, self.gate_up.N):
             raise ValueError(f"down {tuple(down.shape)} does not fit gate {tuple(gate.shape)}")
         self.dtype = self.down.dtype
+
+    def refuse(self, x, out, width: int):
+        """Raise for a step `width` wide on x that this expert cannot run beside."""
+        if self.down.N != width:
+            raise ValueError(f"the shared expert is {self.down.N} wide, the step {width}")
+        _no_grad(x, out, *self.gate_up.tensors, *self.down.tensors)
 
     def forward(self, x, residual=None, out=None, stream=None):
         """[n, D] -> [n, D], plus `residual` (which `out` may be)."""

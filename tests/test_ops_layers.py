@@ -22,8 +22,8 @@ class FakeLib:
 class FakeShared:
     dtype = BF16
 
-    class down:
-        N = 512
+    def refuse(self, x, out, width):
+        pass
 
     def forward(self, x, residual, out, stream):
         return out.add_(1)
@@ -78,6 +78,20 @@ def test_shared_expert_of_another_width_is_refused_before_the_step(monkeypatch):
     x, out = torch.zeros(2, 512, dtype=BF16), torch.zeros(2, 512, dtype=BF16)
     with pytest.raises(ValueError, match="wide"):
         lay.forward(x, weights, out=out, stream=77, shared=q.SharedExpert(g, g, d))
+
+
+def test_shared_expert_that_asks_for_gradients_is_refused_before_the_step(monkeypatch):
+    ops._lib()
+    lay = step_layer(monkeypatch)
+    weights = layer.DeviceLayer.__new__(layer.DeviceLayer)
+    weights.D, weights.router_w, weights.router_bias, weights.c_planes = 512, None, None, None
+    monkeypatch.setattr(_abi, "moe_decode_forward", lambda *a: pytest.fail("launched"))
+    t = lambda *s: torch.zeros(*s, dtype=BF16)  # noqa: E731
+    for i in range(4):
+        given = [t(16, 512), t(16, 512), t(512, 16), t(2, 512)]
+        given[i] = torch.nn.Parameter(given[i])
+        with pytest.raises(RuntimeError, match="requires a gradient"):
+            lay.forward(given[3], weights, out=t(2, 512), stream=77, shared=q.SharedExpert(*given[:3]))
 
 
 def test_routed_experts_refuse_ids_of_other_tokens(monkeypatch):
