@@ -11,6 +11,7 @@ using namespace moe::ops;
 namespace {
 
 constexpr int kMaxE = 1024, kMaxK = 65536, kMaxN = 1 << 20, kMaxRows = 1 << 24, kMaxRanks = 64;
+constexpr long long kMaxSlots = 1 << 24;  // as moe_group_slots takes
 
 bool misaligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 
@@ -38,6 +39,24 @@ moe_status check_product(const moe_product *p) {
     return MOE_OK;
 }
 
+moe_status check_product_q8(const moe_product_q8 *p) {
+    if (!p || !p->w || !p->scale || (p->w_up && !p->scale_up)) return MOE_ERR_INVALID_ARG;
+    if (p->dtype == MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
+    if (p->dtype != MOE_DTYPE_BF16 && p->dtype != MOE_DTYPE_F16) return MOE_ERR_INVALID_ARG;
+    if (p->E < 1 || p->N < 1 || p->K < 1) return MOE_ERR_INVALID_ARG;
+    if (p->E > kMaxE || p->N > kMaxN || p->K > kMaxK || p->K % 16) return MOE_ERR_UNSUPPORTED;
+    if (p->ldw < p->K || p->ldw % 16 || p->ldw > (1LL << 32)) return MOE_ERR_INVALID_ARG;
+    if (p->E > 1 && (p->stride_e < 0 || p->stride_e % 16 || p->stride_e > (1LL << 36))) return MOE_ERR_INVALID_ARG;
+    if (misaligned(p->w, 16) || misaligned(p->w_up, 16) || misaligned(p->bias, 2) || misaligned(p->bias_up, 2) ||
+        misaligned(p->scale, 4) || misaligned(p->scale_up, 4))
+        return MOE_ERR_INVALID_ARG;
+    if ((p->bias_up || p->scale_up) && !p->w_up) return MOE_ERR_INVALID_ARG;
+    if (p->activation < MOE_EPI_NONE || p->activation > MOE_EPI_GELU_TANH) return MOE_ERR_INVALID_ARG;
+    if (!(p->act_limit >= 0.0f && p->act_limit <= 3.0e38f) || (p->act_limit > 0.0f && !p->w_up))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 // rows `ld` elements apart that hold `cols` elements each
 bool bad_rows(int64_t ld, int64_t cols) { return ld < cols || ld > (1LL << 32); }
 
@@ -45,6 +64,25 @@ Product product_of(const moe_product *p) {
     Product a{};
     a.w = p->w;
     a.w_up = p->w_up;
+    a.bias = p->bias;
+    a.bias_up = p->bias_up;
+    a.ldw = p->ldw;
+    a.stride_e = p->E > 1 ? p->stride_e : 0;
+    a.E = p->E;
+    a.N = p->N;
+    a.K = p->K;
+    a.dtype = p->dtype;
+    a.act = p->activation;
+    a.limit = p->act_limit;
+    return a;
+}
+
+Product product_of(const moe_product_q8 *p) {
+    Product a{};
+    a.w = p->w;
+    a.w_up = p->w_up;
+    a.w_scale = p->scale;
+    a.w_up_scale = p->scale_up;
     a.bias = p->bias;
     a.bias_up = p->bias_up;
     a.ldw = p->ldw;
@@ -86,6 +124,8 @@ moe_status run(const Product &a, cudaStream_t st) {
     }
     return of(launch_product_rows(a, st));
 }
+
+moe_status run_q8(const Product &a, cudaStream_t st) { return of(launch_product_rows_q8(a, st)); }
 
 }  // namespace
 
@@ -136,6 +176,106 @@ moe_status moe_grouped_linear(const moe_product *p, const int32_t *offsets, cons
     return run(a, static_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_linear_q8(const moe_product_q8 *p, const int8_t *x, int64_t ldx, const float *x_scale, int n,
+                         const void *residual, int64_t ldr, void *out, int64_t ldo, void *stream) {
+    const moe_status bad = check_product_q8(p);
+    if (bad != MOE_OK) return bad;
+    if (!x || !x_scale || !out || n < 0 || p->E != 1) return MOE_ERR_INVALID_ARG;
+    if (n > kMaxRows) return MOE_ERR_UNSUPPORTED;
+    if (bad_rows(ldx, p->K) || ldx % 16 || bad_rows(ldo, p->N) || (residual && bad_rows(ldr, p->N)))
+        return MOE_ERR_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(x_scale, 4) || misaligned(out, 2) || misaligned(residual, 2) || out == x ||
+        out == x_scale || (residual == out && ldr != ldo))
+        return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    Product a = product_of(p);
+    a.x = x;
+    a.x_scale = x_scale;
+    a.ldx = ldx;
+    a.x_rows = a.rows = n;
+    a.residual = residual;
+    a.ldr = ldr;
+    a.out = out;
+    a.ldo = ldo;
+    return run_q8(a, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_grouped_linear_q8(const moe_product_q8 *p, const int32_t *offsets, const int32_t *row_token,
+                                 const int8_t *x, int64_t ldx, const float *x_scale, int x_rows, int rows, void *out,
+                                 int64_t ldo, void *stream) {
+    const moe_status bad = check_product_q8(p);
+    if (bad != MOE_OK) return bad;
+    if (!offsets || !x || !x_scale || !out || rows < 0 || x_rows < 0) return MOE_ERR_INVALID_ARG;
+    if (rows > kMaxRows || x_rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
+    if (bad_rows(ldx, p->K) || ldx % 16 || bad_rows(ldo, p->N)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(x_scale, 4) || misaligned(out, 2) || misaligned(offsets, 4) ||
+        misaligned(row_token, 4) || out == x || out == x_scale)
+        return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (row_token ? x_rows == 0 : x_rows < rows)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    Product a = product_of(p);
+    a.x = x;
+    a.x_scale = x_scale;
+    a.ldx = ldx;
+    a.x_rows = x_rows;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.row_token = row_token;
+    a.out = out;
+    a.ldo = ldo;
+    return run_q8(a, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_quantize_rows(int dtype, const void *x, int64_t ldx, int n, int K, int8_t *codes, int64_t ldc,
+                             float *scale, void *stream) {
+    if (!x || !codes || !scale || n < 0 || K < 1) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) return MOE_ERR_UNSUPPORTED;
+    if (n > kMaxRows || K > kMaxN) return MOE_ERR_UNSUPPORTED;
+    if (bad_rows(ldx, K) || bad_rows(ldc, K) || misaligned(x, 2) || misaligned(scale, 4) || x == codes ||
+        x == (const void *)scale || (const void *)codes == (const void *)scale)
+        return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    return of(launch_quantize_rows(dtype, x, ldx, n, K, codes, ldc, scale, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_route(const moe_router *r, int dtype, const void *logits, int64_t ldl, int n, int32_t *topk_idx,
+                     float *topk_w, void *stream) {
+    if (!r || !logits || !topk_idx || !topk_w || n < 0) return MOE_ERR_INVALID_ARG;
+    if (r->E < 1 || r->top_k < 1 || r->groups < 1 || r->top_groups < 1 || r->top_groups > r->groups ||
+        r->E % r->groups)
+        return MOE_ERR_INVALID_ARG;
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (r->group_best != 1 && r->group_best != 2) return MOE_ERR_INVALID_ARG;
+    if (r->top_k > (long long)r->top_groups * (r->E / r->groups)) return MOE_ERR_INVALID_ARG;
+    if (!(r->scale >= -3.0e38f && r->scale <= 3.0e38f)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16 && dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+    if (r->E > kMaxE || r->top_k > kMaxRanks || r->groups > 32 || n > kMaxRows || (long long)n * r->top_k > kMaxSlots)
+        return MOE_ERR_UNSUPPORTED;
+    const unsigned size = dtype == MOE_DTYPE_F32 ? 4 : 2;
+    if (bad_rows(ldl, r->E) || misaligned(logits, size) || misaligned(r->bias, 4) || misaligned(topk_idx, 4) ||
+        misaligned(topk_w, 4) || (const void *)topk_idx == (const void *)topk_w || logits == (const void *)topk_idx ||
+        logits == (const void *)topk_w)
+        return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    RouteArgs a{};
+    a.logits = logits;
+    a.bias = r->bias;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.ldl = ldl;
+    a.n = n;
+    a.E = r->E;
+    a.k = r->top_k;
+    a.dtype = dtype;
+    a.score = r->score;
+    a.groups = r->top_groups < r->groups ? r->groups : 1;  // all of them stay: no groups
+    a.top_groups = r->top_groups;
+    a.top2 = r->group_best == 2;
+    a.renormalize = r->renormalize != 0;
+    a.scale = r->scale;
+    return of(launch_route(a, static_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_group_slots(const int32_t *topk_idx, int n, int top_k, int E, int expert_begin, int expert_end,
                            int32_t *offsets, int32_t *slot_token, int32_t *slot_k, int32_t *slot_of, void *stream) {
     if (!topk_idx || !offsets || !slot_token || !slot_of || n < 0 || top_k < 1 || E < 1) return MOE_ERR_INVALID_ARG;
@@ -143,7 +283,7 @@ moe_status moe_group_slots(const int32_t *topk_idx, int n, int top_k, int E, int
     if (misaligned(topk_idx, 4) || misaligned(offsets, 4) || misaligned(slot_token, 4) || misaligned(slot_k, 4) ||
         misaligned(slot_of, 4))
         return MOE_ERR_INVALID_ARG;
-    if (E > kMaxE || top_k > kMaxRanks || (long long)n * top_k > kMaxRows) return MOE_ERR_UNSUPPORTED;
+    if (E > kMaxE || top_k > kMaxRanks || (long long)n * top_k > kMaxSlots) return MOE_ERR_UNSUPPORTED;
     return of(launch_group_slots(topk_idx, n, top_k, E, expert_begin, expert_end, offsets, slot_token, slot_k, slot_of,
                                  static_cast<cudaStream_t>(stream)));
 }

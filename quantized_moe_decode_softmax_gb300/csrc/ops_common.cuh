@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "ops_internal.h"
 
 namespace moe {
@@ -123,6 +125,33 @@ __device__ __forceinline__ void group_rows(const Product &p, int e, int &lo, int
 __device__ __forceinline__ int input_row(const Product &p, int r) {
     r = min(max(r, 0), p.rows - 1);
     return min(p.row_token ? max(p.row_token[r], 0) : r, p.x_rows - 1);
+}
+
+// the g-th group that holds rows, or -1 (one warp; E <= 1024)
+__device__ __forceinline__ int nth_group(const Product &p, int g) {
+    const int lane = threadIdx.x & 31;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+        int lo = 0, hi = 0;
+        if (e0 + lane < p.E) group_rows(p, e0 + lane, lo, hi);
+        const unsigned m = __ballot_sync(0xffffffffu, hi > lo);
+        const int c = __popc(m);
+        if (g < c) return e0 + __fns(m, 0, g + 1);
+        g -= c;
+    }
+    return -1;
+}
+
+// SMs of the current device, looked up once per device
+inline cudaError_t sm_count(int &sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms > 0) return cudaSuccess;
+    if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 }  // namespace ops

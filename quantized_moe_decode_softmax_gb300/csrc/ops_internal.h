@@ -23,6 +23,25 @@ struct Product {
     int E, N, K;
     int dtype, act;
     float limit;                 // 0: no clamp
+    // products of 8-bit codes: a scale per row of x and per row of each weight matrix
+    // (x, w and w_up are then int8, and ldx, ldw and stride_e count bytes)
+    const float *x_scale, *w_scale, *w_up_scale;
+};
+
+// One routing (moe_route), device pointers.
+struct RouteArgs {
+    const void *logits;
+    const float *bias;           // may be nullptr
+    int *topk_idx;
+    float *topk_w;
+    long long ldl;
+    int n, E, k, dtype, score;
+    int groups, top_groups;
+    bool top2;                   // a group's score is the sum of its best two
+    bool renormalize;
+    bool vector;                 // rows of logits are aligned for wide loads
+    int scratch;                 // doubles of shared memory per warp
+    float scale;
 };
 
 // A kernel launch that may begin before the stream's previous kernel has ended: the
@@ -57,6 +76,12 @@ cudaError_t launch_product_gemm(const Product &p, cudaStream_t st);
 // the status word of the current device's operators, cleared if it was set
 cudaError_t read_ops_status(unsigned *value, cudaStream_t st);
 
+// the same for products of 8-bit codes (ops_rows_q8.cu, ops_gemm_q8.cu)
+cudaError_t launch_product_rows_q8(const Product &p, cudaStream_t st);
+
+cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);
+cudaError_t launch_quantize_rows(int dtype, const void *x, long long ldx, int n, int K, int8_t *codes, long long ldc,
+                                 float *scale, cudaStream_t st);
 cudaError_t launch_group_slots(const int *topk_idx, int n, int top_k, int E, int e_lo, int e_hi, int *offsets,
                                int *slot_token, int *slot_k, int *slot_of, cudaStream_t st);
 cudaError_t launch_combine_slots(int dtype, const void *y, long long ldy, int rows, const int *slot_of,

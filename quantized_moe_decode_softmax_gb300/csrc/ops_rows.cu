@@ -18,8 +18,6 @@
 // 6.0 (5.6 TB/s); 4096x8192 13.6 (4.9 TB/s); 8 of 128 experts, gated 2048 -> 768, one
 // row each 11.2 (4.5 TB/s). Up to about 10 MB the time is launch, one load latency per
 // slice and the reduction; above, the weights' bytes.
-#include <atomic>
-
 #include "ops_common.cuh"
 #include "ptx.cuh"
 
@@ -50,20 +48,6 @@ __device__ __forceinline__ uint4 load8(const void *row, int k, int K) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(static_cast<const char *>(row) + 2 * (size_t)k));
     return v;
-}
-
-// the g-th group that holds rows, or -1 (one warp; E <= 1024)
-__device__ __forceinline__ int nth_group(const Product &p, int g) {
-    const int lane = threadIdx.x & 31;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        int lo = 0, hi = 0;
-        if (e0 + lane < p.E) group_rows(p, e0 + lane, lo, hi);
-        const unsigned m = __ballot_sync(0xffffffffu, hi > lo);
-        const int c = __popc(m);
-        if (g < c) return e0 + __fns(m, 0, g + 1);
-        g -= c;
-    }
-    return -1;
 }
 
 // MATS 1 or 2 (gated) weight matrices, TB blocks of 8 rows at a time. AHEAD: the
@@ -182,19 +166,6 @@ __global__ void __launch_bounds__(32 * kWarps, min_ctas(MATS, TB, AHEAD)) produc
         }
         __syncthreads();
     }
-}
-
-// SMs of the current device, looked up once per device
-cudaError_t sm_count(int &sms) {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (sms > 0) return cudaSuccess;
-    if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
-    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
-    return cudaSuccess;
 }
 
 template <typename T, int MATS, int TB>

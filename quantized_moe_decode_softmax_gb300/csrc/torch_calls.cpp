@@ -27,6 +27,10 @@ decltype(&moe_linear) fn_linear;
 decltype(&moe_grouped_linear) fn_grouped;
 decltype(&moe_group_slots) fn_slots;
 decltype(&moe_combine_slots) fn_combine;
+decltype(&moe_route) fn_route;
+decltype(&moe_quantize_rows) fn_quantize;
+decltype(&moe_linear_q8) fn_linear_q8;
+decltype(&moe_grouped_linear_q8) fn_grouped_q8;
 
 PyObject *other() { Py_RETURN_NONE; }
 
@@ -72,23 +76,44 @@ PyObject *result(moe_status st, const at::Tensor &out, PyObject *given) {
 
 at::ScalarType type_of(int dtype) { return dtype == MOE_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
 
-// Whether a product's weights (w, w_up, bias, bias_up: tensors or None) are still what
-// *p says of them: a tensor may have been given another storage, shape or device.
-bool weights(PyObject *o, const moe_product *p, int dev) {
-    if (!p || !PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) return false;
-    const void *at[4] = {p->w, p->w_up, p->bias, p->bias_up};
+// tensors that a struct keeps the addresses of (None where it has no address)
+template <int N> struct Kept {
+    const void *at[N];
+    at::ScalarType type[N];
+};
+Kept<4> kept(const moe_product *p) {
     const at::ScalarType dt = type_of(p->dtype);
-    for (int i = 0; i < 4; ++i) {
+    return {{p->w, p->w_up, p->bias, p->bias_up}, {dt, dt, dt, dt}};
+}
+Kept<6> kept(const moe_product_q8 *p) {
+    const at::ScalarType dt = type_of(p->dtype);
+    return {{p->w, p->w_up, p->scale, p->scale_up, p->bias, p->bias_up},
+            {at::kChar, at::kChar, at::kFloat, at::kFloat, dt, dt}};
+}
+
+// whether `w` is still the tensor of type dt at address `at`, on the device
+bool still(PyObject *w, const void *at, at::ScalarType dt, int dev) {
+    if (!THPVariable_Check(w)) return false;
+    const at::Tensor &t = THPVariable_Unpack(w);
+    return t.defined() && t.layout() == at::kStrided && !differentiated(t) && t.scalar_type() == dt && t.is_cuda() &&
+           t.get_device() == dev && t.const_data_ptr() == at;
+}
+
+// Whether a product's weights (w, w_up, then vectors of E N values: tensors or None) are
+// still what *p says of them: a tensor may have been given another storage, shape or device.
+template <typename P> bool weights(PyObject *o, const P *p, int dev) {
+    constexpr int N = sizeof(decltype(kept(p))::at) / sizeof(void *);
+    // (another number: the weights of another kind of product, and p no P)
+    if (!p || !PyTuple_Check(o) || PyTuple_GET_SIZE(o) != N) return false;
+    const auto k = kept(p);
+    for (int i = 0; i < N; ++i) {
         PyObject *w = PyTuple_GET_ITEM(o, i);
         if (w == Py_None) {
-            if (at[i]) return false;
+            if (k.at[i]) return false;
             continue;
         }
-        if (!THPVariable_Check(w)) return false;
+        if (!still(w, k.at[i], k.type[i], dev)) return false;
         const at::Tensor &t = THPVariable_Unpack(w);
-        if (!t.defined() || t.layout() != at::kStrided || differentiated(t) || t.scalar_type() != dt || !t.is_cuda() ||
-            t.get_device() != dev || t.const_data_ptr() != at[i])
-            return false;
         const int64_t d = t.dim();
         if (i < 2) {
             if ((d != 2 && d != 3) || t.size(d - 1) != p->K || t.size(d - 2) != p->N || (d == 3 ? t.size(0) : 1) != p->E)
@@ -225,12 +250,144 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the four entry points)
+// a tensor of `type` and these sizes on another's storage, from byte `at` on
+at::Tensor part_of(const at::Tensor &all, at::ScalarType type, int64_t at, at::IntArrayRef sizes) {
+    const auto meta = c10::scalarTypeToTypeMeta(type);
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), meta);
+    t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)meta.itemsize());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    return t;
+}
+
+// two results of a call, or its status as a number
+PyObject *results(moe_status st, const at::Tensor &first, const at::Tensor &second) {
+    if (st != MOE_OK) return PyLong_FromLong(st);
+    PyObject *t = PyTuple_New(2);
+    if (!t) return nullptr;
+    PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(first));
+    PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(second));
+    return t;
+}
+
+// route(router address, logits, (bias,)): (topk_idx, topk_w)
+PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (n_args != 3 || !PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 1) return other();
+    const auto *r = static_cast<const moe_router *>(PyLong_AsVoidPtr(a[0]));
+    const at::Tensor *l;
+    if (!r || !tensor(a[1], &l) || !l || l->dim() != 2 || !l->is_cuda()) return other();
+    const int dev = (int)l->get_device();
+    PyObject *bias = PyTuple_GET_ITEM(a[2], 0);
+    if (bias == Py_None ? r->bias != nullptr
+                        : !still(bias, r->bias, at::kFloat, dev) || THPVariable_Unpack(bias).numel() != r->E ||
+                              !THPVariable_Unpack(bias).is_contiguous())
+        return other();
+    const at::ScalarType dt = l->scalar_type();
+    int64_t ldl;
+    const int64_t n = l->size(0), k = r->top_k;
+    if ((dt != at::kBFloat16 && dt != at::kHalf && dt != at::kFloat) || !rows(*l, -1, r->E, dt, dev, &ldl) || n == 0 ||
+        n > INT32_MAX || k < 1 || k > 1024 || c10::cuda::current_device() != dev)
+        return other();
+    const at::Tensor all = at::empty({8 * n * k}, l->options().dtype(at::kByte));
+    const at::Tensor idx = part_of(all, at::kInt, 0, {n, k}), w = part_of(all, at::kFloat, 4 * n * k, {n, k});
+    const moe_status st = fn_route(r, dt == at::kFloat ? MOE_DTYPE_F32 : dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16,
+                                   l->const_data_ptr(), ldl, (int)n, idx.mutable_data_ptr<int32_t>(),
+                                   w.mutable_data_ptr<float>(), c10::cuda::getCurrentCUDAStream(dev).stream());
+    return results(st, idx, w);
+    END_HANDLE_TH_ERRORS
+}
+
+// quantize(x): (codes, scale)
+PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *x;
+    if (n_args != 1 || !tensor(a[0], &x) || !x || x->dim() != 2 || !x->is_cuda()) return other();
+    const int dev = (int)x->get_device();
+    const at::ScalarType dt = x->scalar_type();
+    const int64_t n = x->size(0), K = x->size(1);
+    int64_t ldx;
+    if ((dt != at::kBFloat16 && dt != at::kHalf) || n == 0 || K == 0 || n > INT32_MAX || K > INT32_MAX ||
+        !rows(*x, -1, K, dt, dev, &ldx) || c10::cuda::current_device() != dev)
+        return other();
+    const int64_t at_scale = (n * K + 15) / 16 * 16;
+    const at::Tensor all = at::empty({at_scale + 4 * n}, x->options().dtype(at::kByte));
+    const at::Tensor codes = part_of(all, at::kChar, 0, {n, K}), scale = part_of(all, at::kFloat, at_scale, {n});
+    const moe_status st = fn_quantize(dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16, x->const_data_ptr(), ldx, (int)n,
+                                      (int)K, codes.mutable_data_ptr<int8_t>(), K, scale.mutable_data_ptr<float>(),
+                                      c10::cuda::getCurrentCUDAStream(dev).stream());
+    return results(st, codes, scale);
+    END_HANDLE_TH_ERRORS
+}
+
+// codes [rows, K] and the scale of each row
+bool coded(PyObject *c, PyObject *s, int64_t K, int dev, const at::Tensor **x, const at::Tensor **scale, int64_t *ldx) {
+    return tensor(c, x) && *x && tensor(s, scale) && *scale && rows(**x, -1, K, at::kChar, dev, ldx) &&
+           dense(**scale, at::kFloat, dev) && (*scale)->dim() == 1 && (*scale)->size(0) == (*x)->size(0);
+}
+
+// linear_q8(product address, device, codes, scale, residual, out, weights)
+PyObject *linear_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (n_args != 7) return other();
+    const auto *p = static_cast<const moe_product_q8 *>(PyLong_AsVoidPtr(a[0]));
+    const int dev = (int)PyLong_AsLong(a[1]);
+    if (dev < 0 || !weights(a[6], p, dev) || p->E != 1) return other();
+    const at::Tensor *x, *scale, *res, *given;
+    int64_t ldx, ldr = 0, ldo = p->N;
+    if (!coded(a[2], a[3], p->K, dev, &x, &scale, &ldx) || !tensor(a[4], &res) || !tensor(a[5], &given)) return other();
+    const at::ScalarType dt = type_of(p->dtype);
+    const int64_t n = x->size(0);
+    if (n == 0 || n > INT32_MAX || (res && !rows(*res, n, p->N, dt, dev, &ldr)) ||
+        (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
+        return other();
+    const at::Tensor out = given ? *given : at::empty({n, p->N}, x->options().dtype(dt));
+    const moe_status st =
+        fn_linear_q8(p, x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)n,
+                     res ? res->const_data_ptr() : nullptr, ldr, out.mutable_data_ptr(), ldo,
+                     c10::cuda::getCurrentCUDAStream(dev).stream());
+    return result(st, out, a[5]);
+    END_HANDLE_TH_ERRORS
+}
+
+// grouped_q8(product address, device, codes, scale, offsets, row_token, out, weights)
+PyObject *grouped_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    if (n_args != 8) return other();
+    const auto *p = static_cast<const moe_product_q8 *>(PyLong_AsVoidPtr(a[0]));
+    const int dev = (int)PyLong_AsLong(a[1]);
+    if (dev < 0 || !weights(a[7], p, dev)) return other();
+    const at::Tensor *x, *scale, *off, *token, *given;
+    int64_t ldx, ldo = p->N;
+    if (!coded(a[2], a[3], p->K, dev, &x, &scale, &ldx) || !tensor(a[4], &off) || !off || !tensor(a[5], &token) ||
+        !tensor(a[6], &given))
+        return other();
+    if (!dense(*off, at::kInt, dev) || off->dim() != 1 || off->size(0) != p->E + 1 ||
+        (token && (!dense(*token, at::kInt, dev) || token->dim() != 1)))
+        return other();
+    const at::ScalarType dt = type_of(p->dtype);
+    const int64_t x_rows = x->size(0), n = token ? token->size(0) : x_rows;
+    if (n == 0 || x_rows == 0 || n > INT32_MAX || x_rows > INT32_MAX ||
+        (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
+        return other();
+    const at::Tensor out = given ? *given : at::empty({n, p->N}, x->options().dtype(dt));
+    const moe_status st = fn_grouped_q8(
+        p, off->const_data_ptr<int32_t>(), token ? token->const_data_ptr<int32_t>() : nullptr,
+        x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)x_rows, (int)n, out.mutable_data_ptr(), ldo,
+        c10::cuda::getCurrentCUDAStream(dev).stream());
+    return result(st, out, a[6]);
+    END_HANDLE_TH_ERRORS
+}
+
+// bind(addresses of the eight entry points)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
-    if (n_args != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+    if (n_args != 8) {
+        PyErr_SetString(PyExc_TypeError, "bind takes eight addresses");
         return nullptr;
     }
+    fn_route = reinterpret_cast<decltype(fn_route)>(PyLong_AsVoidPtr(a[4]));
+    fn_quantize = reinterpret_cast<decltype(fn_quantize)>(PyLong_AsVoidPtr(a[5]));
+    fn_linear_q8 = reinterpret_cast<decltype(fn_linear_q8)>(PyLong_AsVoidPtr(a[6]));
+    fn_grouped_q8 = reinterpret_cast<decltype(fn_grouped_q8)>(PyLong_AsVoidPtr(a[7]));
     fn_linear = reinterpret_cast<decltype(fn_linear)>(PyLong_AsVoidPtr(a[0]));
     fn_grouped = reinterpret_cast<decltype(fn_grouped)>(PyLong_AsVoidPtr(a[1]));
     fn_slots = reinterpret_cast<decltype(fn_slots)>(PyLong_AsVoidPtr(a[2]));
@@ -244,7 +401,9 @@ constexpr PyMethodDef method(const char *name) {
 }
 
 PyMethodDef methods[] = {method<linear>("linear"),   method<grouped>("grouped"), method<slots>("slots"),
-                         method<combine>("combine"), method<bind>("bind"),       {nullptr, nullptr, 0, nullptr}};
+                         method<combine>("combine"), method<route>("route"),     method<quantize>("quantize"),
+                         method<linear_q8>("linear_q8"), method<grouped_q8>("grouped_q8"), method<bind>("bind"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,5 +1,5 @@
 """Convenience wrappers over the C ABI: resident layer weights and a layer
-object that owns a plan, and the 16-bit expert layers that run beside it.
+object that owns a plan, and the 16-bit and 8-bit expert layers that run beside it.
 Argument marshalling only."""
 from __future__ import annotations
 
@@ -8,8 +8,9 @@ from typing import Any, Optional
 import numpy as np
 
 from . import _abi
-from .ops import (LinearWeights, _no_grad, moe_combine_slots, moe_group_slots, moe_grouped_linear, moe_linear,
-                  moe_ops_check)
+from .ops import (LinearWeights, LinearWeightsQ8, Router, _no_grad, moe_combine_slots, moe_group_slots,
+                  moe_grouped_linear, moe_grouped_linear_q8, moe_linear, moe_linear_q8, moe_ops_check,
+                  moe_quantize_rows, moe_route)
 
 _DT = {"f32": _abi.MOE_DTYPE_F32, "bf16": _abi.MOE_DTYPE_BF16}
 
@@ -84,7 +85,7 @@ class MoeDecodeLayer:
         return torch.float32 if self.out_dtype == "f32" else torch.bfloat16
 
     def forward(self, x, w: DeviceLayer, out=None, stream=None, shared=None):
-        """One step. shared: a SharedExpert whose output is added to the routed
+        """One step. shared: a SharedExpert (or SharedExpertQ8) whose output is added to the routed
         experts' (16-bit activations and output: its type)."""
         import torch
         n = x.shape[0]
@@ -142,11 +143,12 @@ class SharedExpert:
     gate, up [F, D], down [D, F]; two launches (moe_linear)."""
 
     def __init__(self, gate, up, down, activation: str = "silu", act_limit: float = 0.0):
-        self.gate_up = LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit)
-        self.down = LinearWeights(down)
-        if (self.down.N, self.down.K) != (self.gate_up.K, self.gate_up.N):
-            raise ValueError(f"down {tuple(down.shape)} does not fit gate {tuple(gate.shape)}")
-        self.dtype = self.down.dtype
+        self._set(LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit), LinearWeights(down))
+
+    def _set(self, gate_up, down):
+        if gate_up.grouped or down.grouped or (down.N, down.K) != (gate_up.K, gate_up.N):
+            raise ValueError(f"down {tuple(down.tensors[0].shape)} does not fit gate {tuple(gate_up.tensors[0].shape)}")
+        self.gate_up, self.down, self.dtype = gate_up, down, down.dtype
 
     def refuse(self, x, out, width: int):
         """Raise for a step `width` wide on x that this expert cannot run beside."""
@@ -171,21 +173,92 @@ class RoutedExperts:
     end) of the expert ids whose slots are run (the weights cover all E ids)."""
 
     def __init__(self, gate, up, down, activation: str = "silu", act_limit: float = 0.0, experts=None):
-        self.gate_up = LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit)
-        self.down = LinearWeights(down)
-        if (self.down.E, self.down.N, self.down.K) != (self.gate_up.E, self.gate_up.K, self.gate_up.N):
-            raise ValueError(f"down {tuple(down.shape)} does not fit gate {tuple(gate.shape)}")
-        self.experts = experts
+        self._set(LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit), LinearWeights(down), experts)
+
+    def _set(self, gate_up, down, experts):
+        if not gate_up.grouped or not down.grouped or (down.E, down.N, down.K) != (gate_up.E, gate_up.K, gate_up.N):
+            raise ValueError(f"down {tuple(down.tensors[0].shape)} does not fit gate {tuple(gate_up.tensors[0].shape)}")
+        self.gate_up, self.down, self.experts = gate_up, down, experts
 
     def forward(self, x, topk_idx, topk_w, residual=None, out=None, stream=None):
         """x [n, D], topk_idx [n, k] int32, topk_w [n, k] float32 -> [n, D]."""
         if x.dim() != 2 or topk_idx.dim() != 2 or x.shape[0] != topk_idx.shape[0]:
             raise ValueError(f"x {tuple(x.shape)} and topk_idx {tuple(topk_idx.shape)} have to be [n, D] and [n, k]")
         g = moe_group_slots(topk_idx, self.gate_up.E, experts=self.experts, stream=stream)
-        h = moe_grouped_linear(x, self.gate_up, g.offsets, row_token=g.slot_token, stream=stream)
-        y = moe_grouped_linear(h, self.down, g.offsets, stream=stream)
+        y = self._products(x, g, stream)
         return moe_combine_slots(y, g.slot_of, topk_w, residual=residual, out=out, stream=stream)
+
+    def _products(self, x, g, stream):
+        h = moe_grouped_linear(x, self.gate_up, g.offsets, row_token=g.slot_token, stream=stream)
+        return moe_grouped_linear(h, self.down, g.offsets, stream=stream)
 
     def check(self, stream=None):
         """moe_ops_check: raise MoeError for a device-side wait that gave up."""
         moe_ops_check(stream)
+
+
+class SharedExpertQ8(SharedExpert):
+    """A SharedExpert in 8-bit codes: gate_up (a gated LinearWeightsQ8 [F, D]) and down
+    ([D, F]). Its inputs are quantised row by row (moe_quantize_rows), x and the
+    activations between the products: four launches."""
+
+    def __init__(self, gate_up: LinearWeightsQ8, down: LinearWeightsQ8):
+        _both_q8(gate_up, down)
+        self._set(gate_up, down)
+
+    @classmethod
+    def quantize(cls, gate, up, down, activation: str = "silu", act_limit: float = 0.0):
+        """From 16-bit weights on the GPU, as SharedExpert takes them."""
+        return cls(*_quantized(gate, up, down, activation, act_limit))
+
+    def forward(self, x, residual=None, out=None, stream=None):
+        """[n, D] -> [n, D], plus `residual` (which `out` may be)."""
+        _no_grad(x, residual, out)
+        h = moe_linear_q8(moe_quantize_rows(x, stream=stream), self.gate_up, stream=stream)
+        return moe_linear_q8(moe_quantize_rows(h, stream=stream), self.down, residual=residual, out=out, stream=stream)
+
+
+class RoutedExpertsQ8(RoutedExperts):
+    """RoutedExperts in 8-bit codes: gate_up (a gated LinearWeightsQ8 [E, F, D]) and down
+    ([E, D, F]). A token is quantised once for all its experts, and the activations
+    between the products row by row: six launches."""
+
+    def __init__(self, gate_up: LinearWeightsQ8, down: LinearWeightsQ8, experts=None):
+        _both_q8(gate_up, down)
+        self._set(gate_up, down, experts)
+
+    @classmethod
+    def quantize(cls, gate, up, down, activation: str = "silu", act_limit: float = 0.0, experts=None):
+        """From 16-bit weights on the GPU, as RoutedExperts takes them."""
+        return cls(*_quantized(gate, up, down, activation, act_limit), experts=experts)
+
+    def _products(self, x, g, stream):
+        h = moe_grouped_linear_q8(moe_quantize_rows(x, stream=stream), self.gate_up, g.offsets, row_token=g.slot_token,
+                                  stream=stream)
+        return moe_grouped_linear_q8(moe_quantize_rows(h, stream=stream), self.down, g.offsets, stream=stream)
+
+
+def _both_q8(*weights):
+    for w in weights:
+        if not isinstance(w, LinearWeightsQ8):
+            raise TypeError(f"the weights are {type(w).__name__}, not LinearWeightsQ8")
+
+
+def _quantized(gate, up, down, activation, act_limit):
+    return (LinearWeightsQ8.quantize(gate, w_up=up, activation=activation, act_limit=act_limit),
+            LinearWeightsQ8.quantize(down))
+
+
+class RouterLayer:
+    """The router of a layer: logits = x weight^T (+ bias), then `rule` (a Router) makes
+    ids and weights of them. weight [E, D] and bias [E] in 16 bits, and so are the logits
+    (moe_linear rounds them once); two launches."""
+
+    def __init__(self, weight, rule: Router, bias=None):
+        self.logits, self.rule = LinearWeights(weight, bias=bias), rule
+        if self.logits.grouped or self.logits.N != rule.E:
+            raise ValueError(f"weight {tuple(weight.shape)} does not fit {rule.E} experts")
+
+    def forward(self, x, stream=None):
+        """x [n, D] -> Routing: topk_idx [n, top_k] int32, topk_w [n, top_k] float32."""
+        return moe_route(moe_linear(x, self.logits, stream=stream), self.rule, stream=stream)

@@ -1,7 +1,9 @@
 """The operators of include/moe_ops.h on torch tensors.
 
-moe_linear, moe_grouped_linear, moe_group_slots and moe_combine_slots keep the
-C names; LinearWeights holds the weights and the epilogue of a product. As in
+moe_linear, moe_grouped_linear, moe_group_slots, moe_combine_slots, moe_route,
+moe_quantize_rows, moe_linear_q8 and moe_grouped_linear_q8 keep the C names;
+LinearWeights and LinearWeightsQ8 hold the weights and the epilogue of a product,
+Router the rule by which logits become ids and weights. As in
 the rest of the binding nothing is computed here: the functions check the
 tensors, pass pointers and sizes to libmoe_decode.so, and turn status codes into
 MoeError. Inference only: a call that autograd would have to record is refused.
@@ -29,7 +31,14 @@ MOE_DTYPE_F16 = 2
 MOE_EPI_NONE, MOE_EPI_SILU, MOE_EPI_GELU, MOE_EPI_GELU_TANH = range(4)
 ACTIVATIONS = {"none": MOE_EPI_NONE, "silu": MOE_EPI_SILU, "gelu": MOE_EPI_GELU, "gelu_tanh": MOE_EPI_GELU_TANH}
 
-OPS_EXPORTED = ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots", "moe_ops_check")
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = range(2)
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+GROUP_SCORES = {"max": 1, "top2": 2}
+
+# as torch_calls.bind takes them
+_CALLS = ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots", "moe_route", "moe_quantize_rows",
+          "moe_linear_q8", "moe_grouped_linear_q8")
+OPS_EXPORTED = _CALLS + ("moe_ops_check",)
 
 
 class moe_product(ctypes.Structure):
@@ -37,6 +46,20 @@ class moe_product(ctypes.Structure):
                 ("w", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("ldw", ctypes.c_int64),
                 ("stride_e", ctypes.c_int64), ("bias", ctypes.c_void_p), ("bias_up", ctypes.c_void_p),
                 ("activation", ctypes.c_int), ("act_limit", ctypes.c_float)]
+
+
+class moe_product_q8(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("E", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("w", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("stride_e", ctypes.c_int64), ("scale", ctypes.c_void_p), ("scale_up", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("bias_up", ctypes.c_void_p),
+                ("activation", ctypes.c_int), ("act_limit", ctypes.c_float)]
+
+
+class moe_router(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("top_k", ctypes.c_int), ("score", ctypes.c_int), ("groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("group_best", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
 torch = None   # bound by _bind: importing the package does not import torch
@@ -53,6 +76,10 @@ def _bind():
     L.moe_grouped_linear.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i64, vp]
     L.moe_group_slots.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
     L.moe_combine_slots.argtypes = [i32, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp]
+    L.moe_route.argtypes = [vp, i32, vp, i64, i32, vp, vp, vp]
+    L.moe_quantize_rows.argtypes = [i32, vp, i64, i32, i32, vp, i64, vp, vp]
+    L.moe_linear_q8.argtypes = [vp, vp, i64, vp, i32, vp, i64, vp, i64, vp]
+    L.moe_grouped_linear_q8.argtypes = [vp, vp, vp, vp, i64, vp, i32, i32, vp, i64, vp]
     L.moe_ops_check.argtypes = [vp]
     for name in OPS_EXPORTED:
         getattr(L, name).restype = i32
@@ -64,8 +91,7 @@ def _bind():
         try:
             m = importlib.util.module_from_spec(
                 importlib.util.spec_from_file_location("_torch_calls", path, loader=loader))
-            m.bind(*[ctypes.cast(getattr(L, f), vp).value for f in
-                     ("moe_linear", "moe_grouped_linear", "moe_group_slots", "moe_combine_slots")])
+            m.bind(*[ctypes.cast(getattr(L, f), vp).value for f in _CALLS])
             _calls = m
         except (ImportError, OSError) as e:  # every call has its way through ctypes
             warnings.warn(f"{path} cannot be loaded ({e}): calls of the operators go through ctypes")
@@ -157,7 +183,41 @@ def _here(device: int, stream) -> bool:
     return stream is None and device >= 0 and torch._C._cuda_getDevice() == device
 
 
-class LinearWeights:
+class _Described:
+    """Tensors (`tensors`, None where there is none) and the C struct `c` that describes
+    them, at address `ref`. A subclass's _describe checks the tensors and returns the struct
+    for them; it is made again when one of them has got another storage."""
+
+    def _start(self, struct):
+        self.c = struct()
+        self.ref = ctypes.addressof(self.c)
+        self._bind()
+
+    def _layout(self):
+        return [None if t is None else (t.data_ptr(), t.shape, t.stride(), t.dtype, t.device) for t in self.tensors]
+
+    def _bind(self):
+        layout = self._layout()
+        c = self._describe()
+        # in one piece and in place: a call of another thread has read `ref`, or copies `c`
+        (ctypes.c_char * ctypes.sizeof(c)).from_buffer(self.c).raw = bytes(c)
+        self._bound = layout
+
+    def _addresses(self):
+        """The tensors' addresses (None for none)."""
+        at = [_abi._ptr(t) for t in self.tensors]
+        if any(t is not None and t.is_cuda and not p for t, p in zip(self.tensors, at)):
+            raise ValueError("the storage of a weight has been freed")
+        return at
+
+    def current(self):
+        """A copy of the struct that describes the tensors as they are now."""
+        if self._layout() != self._bound:
+            self._bind()
+        return type(self.c).from_buffer_copy(self.c)
+
+
+class LinearWeights(_Described):
     """The weights and the epilogue of a product (moe_product).
 
     w: [N, K], or [E, N, K] for one matrix per expert; bfloat16 or float16, inputs
@@ -185,46 +245,136 @@ class LinearWeights:
         if self.E < 1 or self.N < 1 or self.K < 1:
             raise ValueError(f"w is empty: {tuple(w.shape)}")
         self._epilogue = ACTIVATIONS[activation], float(act_limit)
-        self.c = moe_product()
-        self.ref = ctypes.addressof(self.c)
-        self._bind()
+        self._start(moe_product)
 
-    def _layout(self):
-        return [None if t is None else (t.data_ptr(), t.shape, t.stride(), t.dtype, t.device) for t in self.tensors]
-
-    def _bind(self):
-        """Check the tensors and write their addresses and strides into the struct."""
+    def _describe(self):
         w, w_up, bias, bias_up = self.tensors
-        layout = self._layout()
         lead = (self.E,) if self.grouped else ()
         if tuple(w.shape) != lead + (self.N, self.K) or w.dtype != self.dtype:
             raise ValueError(f"w has become {tuple(w.shape)} of {w.dtype}: it was {lead + (self.N, self.K)} of {self.dtype}")
-        if w.stride(-1) != 1 and self.K > 1:
-            raise ValueError("w: the inputs of a row have to be adjacent")
-        if w_up is not None and (w_up.shape != w.shape or w_up.stride() != w.stride() or w_up.dtype != w.dtype
-                                 or w_up.device != w.device):
-            raise ValueError("w_up needs the shape, strides, type and device of w")
-        want = lead + (self.N,)
-        for name, b in (("bias", bias), ("bias_up", bias_up)):
-            if b is not None and (tuple(b.shape) != want or b.dtype != w.dtype or b.device != w.device
-                                  or not b.is_contiguous()):
-                raise ValueError(f"{name} has to be contiguous {want} of {w.dtype} on {w.device}")
-        ptr = _abi._ptr
-        if w.is_cuda and not all(t is None or ptr(t) for t in self.tensors):
-            raise ValueError("the storage of a weight has been freed")
-        c = moe_product(_dtype_code(w.dtype), self.E, self.N, self.K, ptr(w), ptr(w_up),
-                        w.stride(-2) if self.N > 1 else self.K,
-                        w.stride(0) if self.grouped and self.E > 1 else 0, ptr(bias), ptr(bias_up), *self._epilogue)
-        # in one piece and in place: a call of another thread has read `ref`, or copies `c`
-        (ctypes.c_char * ctypes.sizeof(c)).from_buffer(self.c).raw = bytes(c)
+        _check_weights(w, w_up, lead + (self.N,), w.dtype, (("bias", bias), ("bias_up", bias_up)))
+        at, at_up, at_bias, at_bias_up = self._addresses()
         self.device, self.device_index = w.device, w.get_device()
-        self._bound = layout
+        return moe_product(_dtype_code(w.dtype), self.E, self.N, self.K, at, at_up,
+                           w.stride(-2) if self.N > 1 else self.K,
+                           w.stride(0) if self.grouped and self.E > 1 else 0, at_bias, at_bias_up, *self._epilogue)
 
-    def current(self) -> moe_product:
-        """A copy of the struct that describes the tensors as they are now."""
-        if self._layout() != self._bound:
-            self._bind()
-        return moe_product.from_buffer_copy(self.c)
+
+def _check_weights(w, w_up, rows, dtype, biases):
+    """Check the layout of a product's matrices and of the vectors beside them."""
+    if w.stride(-1) != 1 and w.shape[-1] > 1:
+        raise ValueError("w: the inputs of a row have to be adjacent")
+    if w_up is not None and (w_up.shape != w.shape or w_up.stride() != w.stride() or w_up.dtype != w.dtype
+                             or w_up.device != w.device):
+        raise ValueError("w_up needs the shape, strides, type and device of w")
+    for name, b in biases:
+        if b is not None and (tuple(b.shape) != rows or b.dtype != dtype or b.device != w.device
+                              or not b.is_contiguous()):
+            raise ValueError(f"{name} has to be contiguous {rows} of {dtype} on {w.device}")
+
+
+class LinearWeightsQ8(_Described):
+    """The weights and the epilogue of a product of 8-bit codes (moe_product_q8):
+    z = x_scale scale (x w^T) + bias, out = act(z) [* z_up].
+
+    w: int8 [N, K], or [E, N, K] for one matrix per expert; inputs adjacent, rows (and
+    experts) at any distance that is a multiple of 16; K a multiple of 16. scale:
+    float32 [N] or [E, N], contiguous. w_up and scale_up: the second matrix of a gated
+    product, w's shape and strides. bias, bias_up, activation, act_limit: as for
+    LinearWeights. dtype: the type of biases, residual and result, bfloat16 by default.
+
+    The tensors are referenced and followed as LinearWeights does."""
+
+    def __init__(self, w, scale, w_up=None, scale_up=None, bias=None, bias_up=None, activation: str = "none",
+                 act_limit: float = 0.0, dtype=None):
+        _lib()
+        if w.dim() not in (2, 3):
+            raise ValueError(f"w has {w.dim()} dimensions, not 2 or 3")
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
+        if (w_up is None) != (scale_up is None):
+            raise ValueError("w_up and scale_up go together")
+        self.grouped = w.dim() == 3
+        self.E = w.shape[0] if self.grouped else 1
+        self.N, self.K = w.shape[-2], w.shape[-1]
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        self.tensors = (w, w_up, scale, scale_up, bias, bias_up)
+        if self.E < 1 or self.N < 1 or self.K < 1:
+            raise ValueError(f"w is empty: {tuple(w.shape)}")
+        self._epilogue = ACTIVATIONS[activation], float(act_limit)
+        self._start(moe_product_q8)
+
+    @classmethod
+    def quantize(cls, w, w_up=None, bias=None, bias_up=None, activation: str = "none", act_limit: float = 0.0):
+        """From 16-bit weights on the GPU ([N, K] or [E, N, K]): each row by its largest
+        value (moe_quantize_rows). dtype is the weights'."""
+        def rows(t):
+            if t is None:
+                return None, None
+            r = moe_quantize_rows(t.reshape(-1, t.shape[-1]))
+            return r.codes.view(t.shape), r.scale.view(t.shape[:-1])
+        (q, s), (q_up, s_up) = rows(w), rows(w_up)
+        return cls(q, s, q_up, s_up, bias, bias_up, activation, act_limit, w.dtype)
+
+    def _describe(self):
+        w, w_up, scale, scale_up, bias, bias_up = self.tensors
+        lead = (self.E,) if self.grouped else ()
+        if tuple(w.shape) != lead + (self.N, self.K) or w.dtype is not torch.int8:
+            raise ValueError(f"w is {tuple(w.shape)} of {w.dtype}, not {lead + (self.N, self.K)} of torch.int8")
+        rows = lead + (self.N,)
+        _check_weights(w, w_up, rows, self.dtype, (("bias", bias), ("bias_up", bias_up)))
+        _check_weights(w, w_up, rows, torch.float32, (("scale", scale), ("scale_up", scale_up)))
+        at, at_up, at_scale, at_scale_up, at_bias, at_bias_up = self._addresses()
+        self.device, self.device_index = w.device, w.get_device()
+        return moe_product_q8(_dtype_code(self.dtype), self.E, self.N, self.K, at, at_up,
+                              w.stride(-2) if self.N > 1 else self.K,
+                              w.stride(0) if self.grouped and self.E > 1 else 0, at_scale, at_scale_up, at_bias,
+                              at_bias_up, *self._epilogue)
+
+
+class Router(_Described):
+    """How the logits of E experts become the ids and weights of top_k (moe_router).
+
+    score: "softmax" or "sigmoid". bias: float32 [E] on the logits' device, added to the
+    scores for the choice alone (the load balance of a trained router), or None.
+    groups, top_groups: the experts form `groups` groups of neighbours, of which the
+    top_groups best stay, by their best expert (group_score "max") or their best two
+    ("top2"). renormalize: the weights are divided by their sum; scale: a factor on
+    them. The bias tensor is referenced and followed as LinearWeights does."""
+
+    def __init__(self, E: int, top_k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                 group_score: str = "max", renormalize: bool = True, scale: float = 1.0):
+        _lib()
+        if score not in SCORES:
+            raise ValueError(f"unknown score {score!r}: one of {', '.join(SCORES)}")
+        if group_score not in GROUP_SCORES:
+            raise ValueError(f"unknown group_score {group_score!r}: one of {', '.join(GROUP_SCORES)}")
+        self.E, self.top_k = int(E), int(top_k)
+        self.tensors = (bias,)
+        self._rule = (self.E, self.top_k, SCORES[score], int(groups), int(top_groups), GROUP_SCORES[group_score],
+                      int(bool(renormalize)), float(scale))
+        self._start(moe_router)
+
+    def _describe(self):
+        bias = self.tensors[0]
+        if bias is not None and (tuple(bias.shape) != (self.E,) or bias.dtype is not torch.float32
+                                 or not bias.is_contiguous()):
+            raise ValueError(f"bias is {tuple(bias.shape)} of {bias.dtype}: it has to be contiguous [{self.E}] of torch.float32")
+        return moe_router(*self._rule, self._addresses()[0])
+
+
+class Routing(NamedTuple):
+    """What moe_route returns: topk_idx [n, top_k] int32 and topk_w [n, top_k] float32, parts
+    of one allocation: they are not to be resized in place."""
+    topk_idx: object
+    topk_w: object
+
+
+class QuantizedRows(NamedTuple):
+    """What moe_quantize_rows returns: codes [n, K] int8 and scale [n] float32, parts of one
+    allocation: they are not to be resized in place."""
+    codes: object
+    scale: object
 
 
 class SlotGroups(NamedTuple):
@@ -247,6 +397,11 @@ def _no_grad(*tensors):
         raise RuntimeError("an input carries a forward-mode tangent: the operators propagate none")
 
 
+def _kind(weights, cls):
+    if not isinstance(weights, cls):
+        raise TypeError(f"the weights are {type(weights).__name__}, not {cls.__name__}")
+
+
 def _raise(status: int, what: str):
     raise _abi.MoeError(status, what)
 
@@ -257,6 +412,7 @@ def moe_linear(x, weights: LinearWeights, residual=None, out=None, stream=None):
         r = _calls.linear(weights.ref, weights.device_index, x, residual, out, weights.tensors)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_linear")
+    _kind(weights, LinearWeights)
     if weights.grouped:
         raise ValueError("moe_linear takes weights [N, K]; use moe_grouped_linear")
     _no_grad(x, residual, out, *weights.tensors)
@@ -302,6 +458,7 @@ def moe_grouped_linear(x, weights: LinearWeights, offsets, row_token=None, out=N
         r = _calls.grouped(weights.ref, weights.device_index, x, offsets, row_token, out, weights.tensors)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_grouped_linear")
+    _kind(weights, LinearWeights)
     if not weights.grouped:
         raise ValueError("moe_grouped_linear takes weights [E, N, K]; use moe_linear")
     _no_grad(x, out, *weights.tensors)
@@ -421,6 +578,164 @@ def _combine(code, y, ldy, slot_of, topk_w, residual, ldr, out, ldo, st):
                                       ldo, st)
         if status:
             _raise(status, "moe_combine_slots")
+    return out
+
+
+def moe_route(logits, router: Router, stream=None) -> Routing:
+    """Ids and weights of each row's top_k experts: logits [n, E] (bfloat16, float16 or
+    float32, columns adjacent). Ids are in falling order of what decides, ties by the
+    lower id; -1 with weight 0 where experts whose logit or bias is -inf leave fewer."""
+    if stream is None and _calls is not None:
+        r = _calls.route(router.ref, logits, router.tensors)
+        if r is not None:
+            return Routing._make(r) if r.__class__ is not int else _raise(r, "moe_route")
+    _kind(router, Router)
+    bias = router.tensors[0]
+    _no_grad(logits, bias)
+    c = router.current()
+    dev, dt = logits.get_device(), logits.dtype
+    code = _abi.MOE_DTYPE_F32 if dt is torch.float32 else _dtype_code(dt)
+    ldl = _rows(logits, "logits", router.E, dt, dev)
+    if bias is not None and bias.get_device() != dev:
+        raise ValueError(f"the router's bias is on {bias.device}, the logits are on {logits.device}")
+    if _here(dev, stream):
+        return _route(c, code, logits, ldl, router, torch._C._cuda_getCurrentRawStream(dev))
+    with _Elsewhere(dev, stream, (logits, bias)) as st:
+        return _route(c, code, logits, ldl, router, st)
+
+
+def _route(c, code, logits, ldl, router, st):
+    n, k = logits.shape[0], router.top_k
+    idx = torch.empty((n, max(k, 0)), dtype=torch.int32, device=logits.device)
+    w = torch.empty((n, max(k, 0)), dtype=torch.float32, device=logits.device)
+    if n:
+        status = _c.moe_route(ctypes.addressof(c), code, logits.data_ptr(), ldl, n, idx.data_ptr(), w.data_ptr(), st)
+        if status:
+            _raise(status, "moe_route")
+    return Routing(idx, w)
+
+
+def moe_quantize_rows(x, stream=None) -> QuantizedRows:
+    """8-bit codes of the rows of x [n, K] (bfloat16 or float16, columns adjacent) and the
+    scale of each: x is about codes * scale[:, None], the largest of a row at 127."""
+    _lib()
+    if stream is None and _calls is not None:
+        r = _calls.quantize(x)
+        if r is not None:
+            return QuantizedRows._make(r) if r.__class__ is not int else _raise(r, "moe_quantize_rows")
+    _no_grad(x)
+    dev, dt = x.get_device(), x.dtype
+    code = _dtype_code(dt)
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError(f"x has shape {tuple(x.shape)}, not [n, K]")
+    ldx = _rows(x, "x", x.shape[1], dt, dev)
+    if _here(dev, stream):
+        return _quantize(code, x, ldx, torch._C._cuda_getCurrentRawStream(dev))
+    with _Elsewhere(dev, stream, (x,)) as st:
+        return _quantize(code, x, ldx, st)
+
+
+def _quantize(code, x, ldx, st):
+    n, K = x.shape
+    codes = torch.empty((n, K), dtype=torch.int8, device=x.device)
+    scale = torch.empty(n, dtype=torch.float32, device=x.device)
+    if n:
+        status = _c.moe_quantize_rows(code, x.data_ptr(), ldx, n, K, codes.data_ptr(), K, scale.data_ptr(), st)
+        if status:
+            _raise(status, "moe_quantize_rows")
+    return QuantizedRows(codes, scale)
+
+
+def _codes(x, K, dev):
+    """Check codes and scales of rows; codes, scale and the distance of the rows."""
+    if not isinstance(x, tuple) or len(x) != 2:
+        raise TypeError("x has to be (codes, scale), as moe_quantize_rows returns it")
+    codes, scale = x
+    ldx = _rows(codes, "codes", K, torch.int8, dev)
+    if tuple(scale.shape) != (codes.shape[0],) or scale.dtype is not torch.float32 or scale.get_device() != dev \
+            or not scale.is_contiguous():
+        raise ValueError(f"scale has to be contiguous float32 [{codes.shape[0]}] on CUDA device {dev}")
+    return codes, scale, ldx
+
+
+def moe_linear_q8(x, weights: LinearWeightsQ8, residual=None, out=None, stream=None):
+    """moe_linear on codes: x is (codes [n, K] int8, scale [n] float32), as moe_quantize_rows
+    returns it; out [n, N] of the weights' dtype; `out` may be `residual`."""
+    if stream is None and _calls is not None and x.__class__ in (QuantizedRows, tuple) and len(x) == 2:
+        r = _calls.linear_q8(weights.ref, weights.device_index, x[0], x[1], residual, out, weights.tensors)
+        if r is not None:
+            return r if r.__class__ is not int else _raise(r, "moe_linear_q8")
+    _kind(weights, LinearWeightsQ8)
+    if weights.grouped:
+        raise ValueError("moe_linear_q8 takes weights [N, K]; use moe_grouped_linear_q8")
+    c = weights.current()
+    dt, dev, N = weights.dtype, weights.device_index, weights.N
+    codes, scale, ldx = _codes(x, weights.K, dev)
+    _no_grad(scale, residual, out, *weights.tensors)
+    n = codes.shape[0]
+    ldr = N if residual is None else _rows(residual, "residual", N, dt, dev, n)
+    ldo = N if out is None else _rows(out, "out", N, dt, dev, n)
+    if _here(dev, stream):
+        return _linear_q8(c, codes, ldx, scale, weights, residual, ldr, out, ldo,
+                          torch._C._cuda_getCurrentRawStream(dev))
+    with _Elsewhere(dev, stream, (codes, scale, residual, out, *weights.tensors)) as st:
+        return _linear_q8(c, codes, ldx, scale, weights, residual, ldr, out, ldo, st)
+
+
+def _linear_q8(c, codes, ldx, scale, weights, residual, ldr, out, ldo, st):
+    n = codes.shape[0]
+    if out is None:
+        out = torch.empty((n, weights.N), dtype=weights.dtype, device=weights.device)
+    else:
+        _written(out)
+    if n:
+        status = _c.moe_linear_q8(ctypes.addressof(c), codes.data_ptr(), ldx, scale.data_ptr(), n,
+                                  None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldo, st)
+        if status:
+            _raise(status, "moe_linear_q8")
+    return out
+
+
+def moe_grouped_linear_q8(x, weights: LinearWeightsQ8, offsets, row_token=None, out=None, stream=None):
+    """moe_grouped_linear on codes: x is (codes, scale) of [rows, K], or of [tokens, K] with
+    row_token [rows]; out [rows, N] of the weights' dtype."""
+    if stream is None and _calls is not None and x.__class__ in (QuantizedRows, tuple) and len(x) == 2:
+        r = _calls.grouped_q8(weights.ref, weights.device_index, x[0], x[1], offsets, row_token, out, weights.tensors)
+        if r is not None:
+            return r if r.__class__ is not int else _raise(r, "moe_grouped_linear_q8")
+    _kind(weights, LinearWeightsQ8)
+    if not weights.grouped:
+        raise ValueError("moe_grouped_linear_q8 takes weights [E, N, K]; use moe_linear_q8")
+    c = weights.current()
+    dt, dev, N = weights.dtype, weights.device_index, weights.N
+    codes, scale, ldx = _codes(x, weights.K, dev)
+    _no_grad(scale, out, *weights.tensors)
+    rows = codes.shape[0]
+    if row_token is not None:
+        tokens, rows = rows, row_token.numel()
+        _ints(row_token, "row_token", (rows,), dev)
+        if rows and not tokens:
+            raise ValueError("x has no rows to take")
+    _ints(offsets, "offsets", (weights.E + 1,), dev)
+    ldo = N if out is None else _rows(out, "out", N, dt, dev, rows)
+    if _here(dev, stream):
+        return _grouped_q8(c, codes, ldx, scale, rows, weights, offsets, row_token, out, ldo,
+                           torch._C._cuda_getCurrentRawStream(dev))
+    with _Elsewhere(dev, stream, (codes, scale, offsets, row_token, out, *weights.tensors)) as st:
+        return _grouped_q8(c, codes, ldx, scale, rows, weights, offsets, row_token, out, ldo, st)
+
+
+def _grouped_q8(c, codes, ldx, scale, rows, weights, offsets, row_token, out, ldo, st):
+    if out is None:
+        out = torch.empty((rows, weights.N), dtype=weights.dtype, device=weights.device)
+    else:
+        _written(out)
+    if rows:
+        status = _c.moe_grouped_linear_q8(ctypes.addressof(c), offsets.data_ptr(),
+                                          None if row_token is None else row_token.data_ptr(), codes.data_ptr(), ldx,
+                                          scale.data_ptr(), codes.shape[0], rows, out.data_ptr(), ldo, st)
+        if status:
+            _raise(status, "moe_grouped_linear_q8")
     return out
 
 
