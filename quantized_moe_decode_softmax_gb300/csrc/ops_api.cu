@@ -125,7 +125,29 @@ moe_status run(const Product &a, cudaStream_t st) {
     return of(launch_product_rows(a, st));
 }
 
-moe_status run_q8(const Product &a, cudaStream_t st) { return of(launch_product_rows_q8(a, st)); }
+moe_status run_q8(const Product &a, cudaStream_t st) {
+    if (!streams(a)) {
+        const cudaError_t err = launch_product_gemm_q8(a, st);
+        if (err != cudaErrorNotSupported) return of(err);
+    }
+    return of(launch_product_rows_q8(a, st));
+}
+
+// both status words of the current device, or'ed; cleared if one was set
+cudaError_t read_status(unsigned *value, cudaStream_t st) {
+    *value = 0;
+    cudaError_t err;
+    unsigned word[2] = {0, 0}, *at[2];
+    at[0] = ops_status(&err);
+    if (err == cudaSuccess) at[1] = ops_status_q8(&err);
+    for (int i = 0; i < 2 && err == cudaSuccess; ++i) err = cudaMemcpyAsync(&word[i], at[i], 4, cudaMemcpyDeviceToHost, st);
+    if (err == cudaSuccess) err = cudaStreamSynchronize(st);
+    if (err != cudaSuccess) return err;
+    *value = word[0] | word[1];
+    if (*value == 0) return err;
+    for (int i = 0; i < 2 && err == cudaSuccess; ++i) err = cudaMemsetAsync(at[i], 0, 4, st);
+    return err == cudaSuccess ? cudaStreamSynchronize(st) : err;
+}
 
 }  // namespace
 
@@ -306,7 +328,7 @@ moe_status moe_combine_slots(int dtype, const void *y, int64_t ldy, int rows, co
 
 moe_status moe_ops_check(void *stream) {
     unsigned status = 0;
-    const moe_status st = of(read_ops_status(&status, static_cast<cudaStream_t>(stream)));
+    const moe_status st = of(read_status(&status, static_cast<cudaStream_t>(stream)));
     return st != MOE_OK ? st : status ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 

@@ -1,0 +1,524 @@
+// ops_gemm_q8.cu -- products of 8-bit codes over many rows (moe_linear_q8,
+// moe_grouped_linear_q8) on the 5th-generation tensor cores.
+//
+//   out[r, c] = act(sx[r] sw[c] sum_k x[r, k] w[c, k] + bias[c]) (* the up product) (+ residual[r, c])
+//
+// The tensor cores of this GPU take no 8-bit integers (tcgen05 kind::i8 is not there,
+// mma.sync reaches 150 TOPS), and no pair of 8-bit floats holds one. They take f16 at
+// full rate, where whole numbers to 2048 are exact, so the codes become f16 between
+// shared memory and the MMA. The sums in f32 are exact to 2^24.
+//
+// Tiles, work items and epilogue are those of the 16-bit products (ops_gemm.cu): a
+// pair of CTAs, 128 weight rows per CTA as the M operand, up to 256 rows of x as N. New
+// is what lies between the loads and the MMAs:
+//   - a load stage holds 128 inputs as codes: 16 KB of weights (per matrix) and half of
+//     the tile's rows of x, 128 bytes each, by TMA with the 128-byte swizzle;
+//   - eight warps convert, four of them the first 64 inputs of a stage and four the other 64.
+//     The weights go to tensor memory (thread = weight row = lane; the MMA takes A from
+//     there), the rows of x to a second ring in shared memory, in the swizzled layout of
+//     a 16-bit tile. A half stage is handed to the MMA by itself;
+//   - A in tensor memory is what makes the rates meet: per 64 inputs at 256 rows a CTA's MMAs
+//     take 512 cycles, in which its shared memory moves 64 KB: 16 in by TMA, 16 read by the
+//     converters, 16 written by them (x) and 16 read by the MMAs (x). With A there too it
+//     would be 96. Tensor memory then has room for one accumulator set at 256 rows (two up
+//     to 192; gated: one up to 192, two up to 96).
+//
+// Every wait is bounded (1 s, reported through moe_ops_check); after one gives
+// up, all roles stop and the pair waits for its copies in flight before it ends.
+#include "ops_pair.cuh"
+#include "ops_q8.cuh"
+
+namespace moe {
+namespace ops {
+namespace {
+
+constexpr int kIn = 128;                 // inputs of a load stage: one 128-byte row of a swizzled tile
+constexpr int kTileW = kM * kIn;         // bytes of a weight tile
+constexpr int kMaxStages = 12, kMaxHalves = 4;
+constexpr int kConvert = 8;              // converter warps, two per quadrant of the tensor-memory lanes
+constexpr int kLoadW = kConvert + kEpilogue, kLoadX = kLoadW + 1, kMmaWarp = kLoadX + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+
+struct Tiling : Tiles {
+    int stages;
+    int stage_bytes;
+    int halves;       // half stages as f16, 2 or 4
+    int half_bytes;   // shared memory of one: the rows of x
+    int a_col;        // tensor memory: first column of the weights as f16
+};
+
+// TMA loads into this CTA's shared memory, counted by its own barrier
+__device__ __forceinline__ void load_2d(uint32_t dst, const void *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_gather4(uint32_t dst, const void *map, int x, const int (&r)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint4 lds(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts(uint32_t addr, uint2 a, uint2 b) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// On a barrier of the pair's first CTA. What it orders is in this SM and has completed: stores
+// to tensor memory (wait::st) and to shared memory (the proxy fence); the MMA reads both in
+// this SM. A release at cluster scope would wait for a round trip to L2 in each half stage.
+__device__ __forceinline__ void arrive_in_first(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// wait for what the peer's threads have arrived on, too
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (try_wait_cluster(bar, parity)) return true;
+    return wait_more(bar, parity, abort_flag) && try_wait_cluster(bar, parity);
+}
+
+// D[tmem of both CTAs] (+)= A * B^T: each CTA's tensor memory holds its 128 rows of A, its
+// shared memory half of B's rows; issued by one thread of the first CTA
+__device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 bd, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
+
+template <typename T, int MATS>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_gemm_q8_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling g,
+                           const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmx_half,
+                           const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmu) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    // full, empty: load stages of this CTA. h_full (the first CTA's counts for both), h_empty: half
+    // stages as f16. acc_empty: the first CTA's counts for both
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], h_full[kMaxHalves], h_empty[kMaxHalves];
+    __shared__ uint64_t acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tslot;
+    __shared__ int abort_word, warp_sum[kThreads / 32];
+    __shared__ __align__(16) float row_scale[kEpilogue][128];
+    volatile int *abort_flag = &abort_word;
+    unsigned char *ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char *f16_ring = ring + g.stages * g.stage_bytes;
+    int *first = reinterpret_cast<int *>(f16_ring + g.halves * g.half_bytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank();
+    const int item0 = blockIdx.x / kPair, item_step = gridDim.x / kPair;
+
+    if (tid == 0) {
+        abort_word = 0;
+        for (int i = 0; i < g.stages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], kConvert);
+        }
+        for (int i = 0; i < g.halves; ++i) {
+            ptx::mbar_init(&h_full[i], kConvert / 2 * kPair);
+            ptx::mbar_init(&h_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&acc_full[i], 1);
+            ptx::mbar_init(&acc_empty[i], kEpilogue * kPair);  // the epilogues' warps
+        }
+        ptx::mbar_init(&drain, 1);
+        ptx::mbar_fence_init();
+        ptx::prefetch_tensormap(&tmx);
+        ptx::prefetch_tensormap(&tmx_half);
+        ptx::prefetch_tensormap(&tmw);
+        if (MATS == 2) ptx::prefetch_tensormap(&tmu);
+    }
+    if (warp == kMmaWarp) tmem_alloc_pair(&tslot, kTmemCols);
+    ptx::griddep_wait();
+    const int total = number_items<kThreads>(p, g, first, warp_sum);
+    if (!p.offsets) first = nullptr;
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are ready
+    tc::fence_after_sync();
+    const uint32_t tmem = tslot;
+    const uint32_t ring_addr = tc::smem_u32(ring), full_addr = tc::smem_u32(full), empty_addr = tc::smem_u32(empty);
+    const uint32_t f16_addr = tc::smem_u32(f16_ring), h_full_addr = tc::smem_u32(h_full), h_empty_addr = tc::smem_u32(h_empty);
+    const uint32_t acc_full_addr = tc::smem_u32(acc_full), acc_empty_addr = tc::smem_u32(acc_empty);
+    const Walk walk{p, g, first, total};
+    const int nk = (p.K + kIn - 1) / kIn, nh = (p.K + kK - 1) / kK;  // load stages and half stages of a tile
+    const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
+    const uint32_t h_mask = g.halves - 1, h_log = g.halves == 4 ? 2 : 1;
+
+    if (warp == kLoadW) {
+        // ---- weights ------------------------------------------------------------
+        Ring at{ring_addr, empty_addr, full_addr, 0, 1};  // a fresh barrier passes the wait for phase 1
+        Item it;
+        bool ok = true;
+        for (int i = item0; ok && walk.get(i, it); i += item_step) {
+            const int half = it.T / kPair;  // rows of x that this CTA loads
+            const uint32_t bytes = MATS * kTileW + (p.row_token ? half : box_rows(half)) * kIn;
+            const int col = (it.m * kPair + rank) * kM, plane = p.stride_e ? it.e : 0;
+#pragma unroll 1
+            for (int k = 0; k < nk; ++k) {
+                if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                if (tc::elect_one()) {
+                    expect_tx(at.full, bytes);
+                    load_3d(at.stage, &tmw, k * kIn, col, plane, at.full);
+                    if (MATS == 2) load_3d(at.stage + kTileW, &tmu, k * kIn, col, plane, at.full);
+                }
+                at.next(stages, stage_bytes);
+            }
+        }
+        // Before the CTA may end, every copy has landed and every stage has been handed back, as
+        // in ops_gemm.cu.
+        const unsigned long long t0 = globaltimer();
+        for (uint32_t i = 0; i < stages; ++i) {
+            const uint32_t next = i < at.s ? at.phase ^ 1 : at.phase;
+            settle(full_addr + 8 * i, next, t0);
+            settle(empty_addr + 8 * i, next, t0);
+        }
+        __syncwarp();
+    } else if (warp == kLoadX) {
+        // ---- rows of x ------------------------------------------------------------
+        Ring at{ring_addr + MATS * kTileW, empty_addr, full_addr, 0, 1};
+        Item it;
+        bool ok = true;
+        for (int i = item0; ok && walk.get(i, it); i += item_step) {
+            const int half = it.T / kPair, r0 = it.r0 + rank * half;
+            if (p.row_token) {
+                // lane j's rows are the j-th copy; rows past the end repeat the last one
+                int rows[4] = {};
+                if (lane < half / 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) rows[j] = input_row(p, min(r0 + 4 * lane + j, it.r0 + it.rows - 1));
+                }
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k) {
+                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                    if (lane < half / 4) load_gather4(at.stage + lane * 512, &tmx, k * kIn, rows, at.full);
+                    at.next(stages, stage_bytes);
+                }
+            } else {
+                // two boxes of x at most: the last one is half as high if that is enough
+                const int n1 = half > kBoxRows ? (half - kBoxRows > kBoxRows / 2 ? 2 : 1) : 0;
+                const CUtensorMap *map0 = half > kBoxRows / 2 ? &tmx : &tmx_half, *map1 = n1 == 2 ? &tmx : &tmx_half;
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k) {
+                    if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
+                    if (tc::elect_one()) {
+                        load_2d(at.stage, map0, k * kIn, r0, at.full);
+                        if (n1) load_2d(at.stage + kBoxRows * kIn, map1, k * kIn, r0 + kBoxRows, at.full);
+                    }
+                    at.next(stages, stage_bytes);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp && rank == 0) {
+        // ---- MMAs --------------------------------------------------------------
+        if (tc::elect_one()) {
+            uint32_t c = 0;  // half stages so far
+            int n = 0;
+            Item it;
+            bool ok = true;
+            const uint32_t base = tc::idesc_f16_f32(kPair * kM, 0);
+            for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
+                const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
+                const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
+                const uint32_t acc = tmem + (uint32_t)(buf * MATS * g.tcap), acc_up = acc + g.tcap;
+                // the epilogues have read what this accumulator set held
+                if (!(ok = wait(acc_empty_addr + 8 * buf, (uint32_t)((use & 1) ^ 1), abort_flag))) break;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int k = 0; k < nh; ++k, ++c) {
+                    const uint32_t s = c & h_mask;
+                    if (!(ok = wait_cluster(h_full_addr + 8 * s, (c >> h_log) & 1, abort_flag))) break;
+                    tc::fence_after_sync();
+                    const uint32_t a = tmem + g.a_col + s * (MATS * kK / 2), b = desc_low(f16_addr + s * g.half_bytes);
+                    // the first MMA of a tile overwrites
+#pragma unroll
+                    for (int q = 0; q < kK / 16; ++q) {
+                        mma_pair_ts(acc, a + 8 * q, b + 2 * q, idesc, q ? 1 : k);
+                        if (MATS == 2) mma_pair_ts(acc_up, a + kK / 2 + 8 * q, b + 2 * q, idesc, q ? 1 : k);
+                    }
+                    commit_pair(h_empty_addr + 8 * s);
+                }
+                if (ok) commit_pair(acc_full_addr + 8 * buf);
+            }
+            if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
+                commit_pair(tc::smem_u32(&drain));
+                settle(tc::smem_u32(&drain), 0, globaltimer());
+            }
+        }
+        __syncwarp();
+    } else if (warp < kConvert) {
+        // ---- codes to f16 --------------------------------------------------------
+        const int q = warp & 3, h = warp >> 2;  // quadrant of the lanes; half of a stage
+        Ring at{ring_addr, empty_addr, full_addr, 0, 0};
+        const uint32_t peer_full = in_first(h_full_addr);
+        const int wr = 32 * q + lane;  // this thread's weight row
+        // this thread's pieces of x: row and 16 codes of an atom of 8 rows. The lanes of a quarter
+        // warp take rows r and r + 4 and write their two pieces in turn, which keeps them on
+        // different banks
+        const int l = lane & 7, xr = (lane >> 3) + 4 * (l >> 2), swap = l >> 2;
+        const uint32_t x_src = xr * 128 + (((4 * h + (l & 3)) ^ xr) << 4);
+        const uint32_t x_dst0 = xr * 128 + (((2 * (l & 3) + swap) ^ xr) << 4);
+        const uint32_t x_dst1 = xr * 128 + (((2 * (l & 3) + 1 - swap) ^ xr) << 4);
+        uint32_t c = h;  // this half stage among all
+        Item it;
+        bool ok = true;
+        for (int i = item0; ok && walk.get(i, it); i += item_step) {
+            const int atoms = it.T / (kPair * 8);
+#pragma unroll 1
+            for (int k = 0; k < nk; ++k) {
+                const bool mine = 2 * k + h < nh;  // (the last stage may end after its first half)
+                if (!(ok = __all_sync(0xffffffffu, wait(at.full, at.phase, abort_flag)))) break;
+                if (mine) {
+                    const uint32_t s = c & h_mask;
+                    uint4 w[MATS][4];
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[m][j] = lds(at.stage + m * kTileW + wr * 128 + (((4 * h + j) ^ (wr & 7)) << 4));
+                    // the MMAs have read what this half stage held
+                    if (!(ok = __all_sync(0xffffffffu, wait(h_empty_addr + 8 * s, ((c >> h_log) & 1) ^ 1, abort_flag)))) break;
+                    tc::fence_after_sync();
+                    const uint32_t a = tmem + ((uint32_t)(32 * q) << 16) + g.a_col + s * (MATS * kK / 2);
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            uint32_t v[16];
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) {
+                                const uint2 f = codes_to_f16(word(w[m][j + (b >> 2)], b & 3));
+                                v[2 * b] = f.x;
+                                v[2 * b + 1] = f.y;
+                            }
+                            tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, v);
+                        }
+                    const uint32_t src = at.stage + MATS * kTileW + x_src, dst = f16_addr + s * g.half_bytes;
+#pragma unroll 2
+                    for (int t = q; t < atoms; t += 4) {
+                        const uint4 x = lds(src + t * 1024);
+                        const uint2 f0 = codes_to_f16(x.x), f1 = codes_to_f16(x.y), f2 = codes_to_f16(x.z), f3 = codes_to_f16(x.w);
+                        sts(dst + t * 1024 + x_dst0, swap ? f2 : f0, swap ? f3 : f1);
+                        sts(dst + t * 1024 + x_dst1, swap ? f0 : f2, swap ? f1 : f3);
+                    }
+                    tc::wait_st();
+                    tc::fence_async_shared();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) arrive_in_first(peer_full + 8 * s);
+                }
+                __syncwarp();
+                if (lane == 0) arrive(at.empty);
+                at.next(stages, stage_bytes);
+                if (mine) c += 2;
+            }
+            // the next tile begins with the first group of converters whatever this one ended with
+            if (nh & 1) c += h ? 1 : -1;
+        }
+        // the commits on the half stages have arrived before the CTA may end
+        if (warp == 0) {
+            const unsigned long long t0 = globaltimer();
+            for (uint32_t s = 0; ok && s < (uint32_t)g.halves; ++s)
+                if (c > s) settle(h_empty_addr + 8 * s, ((c - s - 1) >> h_log) & 1, t0);
+        }
+        __syncwarp();
+    } else if (warp >= kConvert && warp < kConvert + kEpilogue) {
+        // ---- epilogue ----------------------------------------------------------
+        store_tiles<T, MATS, true>(p, g, walk, item0, item_step, rank, tmem, warp - kConvert, acc_full_addr, acc_empty_addr,
+                                   abort_flag, row_scale[warp - kConvert]);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // neither CTA ends while the other may still use its memory
+    tc::fence_after_sync();
+    if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// rows of `cols` codes `ld` apart, `planes` of them (rank 3) or one (rank 2), boxes of
+// 128 columns x box_rows rows; what lies outside reads as zeros
+bool encode(CUtensorMap *m, const void *base, long long cols, long long rows, long long ld, int planes, long long stride,
+            int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const int rank = planes ? 3 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(planes ? planes : 1)};
+    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
+    cuuint32_t box[3] = {(cuuint32_t)kIn, (cuuint32_t)box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// what a launch needs to know of a device, looked up once
+struct Device {
+    std::atomic<int> pairs{0};       // CTA pairs that run at once
+    std::atomic<int> smem{0};        // dynamic shared memory a CTA may ask for
+    std::atomic<unsigned> ready{0};  // kernels whose shared-memory limit is raised
+};
+constexpr int kMaxDevices = 64;
+Device g_devices[kMaxDevices];
+
+// accumulator sets and half stages that fit tensor memory beside each other
+void share_tmem(int mats, Tiling &g) {
+    const int set = mats * g.tcap, half = mats * kK / 2;
+    g.bufs = 2 * set + 2 * half <= kTmemCols ? 2 : 1;
+    g.halves = g.bufs * set + 4 * half <= kTmemCols ? 4 : 2;
+    g.a_col = kTmemCols - g.halves * half;
+}
+
+// Rows per tile: the least time of a simple model, in cycles per 128 inputs, as in
+// ops_gemm.cu: the MMAs, shared memory at 128 bytes a cycle (128 x mats + half the rows in and
+// out of the converters, x written and read as f16), the converters.
+int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int pairs) {
+    const int mats = p.w_up ? 2 : 1;
+    const int per_row = 20 + 15 * (mats - 1) + (p.act != MOE_EPI_NONE ? 15 : 0) + (p.residual ? 15 : 0);
+    int best = kStepRows;
+    long long least = -1;
+    for (int cap = mats == 2 ? 192 : 256; cap >= kStepRows; cap -= kStepRows) {
+        Tiling g;
+        g.tcap = cap;
+        share_tmem(mats, g);
+        const int t = tile_rows(mean, cap);
+        const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
+        const long long waves = (items + pairs - 1) / pairs;
+        const long long step = max(max(4 * mats * t, 256 * mats + (2 + mats) * t), 200 * mats + t + 150);
+        const long long cost = waves * nk * step + per_row * t + (g.bufs == 1 ? waves * per_row * t / 2 : 0);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = cap;
+        }
+    }
+    return best;
+}
+
+cudaError_t look_up(int dev, Device &d) {
+    int smem = 0, sms = 0, pairs = 0;
+    cudaFuncAttributes fa;
+    cudaError_t err;
+    auto k = product_gemm_q8_kernel<__half, 2>;
+    if ((err = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (err = cudaFuncGetAttributes(&fa, k)) != cudaSuccess)
+        return err;
+    smem -= (int)((fa.sharedSizeBytes + 127) / 128 * 128);
+    if ((err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms / kPair * kPair);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((err = cudaOccupancyMaxActiveClusters(&pairs, k, &cfg)) != cudaSuccess) return err;
+    if (pairs < 1) return cudaErrorNotSupported;
+    d.smem.store(smem, std::memory_order_relaxed);
+    d.pairs.store(min(pairs, sms / kPair), std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <typename T, int MATS>
+cudaError_t launch(const Product &p, const Tiling &g, int pairs, int smem, Device &d, const CUtensorMap &tmx,
+                   const CUtensorMap &tmx_half, const CUtensorMap &tmw, const CUtensorMap &tmu, cudaStream_t st) {
+    auto k = product_gemm_q8_kernel<T, MATS>;
+    const unsigned bit = 1u << (MATS - 1 + (p.dtype == MOE_DTYPE_BF16 ? 2 : 0));
+    if (!(d.ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     d.smem.load(std::memory_order_relaxed));
+        if (err != cudaSuccess) return err;
+        d.ready.fetch_or(bit, std::memory_order_release);
+    }
+    return launch_overlapped(k, dim3(kPair * pairs), kThreads, smem, kPair, st, p, g, tmx, tmx_half, tmw, tmu);
+}
+
+}  // namespace
+
+cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    Device &d = g_devices[dev];
+    if (d.pairs.load(std::memory_order_acquire) == 0 && (err = look_up(dev, d)) != cudaSuccess) return err;
+    const int all = d.pairs.load(std::memory_order_acquire);
+    const int mats = p.w_up ? 2 : 1;
+    const int mblocks = (p.N + kPair * kM - 1) / (kPair * kM);
+    const int groups = p.offsets ? min(p.E, p.rows) : 1;
+    Tiling g;
+    g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all);
+    share_tmem(mats, g);
+    g.stage_bytes = mats * kTileW + box_rows(g.tcap / kPair) * kIn;
+    g.half_bytes = g.tcap / kPair * kK * 2;
+    g.mblocks = mblocks;
+    auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
+    g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
+    const int table = p.offsets ? p.E * 4 : 0;
+    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - g.halves * g.half_bytes;
+    g.stages = min(kMaxStages, budget / g.stage_bytes);
+    if (g.stages < 2) return cudaErrorNotSupported;
+    const int smem = 1024 + g.stages * g.stage_bytes + g.halves * g.half_bytes + table;
+    const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
+    // items are numbered in 32 bits, also where offsets that do not ascend give every
+    // expert all rows
+    if ((p.offsets ? p.E : 1) * ((p.rows + g.tcap - 1) / g.tcap) * (long long)mblocks > 0x7fff0000LL)
+        return cudaErrorNotSupported;
+    const int planes = p.stride_e ? p.E : 1;  // experts may share one matrix
+    alignas(64) CUtensorMap tmx, tmx_half, tmw, tmu;
+    if (!encode(&tmx, p.x, p.K, p.x_rows, p.ldx, 0, 0, p.row_token ? 1 : kBoxRows) ||
+        !encode(&tmx_half, p.x, p.K, p.x_rows, p.ldx, 0, 0, kBoxRows / 2) ||
+        !encode(&tmw, p.w, p.K, p.N, p.ldw, planes, p.stride_e ? p.stride_e : p.ldw, kM))
+        return cudaErrorNotSupported;
+    tmu = tmw;
+    if (mats == 2 && !encode(&tmu, p.w_up, p.K, p.N, p.ldw, planes, p.stride_e ? p.stride_e : p.ldw, kM))
+        return cudaErrorNotSupported;
+    const int n = (int)min(most, (long long)all);
+    if (p.dtype == MOE_DTYPE_BF16)
+        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
+                         : launch<__nv_bfloat16, 1>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
+    return mats == 2 ? launch<__half, 2>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
+                     : launch<__half, 1>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
+}
+
+unsigned *ops_status_q8(cudaError_t *err) {
+    void *at = nullptr;
+    *err = cudaGetSymbolAddress(&at, g_ops_status);
+    return static_cast<unsigned *>(at);
+}
+
+}  // namespace ops
+}  // namespace moe

@@ -73,11 +73,12 @@ cudaError_t launch_product_rows(const Product &p, cudaStream_t st);
 // many rows per expert: tcgen05 (ops_gemm.cu); cudaErrorNotSupported, with nothing
 // launched, where the driver declines a tensor map
 cudaError_t launch_product_gemm(const Product &p, cudaStream_t st);
-// the status word of the current device's operators, cleared if it was set
-cudaError_t read_ops_status(unsigned *value, cudaStream_t st);
-
 // the same for products of 8-bit codes (ops_rows_q8.cu, ops_gemm_q8.cu)
 cudaError_t launch_product_rows_q8(const Product &p, cudaStream_t st);
+cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st);
+// the status words of the current device's kernels with waits: set when one gave up
+unsigned *ops_status(cudaError_t *err);
+unsigned *ops_status_q8(cudaError_t *err);
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st);
 cudaError_t launch_quantize_rows(int dtype, const void *x, long long ldx, int n, int K, int8_t *codes, long long ldc,
