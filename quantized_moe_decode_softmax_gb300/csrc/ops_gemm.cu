@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kLoaders && warp < kMmaWarp) {
         // ---- epilogue ----------------------------------------------------------
-        store_tiles<T, MATS, false>(p, g, walk, item0, item_step, rank, tmem, warp - kLoaders, acc_full_addr, acc_empty_addr,
-                                    abort_flag, nullptr);
+        store_tiles<T, MATS, false>(p, g, OwnWalk{walk, item0, item_step}, rank, tmem, warp - kLoaders, acc_full_addr,
+                                    acc_empty_addr, abort_flag, nullptr);
     }
     tc::fence_before_sync();
     __syncthreads();

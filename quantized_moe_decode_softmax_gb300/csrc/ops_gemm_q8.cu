@@ -34,16 +34,17 @@ namespace {
 
 constexpr int kIn = 128;                 // inputs of a load stage: one 128-byte row of a swizzled tile
 constexpr int kTileW = kM * kIn;         // bytes of a weight tile
-constexpr int kMaxStages = 12, kMaxHalves = 4;
-constexpr int kConvert = 8;              // converter warps, two per quadrant of the tensor-memory lanes
+constexpr int kMaxStages = 12, kMinStages = 4, kHalves = 4;  // load stages; half stages as f16
+constexpr int kItems = 4;                // work items that the loads may be ahead
+constexpr int kGroups = 3;               // groups of four converter warps, one per quadrant of the tensor-memory lanes
+constexpr int kConvert = 4 * kGroups;
 constexpr int kLoadW = kConvert + kEpilogue, kLoadX = kLoadW + 1, kMmaWarp = kLoadX + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 
 struct Tiling : Tiles {
     int stages;
     int stage_bytes;
-    int halves;       // half stages as f16, 2 or 4
-    int half_bytes;   // shared memory of one: the rows of x
+    int half_bytes;   // shared memory of a half stage as f16: the rows of x
     int a_col;        // tensor memory: first column of the weights as f16
 };
 
@@ -117,6 +118,24 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint32_t b, 
         : "memory");
 }
 
+// The pair's items, as the weights' warp has found them. (To find one takes a thousand cycles of
+// divisions and dependent loads, longer than a short tile's conversions.)
+struct RingItems {
+    const Item *ring;
+    uint32_t full, empty;
+    volatile int *abort_flag;
+    uint32_t n;
+    __device__ __forceinline__ bool next(Item &it) {
+        const uint32_t s = n % kItems;
+        if (!__all_sync(0xffffffffu, wait(full + 8 * s, (n / kItems) & 1, abort_flag))) return false;
+        it = ring[s];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) arrive(empty + 8 * s);
+        ++n;
+        return it.T != 0;
+    }
+};
+
 template <typename T, int MATS>
 __global__ void __launch_bounds__(kThreads, 1)
     product_gemm_q8_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling g,
@@ -125,15 +144,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     // full, empty: load stages of this CTA. h_full (the first CTA's counts for both), h_empty: half
     // stages as f16. acc_empty: the first CTA's counts for both
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], h_full[kMaxHalves], h_empty[kMaxHalves];
-    __shared__ uint64_t acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], h_full[kHalves], h_empty[kHalves];
+    __shared__ uint64_t acc_full[2], acc_empty[2], item_full[kItems], item_empty[kItems], drain;
+    __shared__ Item item_ring[kItems];
     __shared__ uint32_t tslot;
     __shared__ int abort_word, warp_sum[kThreads / 32];
     __shared__ __align__(16) float row_scale[kEpilogue][128];
     volatile int *abort_flag = &abort_word;
     unsigned char *ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *f16_ring = ring + g.stages * g.stage_bytes;
-    int *first = reinterpret_cast<int *>(f16_ring + g.halves * g.half_bytes);
+    int *first = reinterpret_cast<int *>(f16_ring + kHalves * g.half_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
     const int item0 = blockIdx.x / kPair, item_step = gridDim.x / kPair;
@@ -142,15 +162,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort_word = 0;
         for (int i = 0; i < g.stages; ++i) {
             ptx::mbar_init(&full[i], 1);
-            ptx::mbar_init(&empty[i], kConvert);
+            ptx::mbar_init(&empty[i], 8);  // the warps that convert its two halves
         }
-        for (int i = 0; i < g.halves; ++i) {
-            ptx::mbar_init(&h_full[i], kConvert / 2 * kPair);
+        for (int i = 0; i < kHalves; ++i) {
+            ptx::mbar_init(&h_full[i], 4 * kPair);
             ptx::mbar_init(&h_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
             ptx::mbar_init(&acc_empty[i], kEpilogue * kPair);  // the epilogues' warps
+        }
+        for (int i = 0; i < kItems; ++i) {
+            ptx::mbar_init(&item_full[i], 1);
+            ptx::mbar_init(&item_empty[i], kConvert + kEpilogue + 1 + (rank == 0 ? 1 : 0));  // all but the weights' warp
         }
         ptx::mbar_init(&drain, 1);
         ptx::mbar_fence_init();
@@ -172,16 +196,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t f16_addr = tc::smem_u32(f16_ring), h_full_addr = tc::smem_u32(h_full), h_empty_addr = tc::smem_u32(h_empty);
     const uint32_t acc_full_addr = tc::smem_u32(acc_full), acc_empty_addr = tc::smem_u32(acc_empty);
     const Walk walk{p, g, first, total};
-    const int nk = (p.K + kIn - 1) / kIn, nh = (p.K + kK - 1) / kK;  // load stages and half stages of a tile
+    const int nk = (p.K + kIn - 1) / kIn, nh = 2 * nk;  // load stages and half stages of a tile (past K: zeros)
+    RingItems items{item_ring, tc::smem_u32(item_full), tc::smem_u32(item_empty), abort_flag, 0};
     const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
-    const uint32_t h_mask = g.halves - 1, h_log = g.halves == 4 ? 2 : 1;
 
     if (warp == kLoadW) {
         // ---- weights ------------------------------------------------------------
         Ring at{ring_addr, empty_addr, full_addr, 0, 1};  // a fresh barrier passes the wait for phase 1
         Item it;
         bool ok = true;
-        for (int i = item0; ok && walk.get(i, it); i += item_step) {
+        uint32_t n = 0;
+        for (int i = item0; ok; i += item_step, ++n) {
+            const bool more = walk.get(i, it);
+            const uint32_t slot = n % kItems;
+            if (!(ok = __all_sync(0xffffffffu, wait(items.empty + 8 * slot, ((n / kItems) & 1) ^ 1, abort_flag)))) break;
+            if (lane == 0) {
+                if (!more) it.T = 0;  // the end
+                item_ring[slot] = it;
+                arrive(items.full + 8 * slot);
+            }
+            __syncwarp();
+            if (!more) break;
             const int half = it.T / kPair;  // rows of x that this CTA loads
             const uint32_t bytes = MATS * kTileW + (p.row_token ? half : box_rows(half)) * kIn;
             const int col = (it.m * kPair + rank) * kM, plane = p.stride_e ? it.e : 0;
@@ -210,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring at{ring_addr + MATS * kTileW, empty_addr, full_addr, 0, 1};
         Item it;
         bool ok = true;
-        for (int i = item0; ok && walk.get(i, it); i += item_step) {
+        while (ok && items.next(it)) {
             const int half = it.T / kPair, r0 = it.r0 + rank * half;
             if (p.row_token) {
                 // lane j's rows are the j-th copy; rows past the end repeat the last one
@@ -243,23 +278,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
         // ---- MMAs --------------------------------------------------------------
-        if (tc::elect_one()) {
-            uint32_t c = 0;  // half stages so far
-            int n = 0;
-            Item it;
-            bool ok = true;
-            const uint32_t base = tc::idesc_f16_f32(kPair * kM, 0);
-            for (int i = item0; ok && walk.get(i, it); i += item_step, ++n) {
+        uint32_t c = 0;  // half stages so far
+        Item it;
+        bool ok = true;
+        const uint32_t base = tc::idesc_f16_f32(kPair * kM, 0);
+        for (int n = 0; ok && items.next(it); ++n) {
+            if (tc::elect_one()) {
                 const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
                 const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
                 const uint32_t acc = tmem + (uint32_t)(buf * MATS * g.tcap), acc_up = acc + g.tcap;
                 // the epilogues have read what this accumulator set held
-                if (!(ok = wait(acc_empty_addr + 8 * buf, (uint32_t)((use & 1) ^ 1), abort_flag))) break;
+                ok = wait(acc_empty_addr + 8 * buf, (uint32_t)((use & 1) ^ 1), abort_flag);
                 tc::fence_after_sync();
 #pragma unroll 1
-                for (int k = 0; k < nh; ++k, ++c) {
-                    const uint32_t s = c & h_mask;
-                    if (!(ok = wait_cluster(h_full_addr + 8 * s, (c >> h_log) & 1, abort_flag))) break;
+                for (int k = 0; ok && k < nh; ++k) {
+                    const uint32_t s = (c + k) % kHalves;
+                    if (!(ok = wait_cluster(h_full_addr + 8 * s, ((c + k) / kHalves) & 1, abort_flag))) break;
                     tc::fence_after_sync();
                     const uint32_t a = tmem + g.a_col + s * (MATS * kK / 2), b = desc_low(f16_addr + s * g.half_bytes);
                     // the first MMA of a tile overwrites
@@ -272,92 +306,106 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) commit_pair(acc_full_addr + 8 * buf);
             }
-            if (!ok) {  // let the MMAs in flight end before the tensor memory is freed
-                commit_pair(tc::smem_u32(&drain));
-                settle(tc::smem_u32(&drain), 0, globaltimer());
-            }
+            ok = __all_sync(0xffffffffu, ok);
+            c += nh;
+        }
+        // after an abort, let the MMAs in flight end before the tensor memory is freed
+        if (__any_sync(0xffffffffu, *abort_flag) && tc::elect_one()) {
+            commit_pair(tc::smem_u32(&drain));
+            settle(tc::smem_u32(&drain), 0, globaltimer());
         }
         __syncwarp();
     } else if (warp < kConvert) {
         // ---- codes to f16 --------------------------------------------------------
-        const int q = warp & 3, h = warp >> 2;  // quadrant of the lanes; half of a stage
-        Ring at{ring_addr, empty_addr, full_addr, 0, 0};
+        // The half stages of all tiles are dealt to the groups in turn. (No more groups than half
+        // stages: a group that skips one must not be two uses of it ahead.)
+        const int q = warp & 3;  // quadrant of the lanes
         const uint32_t peer_full = in_first(h_full_addr);
         const int wr = 32 * q + lane;  // this thread's weight row
+        uint32_t w_src[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w_src[j] = ring_addr + wr * 128 + ((j ^ (wr & 7)) << 4);  // (second half: bit 6 turned)
         // this thread's pieces of x: row and 16 codes of an atom of 8 rows. The lanes of a quarter
         // warp take rows r and r + 4 and write their two pieces in turn, which keeps them on
         // different banks
         const int l = lane & 7, xr = (lane >> 3) + 4 * (l >> 2), swap = l >> 2;
-        const uint32_t x_src = xr * 128 + (((4 * h + (l & 3)) ^ xr) << 4);
-        const uint32_t x_dst0 = xr * 128 + (((2 * (l & 3) + swap) ^ xr) << 4);
-        const uint32_t x_dst1 = xr * 128 + (((2 * (l & 3) + 1 - swap) ^ xr) << 4);
-        uint32_t c = h;  // this half stage among all
-        Item it;
+        const uint32_t x_src = ring_addr + MATS * kTileW + q * 1024 + xr * 128 + (((l & 3) ^ xr) << 4);
+        const uint32_t x_dst0 = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3) + swap) ^ xr) << 4);
+        const uint32_t x_dst1 = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3) + 1 - swap) ^ xr) << 4);
+        const uint32_t a_at = tmem + ((uint32_t)(32 * q) << 16) + g.a_col;
+        uint32_t c = warp >> 2;        // this group's half stage
+        uint32_t slot = c >> 1, phase = 0;  // its load stage in the ring, and the lap
+        uint32_t end = 0;              // half stages of the tiles so far
+        int atoms = 0;                 // this warp's of the tile: every fourth
         bool ok = true;
-        for (int i = item0; ok && walk.get(i, it); i += item_step) {
-            const int atoms = it.T / (kPair * 8);
+        Item it;
+        while ((ok = items.next(it))) {
+            end += nh;
+            atoms = it.T / (kPair * 8) - q;
 #pragma unroll 1
-            for (int k = 0; k < nk; ++k) {
-                const bool mine = 2 * k + h < nh;  // (the last stage may end after its first half)
-                if (!(ok = __all_sync(0xffffffffu, wait(at.full, at.phase, abort_flag)))) break;
-                if (mine) {
-                    const uint32_t s = c & h_mask;
-                    uint4 w[MATS][4];
+            for (; c < end; c += kGroups) {
+                const uint32_t h = (c & 1) << 6, s = c % kHalves, stage = slot * stage_bytes;
+                if (!(ok = __all_sync(0xffffffffu, wait(full_addr + 8 * slot, phase, abort_flag)))) break;
+                uint4 w[MATS][4], x[4];
 #pragma unroll
-                    for (int m = 0; m < MATS; ++m)
+                for (int m = 0; m < MATS; ++m)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[m][j] = lds(at.stage + m * kTileW + wr * 128 + (((4 * h + j) ^ (wr & 7)) << 4));
-                    // the MMAs have read what this half stage held
-                    if (!(ok = __all_sync(0xffffffffu, wait(h_empty_addr + 8 * s, ((c >> h_log) & 1) ^ 1, abort_flag)))) break;
-                    tc::fence_after_sync();
-                    const uint32_t a = tmem + ((uint32_t)(32 * q) << 16) + g.a_col + s * (MATS * kK / 2);
+                    for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ h);
 #pragma unroll
-                    for (int m = 0; m < MATS; ++m)
+                for (int j = 0; j < 4; ++j)
+                    if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ h);
+                // the MMAs have read what this half stage held
+                if (!(ok = __all_sync(0xffffffffu, wait(h_empty_addr + 8 * s, ((c / kHalves) & 1) ^ 1, abort_flag)))) break;
+                tc::fence_after_sync();
+                const uint32_t a = a_at + s * (MATS * kK / 2), dst = s * g.half_bytes;
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
-                            uint32_t v[16];
+                for (int m = 0; m < MATS; ++m)
 #pragma unroll
-                            for (int b = 0; b < 8; ++b) {
-                                const uint2 f = codes_to_f16(word(w[m][j + (b >> 2)], b & 3));
-                                v[2 * b] = f.x;
-                                v[2 * b + 1] = f.y;
-                            }
-                            tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, v);
+                    for (int j = 0; j < 4; j += 2) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const uint2 f = codes_to_f16(word(w[m][j + (b >> 2)], b & 3));
+                            v[2 * b] = f.x;
+                            v[2 * b + 1] = f.y;
                         }
-                    const uint32_t src = at.stage + MATS * kTileW + x_src, dst = f16_addr + s * g.half_bytes;
-#pragma unroll 2
-                    for (int t = q; t < atoms; t += 4) {
-                        const uint4 x = lds(src + t * 1024);
-                        const uint2 f0 = codes_to_f16(x.x), f1 = codes_to_f16(x.y), f2 = codes_to_f16(x.z), f3 = codes_to_f16(x.w);
-                        sts(dst + t * 1024 + x_dst0, swap ? f2 : f0, swap ? f3 : f1);
-                        sts(dst + t * 1024 + x_dst1, swap ? f0 : f2, swap ? f1 : f3);
+                        tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, v);
                     }
-                    tc::wait_st();
-                    tc::fence_async_shared();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) arrive_in_first(peer_full + 8 * s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (4 * j >= atoms) break;
+                    const uint2 f0 = codes_to_f16(x[j].x), f1 = codes_to_f16(x[j].y), f2 = codes_to_f16(x[j].z),
+                                f3 = codes_to_f16(x[j].w);
+                    sts(dst + j * 4096 + x_dst0, swap ? f2 : f0, swap ? f3 : f1);
+                    sts(dst + j * 4096 + x_dst1, swap ? f0 : f2, swap ? f1 : f3);
                 }
+                tc::wait_st();
+                tc::fence_async_shared();
+                tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive(at.empty);
-                at.next(stages, stage_bytes);
-                if (mine) c += 2;
+                if (lane == 0) {
+                    arrive_in_first(peer_full + 8 * s);
+                    arrive(empty_addr + 8 * slot);
+                }
+                slot += ((c + kGroups) >> 1) - (c >> 1);
+                if (slot >= stages) {
+                    slot -= stages;
+                    phase ^= 1;
+                }
             }
-            // the next tile begins with the first group of converters whatever this one ended with
-            if (nh & 1) c += h ? 1 : -1;
+            if (!ok) break;
         }
         // the commits on the half stages have arrived before the CTA may end
         if (warp == 0) {
             const unsigned long long t0 = globaltimer();
-            for (uint32_t s = 0; ok && s < (uint32_t)g.halves; ++s)
-                if (c > s) settle(h_empty_addr + 8 * s, ((c - s - 1) >> h_log) & 1, t0);
+            for (uint32_t s = 0; s < kHalves; ++s)
+                if (end > s) settle(h_empty_addr + 8 * s, ((end - s - 1) / kHalves) & 1, t0);
         }
         __syncwarp();
     } else if (warp >= kConvert && warp < kConvert + kEpilogue) {
         // ---- epilogue ----------------------------------------------------------
-        store_tiles<T, MATS, true>(p, g, walk, item0, item_step, rank, tmem, warp - kConvert, acc_full_addr, acc_empty_addr,
-                                   abort_flag, row_scale[warp - kConvert]);
+        store_tiles<T, MATS, true>(p, g, items, rank, tmem, warp - kConvert, acc_full_addr, acc_empty_addr, abort_flag,
+                                   row_scale[warp - kConvert]);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -391,13 +439,11 @@ struct Device {
 constexpr int kMaxDevices = 64;
 Device g_devices[kMaxDevices];
 
-// accumulator sets and half stages that fit tensor memory beside each other
-void share_tmem(int mats, Tiling &g) {
-    const int set = mats * g.tcap, half = mats * kK / 2;
-    g.bufs = 2 * set + 2 * half <= kTmemCols ? 2 : 1;
-    g.halves = g.bufs * set + 4 * half <= kTmemCols ? 4 : 2;
-    g.a_col = kTmemCols - g.halves * half;
-}
+// tensor memory: kHalves half stages of weights as f16 at the end, one or two accumulator sets
+constexpr int a_col(int mats) { return kTmemCols - kHalves * mats * kK / 2; }
+constexpr int max_rows(int mats) { return mats == 2 ? 128 : 256; }
+static_assert(kGroups <= kHalves, "see the converters");
+static_assert(max_rows(1) <= a_col(1) && 2 * max_rows(2) <= a_col(2), "an accumulator set fits");
 
 // Rows per tile: the least time of a simple model, in cycles per 128 inputs, as in
 // ops_gemm.cu: the MMAs, shared memory at 128 bytes a cycle (128 x mats + half the rows in and
@@ -407,15 +453,13 @@ int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int p
     const int per_row = 20 + 15 * (mats - 1) + (p.act != MOE_EPI_NONE ? 15 : 0) + (p.residual ? 15 : 0);
     int best = kStepRows;
     long long least = -1;
-    for (int cap = mats == 2 ? 192 : 256; cap >= kStepRows; cap -= kStepRows) {
-        Tiling g;
-        g.tcap = cap;
-        share_tmem(mats, g);
+    for (int cap = max_rows(mats); cap >= kStepRows; cap -= kStepRows) {
         const int t = tile_rows(mean, cap);
         const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
         const long long waves = (items + pairs - 1) / pairs;
         const long long step = max(max(4 * mats * t, 256 * mats + (2 + mats) * t), 200 * mats + t + 150);
-        const long long cost = waves * nk * step + per_row * t + (g.bufs == 1 ? waves * per_row * t / 2 : 0);
+        const bool one_set = 2 * mats * cap > a_col(mats);
+        const long long cost = waves * nk * step + per_row * t + (one_set ? waves * per_row * t / 2 : 0);
         if (least < 0 || cost < least) {
             least = cost;
             best = cap;
@@ -481,17 +525,18 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
     Tiling g;
     g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all);
-    share_tmem(mats, g);
+    g.a_col = a_col(mats);
+    g.bufs = 2 * mats * g.tcap <= g.a_col ? 2 : 1;
     g.stage_bytes = mats * kTileW + box_rows(g.tcap / kPair) * kIn;
     g.half_bytes = g.tcap / kPair * kK * 2;
     g.mblocks = mblocks;
     auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
     g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
     const int table = p.offsets ? p.E * 4 : 0;
-    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - g.halves * g.half_bytes;
+    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - kHalves * g.half_bytes;
     g.stages = min(kMaxStages, budget / g.stage_bytes);
-    if (g.stages < 2) return cudaErrorNotSupported;
-    const int smem = 1024 + g.stages * g.stage_bytes + g.halves * g.half_bytes + table;
+    if (g.stages < kMinStages) return cudaErrorNotSupported;
+    const int smem = 1024 + g.stages * g.stage_bytes + kHalves * g.half_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     // items are numbered in 32 bits, also where offsets that do not ascend give every
     // expert all rows

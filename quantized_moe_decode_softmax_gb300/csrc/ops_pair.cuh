@@ -255,6 +255,17 @@ struct Walk {
     }
 };
 
+// The items of one pair, each role walking for itself.
+struct OwnWalk {
+    const Walk &walk;
+    int i, step;
+    __device__ __forceinline__ bool next(Item &it) {
+        const bool more = walk.get(i, it);
+        i += step;
+        return more;
+    }
+};
+
 // The first item of each group (`first`, shared memory) and the number of all items, by a
 // block of THREADS threads; without groups no table. warp_sum: THREADS / 32 numbers.
 template <int THREADS>
@@ -300,18 +311,19 @@ __device__ __forceinline__ int number_items(const Product &p, const Tiles &g, in
 
 // The epilogue of a pair's tiles, by warp w of kEpilogue (and lane quadrant w % 4 of tensor
 // memory). SCALED: sums of 8-bit codes, to be multiplied by the scale of their row (row_scale:
-// 128 floats of shared memory of this warp) and of their column.
-template <typename T, int MATS, bool SCALED>
-__device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, const Walk &walk, int item0, int item_step,
-                                            int rank, uint32_t tmem, int w, uint32_t acc_full_addr,
-                                            uint32_t acc_empty_addr, volatile int *abort_flag, float *row_scale) {
+// 128 floats of shared memory of this warp) and of their column. items: next(it) gives the
+// pair's items in turn.
+template <typename T, int MATS, bool SCALED, typename Items>
+__device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, Items items, int rank, uint32_t tmem, int w,
+                                            uint32_t acc_full_addr, uint32_t acc_empty_addr, volatile int *abort_flag,
+                                            float *row_scale) {
     const int lane = threadIdx.x & 31;
     const int q = w & 3;      // the lanes this warp can read
     const int part = w >> 2;  // its half of the tile's chunks of 16 rows
     const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
     int n = 0;
     Item it;
-    for (int i = item0; walk.get(i, it); i += item_step, ++n) {
+    for (; items.next(it); ++n) {
         const int c = (it.m * kPair + rank) * kM + 32 * q + lane;
         const bool mine = c < p.N;
         float b0 = 0.f, b1 = 0.f;
@@ -342,10 +354,10 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, co
         const long long c_first = g.paired ? c - odd : c, r_first = it.r0 + (g.paired ? odd : 0);
         if (res) res += 2 * (r_first * p.ldr + c_first);
         out += 2 * (r_first * p.ldo + c_first);
-        // a residual is read two chunks ahead, the first two before the tile is done;
-        // the values stay as loaded until they are used, so that nothing waits for
-        // them earlier
-        uint32_t ra[16], rb[16];
+        // a residual is read two chunks ahead, the first two before the tile is done (SCALED,
+        // where more warps share the registers: one); the values stay as loaded until they
+        // are used, so that nothing waits for them earlier
+        uint32_t ra[16], rb[SCALED ? 1 : 16];
         auto load_res = [&](uint32_t (&d)[16], int t0) {
             const char *s = res + 2 * (size_t)t0 * p.ldr;
             if (g.paired) {
@@ -360,7 +372,7 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, co
         };
         if (res) {
             load_res(ra, 16 * part);
-            load_res(rb, 16 * part + 32);
+            if constexpr (!SCALED) load_res(rb, 16 * part + 32);
         }
         const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
         if (!__all_sync(0xffffffffu, wait(acc_full_addr + 8 * buf, (uint32_t)(use & 1), abort_flag))) break;
@@ -417,7 +429,7 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, co
                     v[2 * j] += f.x;
                     v[2 * j + 1] += f.y;
                 }
-                load_res(r, t0 + 64);
+                load_res(r, t0 + (SCALED ? 32 : 64));
             }
             char *o = out + 2 * (size_t)t0 * p.ldo;
             if (g.paired) {
@@ -436,7 +448,11 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, co
 #pragma unroll 1
         for (int t0 = 16 * part; t0 < it.rows; t0 += 64) {
             chunk(t0, ra);
-            if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
+            if constexpr (SCALED) {
+                if (t0 + 32 < it.rows) chunk(t0 + 32, ra);
+            } else {
+                if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
+            }
         }
         if (16 * part >= it.rows) done_reading();  // a tile of at most 16 rows has no chunk for the other half
     }
