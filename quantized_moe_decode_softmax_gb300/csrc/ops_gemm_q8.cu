@@ -38,7 +38,8 @@ constexpr int kMaxStages = 12, kMinStages = 4, kHalves = 4;  // load stages; hal
 constexpr int kItems = 4;                // work items that the loads may be ahead
 constexpr int kGroups = 3;               // groups of four converter warps, one per quadrant of the tensor-memory lanes
 constexpr int kConvert = 4 * kGroups;
-constexpr int kLoadW = kConvert + kEpilogue, kLoadX = kLoadW + 1, kMmaWarp = kLoadX + 1;
+constexpr int kXWarps = 2;               // load warps for x
+constexpr int kLoadW = kConvert + kEpilogue, kLoadX = kLoadW + 1, kMmaWarp = kLoadX + kXWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 
 struct Tiling : Tiles {
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             ptx::mbar_init(&item_full[i], 1);
-            ptx::mbar_init(&item_empty[i], kConvert + kEpilogue + 1 + (rank == 0 ? 1 : 0));  // all but the weights' warp
+            ptx::mbar_init(&item_empty[i], kConvert + kEpilogue + kXWarps + (rank == 0 ? 1 : 0));  // all but the weights' warp
         }
         ptx::mbar_init(&drain, 1);
         ptx::mbar_fence_init();
@@ -240,27 +241,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             settle(empty_addr + 8 * i, next, t0);
         }
         __syncwarp();
-    } else if (warp == kLoadX) {
+    } else if (warp >= kLoadX && warp < kLoadX + kXWarps) {
         // ---- rows of x ------------------------------------------------------------
+        // Gathered rows: every warp issues every second copy of four rows. Boxes: the first warp. (Not
+        // in turn: stages are handed back out of order, and a warp that skips some could take
+        // the phase of the lap before the last for the last.)
         Ring at{ring_addr + MATS * kTileW, empty_addr, full_addr, 0, 1};
+        const int w = warp - kLoadX;
         Item it;
         bool ok = true;
         while (ok && items.next(it)) {
             const int half = it.T / kPair, r0 = it.r0 + rank * half;
             if (p.row_token) {
-                // lane j's rows are the j-th copy; rows past the end repeat the last one
+                // lane j's rows are the warp's j-th copy; rows past the end repeat the last one
+                const int copies = (half / 4 - w + kXWarps - 1) / kXWarps, first_row = 4 * (w + kXWarps * lane);
                 int rows[4] = {};
-                if (lane < half / 4) {
+                if (lane < copies) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) rows[j] = input_row(p, min(r0 + 4 * lane + j, it.r0 + it.rows - 1));
+                    for (int j = 0; j < 4; ++j) rows[j] = input_row(p, min(r0 + first_row + j, it.r0 + it.rows - 1));
                 }
 #pragma unroll 1
                 for (int k = 0; k < nk; ++k) {
                     if (!(ok = __all_sync(0xffffffffu, wait(at.empty, at.phase, abort_flag)))) break;
-                    if (lane < half / 4) load_gather4(at.stage + lane * 512, &tmx, k * kIn, rows, at.full);
+                    if (lane < copies) load_gather4(at.stage + first_row * kIn, &tmx, k * kIn, rows, at.full);
                     at.next(stages, stage_bytes);
                 }
-            } else {
+            } else if (w == 0) {
                 // two boxes of x at most: the last one is half as high if that is enough
                 const int n1 = half > kBoxRows ? (half - kBoxRows > kBoxRows / 2 ? 2 : 1) : 0;
                 const CUtensorMap *map0 = half > kBoxRows / 2 ? &tmx : &tmx_half, *map1 = n1 == 2 ? &tmx : &tmx_half;
