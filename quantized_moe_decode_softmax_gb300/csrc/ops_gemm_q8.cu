@@ -34,17 +34,18 @@ namespace {
 
 constexpr int kIn = 128;                 // inputs of a load stage: one 128-byte row of a swizzled tile
 constexpr int kTileW = kM * kIn;         // bytes of a weight tile
-constexpr int kMaxStages = 12, kMinStages = 4, kHalves = 4;  // load stages; half stages as f16
+constexpr int kMaxStages = 12;           // load stages
+constexpr int kUnits = 4;                // hand-overs to the MMAs in flight: half stages, or stages
 constexpr int kItems = 4;                // work items that the loads may be ahead
 constexpr int kGroups = 3;               // groups of four converter warps, one per quadrant of the tensor-memory lanes
 constexpr int kConvert = 4 * kGroups;
-constexpr int kXWarps = 2;               // load warps for x
-constexpr int kLoadW = kConvert + kEpilogue, kLoadX = kLoadW + 1, kMmaWarp = kLoadX + kXWarps;
+constexpr int kLoadW = kConvert + kEpilogue, kLoadX = kLoadW + 1, kWalker = kLoadX + 1, kMmaWarp = kWalker + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 
 struct Tiling : Tiles {
     int stages;
     int stage_bytes;
+    int wide;         // a unit handed to the MMAs is a whole load stage (1) or half of one (0)
     int half_bytes;   // shared memory of a half stage as f16: the rows of x
     int a_col;        // tensor memory: first column of the weights as f16
 };
@@ -90,23 +91,6 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __forceinline__ void arrive_in_first(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// wait for what the peer's threads have arrived on, too
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    if (try_wait_cluster(bar, parity)) return true;
-    return wait_more(bar, parity, abort_flag) && try_wait_cluster(bar, parity);
-}
-
 // D[tmem of both CTAs] (+)= A * B^T: each CTA's tensor memory holds its 128 rows of A, its
 // shared memory half of B's rows; issued by one thread of the first CTA
 __device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
@@ -119,7 +103,7 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint32_t b, 
         : "memory");
 }
 
-// The pair's items, as the weights' warp has found them. (To find one takes a thousand cycles of
+// The pair's items, as one warp has found them. (To find one takes a thousand cycles of
 // divisions and dependent loads, longer than a short tile's conversions.)
 struct RingItems {
     const Item *ring;
@@ -143,9 +127,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmx_half,
                            const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmu) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    // full, empty: load stages of this CTA. h_full (the first CTA's counts for both), h_empty: half
-    // stages as f16. acc_empty: the first CTA's counts for both
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], h_full[kHalves], h_empty[kHalves];
+    // full, empty: load stages of this CTA. u_full (the first CTA's counts for both), u_empty: units.
+    // acc_empty: the first CTA's counts for both
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], u_full[kUnits], u_empty[kUnits];
     __shared__ uint64_t acc_full[2], acc_empty[2], item_full[kItems], item_empty[kItems], drain;
     __shared__ Item item_ring[kItems];
     __shared__ uint32_t tslot;
@@ -154,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &abort_word;
     unsigned char *ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *f16_ring = ring + g.stages * g.stage_bytes;
-    int *first = reinterpret_cast<int *>(f16_ring + kHalves * g.half_bytes);
+    int *first = reinterpret_cast<int *>(f16_ring + (kUnits << g.wide) * g.half_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
     const int item0 = blockIdx.x / kPair, item_step = gridDim.x / kPair;
@@ -165,9 +149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&full[i], 1);
             ptx::mbar_init(&empty[i], 8);  // the warps that convert its two halves
         }
-        for (int i = 0; i < kHalves; ++i) {
-            ptx::mbar_init(&h_full[i], 4 * kPair);
-            ptx::mbar_init(&h_empty[i], 1);
+        for (int i = 0; i < kUnits; ++i) {
+            ptx::mbar_init(&u_full[i], (4 << g.wide) * kPair);
+            ptx::mbar_init(&u_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
@@ -175,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             ptx::mbar_init(&item_full[i], 1);
-            ptx::mbar_init(&item_empty[i], kConvert + kEpilogue + kXWarps + (rank == 0 ? 1 : 0));  // all but the weights' warp
+            ptx::mbar_init(&item_empty[i], kConvert + kEpilogue + 2 + (rank == 0 ? 1 : 0));  // all but the walker
         }
         ptx::mbar_init(&drain, 1);
         ptx::mbar_fence_init();
@@ -194,30 +178,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = tslot;
     const uint32_t ring_addr = tc::smem_u32(ring), full_addr = tc::smem_u32(full), empty_addr = tc::smem_u32(empty);
-    const uint32_t f16_addr = tc::smem_u32(f16_ring), h_full_addr = tc::smem_u32(h_full), h_empty_addr = tc::smem_u32(h_empty);
+    const uint32_t f16_addr = tc::smem_u32(f16_ring), u_full_addr = tc::smem_u32(u_full), u_empty_addr = tc::smem_u32(u_empty);
     const uint32_t acc_full_addr = tc::smem_u32(acc_full), acc_empty_addr = tc::smem_u32(acc_empty);
     const Walk walk{p, g, first, total};
     const int nk = (p.K + kIn - 1) / kIn, nh = 2 * nk;  // load stages and half stages of a tile (past K: zeros)
     RingItems items{item_ring, tc::smem_u32(item_full), tc::smem_u32(item_empty), abort_flag, 0};
     const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
+    const uint32_t wide = MATS == 1 ? g.wide : 0;
 
     if (warp == kLoadW) {
         // ---- weights ------------------------------------------------------------
         Ring at{ring_addr, empty_addr, full_addr, 0, 1};  // a fresh barrier passes the wait for phase 1
         Item it;
         bool ok = true;
-        uint32_t n = 0;
-        for (int i = item0; ok; i += item_step, ++n) {
-            const bool more = walk.get(i, it);
-            const uint32_t slot = n % kItems;
-            if (!(ok = __all_sync(0xffffffffu, wait(items.empty + 8 * slot, ((n / kItems) & 1) ^ 1, abort_flag)))) break;
-            if (lane == 0) {
-                if (!more) it.T = 0;  // the end
-                item_ring[slot] = it;
-                arrive(items.full + 8 * slot);
-            }
-            __syncwarp();
-            if (!more) break;
+        while (ok && items.next(it)) {
             const int half = it.T / kPair;  // rows of x that this CTA loads
             const uint32_t bytes = MATS * kTileW + (p.row_token ? half : box_rows(half)) * kIn;
             const int col = (it.m * kPair + rank) * kM, plane = p.stride_e ? it.e : 0;
@@ -241,20 +215,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             settle(empty_addr + 8 * i, next, t0);
         }
         __syncwarp();
-    } else if (warp >= kLoadX && warp < kLoadX + kXWarps) {
-        // ---- rows of x ------------------------------------------------------------
-        // Gathered rows: every warp issues every second copy of four rows. Boxes: the first warp. (Not
-        // in turn: stages are handed back out of order, and a warp that skips some could take
-        // the phase of the lap before the last for the last.)
+    } else if (warp == kLoadX || warp == kWalker) {
+        // ---- rows of x; the walk over the items -----------------------------------------
+        // Boxes are loaded by the first warp, gathered rows by both (every second copy of four
+        // rows: a warp issues them one after another) unless tiles are the shortest.
+        // (A warp that loads takes part in every stage: they are handed back out of order, and
+        // one that skips some could take the phase of the lap before the last for the last.)
         Ring at{ring_addr + MATS * kTileW, empty_addr, full_addr, 0, 1};
         const int w = warp - kLoadX;
         Item it;
         bool ok = true;
-        while (ok && items.next(it)) {
+        uint32_t n = 0;
+        for (int i = item0; ok; i += item_step, ++n) {
+            if (w) {
+                const bool more = walk.get(i, it);
+                const uint32_t slot = n % kItems;
+                if (!(ok = __all_sync(0xffffffffu, wait(items.empty + 8 * slot, ((n / kItems) & 1) ^ 1, abort_flag)))) break;
+                if (lane == 0) {
+                    if (!more) it.T = 0;  // the end
+                    item_ring[slot] = it;
+                    arrive(items.full + 8 * slot);
+                }
+                __syncwarp();
+                if (!more) break;
+            } else if (!items.next(it)) {
+                break;
+            }
             const int half = it.T / kPair, r0 = it.r0 + rank * half;
             if (p.row_token) {
                 // lane j's rows are the warp's j-th copy; rows past the end repeat the last one
-                const int copies = (half / 4 - w + kXWarps - 1) / kXWarps, first_row = 4 * (w + kXWarps * lane);
+                const int warps = g.tcap > kStepRows ? 2 : 1, copies = (half / 4 - w + warps - 1) / warps;
+                if (w >= warps) continue;
+                const int first_row = 4 * (w + warps * lane);
                 int rows[4] = {};
                 if (lane < copies) {
 #pragma unroll
@@ -284,10 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp && rank == 0) {
         // ---- MMAs --------------------------------------------------------------
-        uint32_t c = 0;  // half stages so far
+        uint32_t c = 0;  // units so far
         Item it;
         bool ok = true;
         const uint32_t base = tc::idesc_f16_f32(kPair * kM, 0);
+        const int units = nh >> wide;  // of a tile
         for (int n = 0; ok && items.next(it); ++n) {
             if (tc::elect_one()) {
                 const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
@@ -297,23 +290,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(acc_empty_addr + 8 * buf, (uint32_t)((use & 1) ^ 1), abort_flag);
                 tc::fence_after_sync();
 #pragma unroll 1
-                for (int k = 0; ok && k < nh; ++k) {
-                    const uint32_t s = (c + k) % kHalves;
-                    if (!(ok = wait_cluster(h_full_addr + 8 * s, ((c + k) / kHalves) & 1, abort_flag))) break;
+                for (int k = 0; ok && k < units; ++k) {
+                    const uint32_t u = (c + k) % kUnits;
+                    if (!(ok = wait(u_full_addr + 8 * u, ((c + k) / kUnits) & 1, abort_flag))) break;
                     tc::fence_after_sync();
-                    const uint32_t a = tmem + g.a_col + s * (MATS * kK / 2), b = desc_low(f16_addr + s * g.half_bytes);
+                    uint32_t a = tmem + g.a_col + (u << wide) * (MATS * kK / 2);
+                    uint32_t b = desc_low(f16_addr + (u << wide) * g.half_bytes);
                     // the first MMA of a tile overwrites
 #pragma unroll
                     for (int q = 0; q < kK / 16; ++q) {
                         mma_pair_ts(acc, a + 8 * q, b + 2 * q, idesc, q ? 1 : k);
                         if (MATS == 2) mma_pair_ts(acc_up, a + kK / 2 + 8 * q, b + 2 * q, idesc, q ? 1 : k);
                     }
-                    commit_pair(h_empty_addr + 8 * s);
+                    if (MATS == 1 && wide) {
+                        a += kK / 2;
+                        b += g.half_bytes >> 4;
+#pragma unroll
+                        for (int q = 0; q < kK / 16; ++q) mma_pair_ts(acc, a + 8 * q, b + 2 * q, idesc, 1);
+                    }
+                    commit_pair(u_empty_addr + 8 * u);
                 }
                 if (ok) commit_pair(acc_full_addr + 8 * buf);
             }
             ok = __all_sync(0xffffffffu, ok);
-            c += nh;
+            c += units;
         }
         // after an abort, let the MMAs in flight end before the tensor memory is freed
         if (__any_sync(0xffffffffu, *abort_flag) && tc::elect_one()) {
@@ -323,10 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp < kConvert) {
         // ---- codes to f16 --------------------------------------------------------
-        // The half stages of all tiles are dealt to the groups in turn. (No more groups than half
-        // stages: a group that skips one must not be two uses of it ahead.)
+        // The half stages of all tiles are dealt to the groups in turn. (A wait takes a barrier two
+        // phases behind for one that is done. None is: this group's last half stage, c - 3, began
+        // once the MMAs of half stage c - 7 had ended (wide: of the load stage six back). That is
+        // after the last use but one of the unit's place, and after the last fill of the stage if
+        // there are at least 4 stages (6).)
         const int q = warp & 3;  // quadrant of the lanes
-        const uint32_t peer_full = in_first(h_full_addr);
+        const uint32_t peer_full = in_first(u_full_addr);
         const int wr = 32 * q + lane;  // this thread's weight row
         uint32_t w_src[4];
 #pragma unroll
@@ -350,32 +353,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             atoms = it.T / (kPair * 8) - q;
 #pragma unroll 1
             for (; c < end; c += kGroups) {
-                const uint32_t h = (c & 1) << 6, s = c % kHalves, stage = slot * stage_bytes;
+                const uint32_t turn = (c & 1) << 6, v = c >> wide, u = v % kUnits, stage = slot * stage_bytes;
                 if (!(ok = __all_sync(0xffffffffu, wait(full_addr + 8 * slot, phase, abort_flag)))) break;
                 uint4 w[MATS][4], x[4];
 #pragma unroll
                 for (int m = 0; m < MATS; ++m)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ h);
+                    for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ turn);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ h);
-                // the MMAs have read what this half stage held
-                if (!(ok = __all_sync(0xffffffffu, wait(h_empty_addr + 8 * s, ((c / kHalves) & 1) ^ 1, abort_flag)))) break;
+                    if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ turn);
+                // the MMAs have read what this unit held
+                if (!(ok = __all_sync(0xffffffffu, wait(u_empty_addr + 8 * u, ((v / kUnits) & 1) ^ 1, abort_flag)))) break;
                 tc::fence_after_sync();
-                const uint32_t a = a_at + s * (MATS * kK / 2), dst = s * g.half_bytes;
+                const uint32_t at = c & ((kUnits << wide) - 1), a = a_at + at * (MATS * kK / 2), dst = at * g.half_bytes;
 #pragma unroll
                 for (int m = 0; m < MATS; ++m)
 #pragma unroll
                     for (int j = 0; j < 4; j += 2) {
-                        uint32_t v[16];
+                        uint32_t f16[16];
 #pragma unroll
                         for (int b = 0; b < 8; ++b) {
                             const uint2 f = codes_to_f16(word(w[m][j + (b >> 2)], b & 3));
-                            v[2 * b] = f.x;
-                            v[2 * b + 1] = f.y;
+                            f16[2 * b] = f.x;
+                            f16[2 * b + 1] = f.y;
                         }
-                        tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, v);
+                        tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, f16);
                     }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive_in_first(peer_full + 8 * s);
+                    arrive_in_first(peer_full + 8 * u);
                     arrive(empty_addr + 8 * slot);
                 }
                 slot += ((c + kGroups) >> 1) - (c >> 1);
@@ -401,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
         }
-        // the commits on the half stages have arrived before the CTA may end
+        // the commits on the units have arrived before the CTA may end
         if (warp == 0) {
             const unsigned long long t0 = globaltimer();
-            for (uint32_t s = 0; s < kHalves; ++s)
-                if (end > s) settle(h_empty_addr + 8 * s, ((end - s - 1) / kHalves) & 1, t0);
+            for (uint32_t u = 0; u < kUnits; ++u)
+                if ((end >> wide) > u) settle(u_empty_addr + 8 * u, (((end >> wide) - u - 1) / kUnits) & 1, t0);
         }
         __syncwarp();
     } else if (warp >= kConvert && warp < kConvert + kEpilogue) {
@@ -445,11 +448,15 @@ struct Device {
 constexpr int kMaxDevices = 64;
 Device g_devices[kMaxDevices];
 
-// tensor memory: kHalves half stages of weights as f16 at the end, one or two accumulator sets
-constexpr int a_col(int mats) { return kTmemCols - kHalves * mats * kK / 2; }
+// Tensor memory beside the accumulator sets: kUnits units of weights as f16. A unit is a whole
+// load stage where that leaves room for two sets (short tiles: half as many hand-overs, 64 tokens
+// down 49 to 45 us), otherwise half of one (long ones: 8192x4096x4096 152 us, 169 in two units).
+constexpr int half_cols(int mats) { return mats * kK / 2; }
 constexpr int max_rows(int mats) { return mats == 2 ? 128 : 256; }
-static_assert(kGroups <= kHalves, "see the converters");
-static_assert(max_rows(1) <= a_col(1) && 2 * max_rows(2) <= a_col(2), "an accumulator set fits");
+static_assert(max_rows(1) + kUnits * half_cols(1) <= kTmemCols && 2 * max_rows(2) + kUnits * half_cols(2) <= kTmemCols, "they fit");
+constexpr int wide_units(int mats, int rows) { return mats == 1 && 2 * rows + 2 * kUnits * half_cols(1) <= kTmemCols ? 1 : 0; }
+constexpr int unit_cols(int mats, int rows) { return (kUnits << wide_units(mats, rows)) * half_cols(mats); }
+constexpr int sets_of(int mats, int rows) { return 2 * mats * rows + unit_cols(mats, rows) <= kTmemCols ? 2 : 1; }
 
 // Rows per tile: the least time of a simple model, in cycles per 128 inputs, as in
 // ops_gemm.cu: the MMAs, shared memory at 128 bytes a cycle (128 x mats + half the rows in and
@@ -464,7 +471,7 @@ int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int p
         const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
         const long long waves = (items + pairs - 1) / pairs;
         const long long step = max(max(4 * mats * t, 256 * mats + (2 + mats) * t), 200 * mats + t + 150);
-        const bool one_set = 2 * mats * cap > a_col(mats);
+        const bool one_set = sets_of(mats, cap) == 1;
         const long long cost = waves * nk * step + per_row * t + (one_set ? waves * per_row * t / 2 : 0);
         if (least < 0 || cost < least) {
             least = cost;
@@ -531,18 +538,19 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
     Tiling g;
     g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all);
-    g.a_col = a_col(mats);
-    g.bufs = 2 * mats * g.tcap <= g.a_col ? 2 : 1;
+    g.wide = wide_units(mats, g.tcap);
+    g.a_col = kTmemCols - unit_cols(mats, g.tcap);
+    g.bufs = sets_of(mats, g.tcap);
     g.stage_bytes = mats * kTileW + box_rows(g.tcap / kPair) * kIn;
     g.half_bytes = g.tcap / kPair * kK * 2;
     g.mblocks = mblocks;
     auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
     g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
     const int table = p.offsets ? p.E * 4 : 0;
-    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - kHalves * g.half_bytes;
+    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - (kUnits << g.wide) * g.half_bytes;
     g.stages = min(kMaxStages, budget / g.stage_bytes);
-    if (g.stages < kMinStages) return cudaErrorNotSupported;
-    const int smem = 1024 + g.stages * g.stage_bytes + kHalves * g.half_bytes + table;
+    if (g.stages < (g.wide ? 6 : 4)) return cudaErrorNotSupported;  // (see the converters)
+    const int smem = 1024 + g.stages * g.stage_bytes + (kUnits << g.wide) * g.half_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     // items are numbered in 32 bits, also where offsets that do not ascend give every
     // expert all rows
