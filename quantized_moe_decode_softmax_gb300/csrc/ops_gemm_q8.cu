@@ -45,7 +45,6 @@ constexpr int kThreads = 32 * (kMmaWarp + 1);
 struct Tiling : Tiles {
     int stages;
     int stage_bytes;
-    int wide;         // a unit handed to the MMAs is a whole load stage (1) or half of one (0)
     int half_bytes;   // shared memory of a half stage as f16: the rows of x
     int a_col;        // tensor memory: first column of the weights as f16
 };
@@ -103,8 +102,82 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint32_t b, 
         : "memory");
 }
 
-// The pair's items, as one warp has found them. (To find one takes a thousand cycles of
-// divisions and dependent loads, longer than a short tile's conversions.)
+// The groups in shared memory: their first item, first row, rows, and tiles x 32 + rows of a tile
+// / 16. (For one group without offsets: entry 0.)
+struct Group {
+    int first, lo, rows, tiles;
+};
+
+// Fill the table, by the block; the number of all items. warp_sum: kThreads / 32 numbers.
+__device__ __forceinline__ int number_groups(const Product &p, const Tiles &g, Group *table, int *warp_sum) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = p.offsets ? p.E : 1;
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += kThreads) {
+        const int e = e0 + tid;
+        int items = 0, lo = 0, hi = 0, t = kStepRows, nt = 0;
+        if (e < E) {
+            group_rows(p, e, lo, hi);
+            if (hi > lo) {
+                t = tile_rows(hi - lo, g.tcap);
+                nt = (hi - lo + t - 1) / t;
+                items = nt * g.mblocks;
+            }
+        }
+        int scan = items;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += v;
+        }
+        if (lane == 31) warp_sum[warp] = scan;
+        __syncthreads();
+        int before = base, sum = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += warp_sum[w];
+            sum += warp_sum[w];
+        }
+        if (e < E) table[e] = Group{before + scan - items, lo, hi - lo, nt * 32 + t / 16};
+        base += sum;
+        __syncthreads();
+    }
+    return base;
+}
+
+// Item i of all (i < total), by a whole warp: two rounds of 32 comparisons find its group.
+__device__ __forceinline__ Item find_item(const Group *table, int E, int mblocks, int i) {
+    const int lane = threadIdx.x & 31;
+    int e = 0;
+    if (E > 1) {
+        const int step = (E + 31) >> 5;  // <= 32
+        const int c = lane * step;
+        e = (__popc(__ballot_sync(0xffffffffu, c < E && table[c].first <= i)) - 1) * step;
+        const int f = e + lane;
+        e += __popc(__ballot_sync(0xffffffffu, lane < step && f < E && table[f].first <= i)) - 1;
+    }
+    const Group g = table[e];
+    const int nt = max(g.tiles >> 5, 1), T = (g.tiles & 31) * 16;
+    i -= g.first;
+    // bands of kBand row tiles: the tiles of a band run side by side on one weight block, then
+    // on the next
+    int band = 0, bh = nt;
+    if (nt > kBand) {
+        band = i / (kBand * mblocks);
+        i -= band * kBand * mblocks;
+        bh = max(min(kBand, nt - band * kBand), 1);
+    }
+    Item it;
+    it.m = bh == 1 ? i : i / bh;
+    it.e = e;
+    it.T = T;
+    const int first = (band * kBand + i - it.m * bh) * T;
+    it.r0 = g.lo + first;
+    it.rows = min(T, g.rows - first);
+    return it;
+}
+
+// The pair's items, as one warp has found them. (To find one takes longer than a short
+// tile's conversions.)
 struct RingItems {
     const Item *ring;
     uint32_t full, empty;
@@ -121,7 +194,7 @@ struct RingItems {
     }
 };
 
-template <typename T, int MATS>
+template <typename T, int MATS, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     product_gemm_q8_kernel(const __grid_constant__ Product p, const __grid_constant__ Tiling g,
                            const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmx_half,
@@ -135,10 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tslot;
     __shared__ int abort_word, warp_sum[kThreads / 32];
     __shared__ __align__(16) float row_scale[kEpilogue][128];
+    constexpr uint32_t kHalves = WIDE ? 2 : 1;  // half stages of a unit
     volatile int *abort_flag = &abort_word;
     unsigned char *ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *f16_ring = ring + g.stages * g.stage_bytes;
-    int *first = reinterpret_cast<int *>(f16_ring + (kUnits << g.wide) * g.half_bytes);
+    Group *table = reinterpret_cast<Group *>(f16_ring + kUnits * kHalves * g.half_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
     const int item0 = blockIdx.x / kPair, item_step = gridDim.x / kPair;
@@ -147,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort_word = 0;
         for (int i = 0; i < g.stages; ++i) {
             ptx::mbar_init(&full[i], 1);
-            ptx::mbar_init(&empty[i], 8);  // the warps that convert its two halves
+            ptx::mbar_init(&empty[i], 8 / kHalves);  // the warps that convert it
         }
         for (int i = 0; i < kUnits; ++i) {
-            ptx::mbar_init(&u_full[i], (4 << g.wide) * kPair);
+            ptx::mbar_init(&u_full[i], 4 * kPair);
             ptx::mbar_init(&u_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -170,8 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kMmaWarp) tmem_alloc_pair(&tslot, kTmemCols);
     ptx::griddep_wait();
-    const int total = number_items<kThreads>(p, g, first, warp_sum);
-    if (!p.offsets) first = nullptr;
+    const int total = number_groups(p, g, table, warp_sum);
     tc::fence_before_sync();
     __syncthreads();
     cluster_sync();  // the peer's barriers are ready
@@ -180,11 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring_addr = tc::smem_u32(ring), full_addr = tc::smem_u32(full), empty_addr = tc::smem_u32(empty);
     const uint32_t f16_addr = tc::smem_u32(f16_ring), u_full_addr = tc::smem_u32(u_full), u_empty_addr = tc::smem_u32(u_empty);
     const uint32_t acc_full_addr = tc::smem_u32(acc_full), acc_empty_addr = tc::smem_u32(acc_empty);
-    const Walk walk{p, g, first, total};
     const int nk = (p.K + kIn - 1) / kIn, nh = 2 * nk;  // load stages and half stages of a tile (past K: zeros)
     RingItems items{item_ring, tc::smem_u32(item_full), tc::smem_u32(item_empty), abort_flag, 0};
     const uint32_t stages = g.stages, stage_bytes = g.stage_bytes;
-    const uint32_t wide = MATS == 1 ? g.wide : 0;
 
     if (warp == kLoadW) {
         // ---- weights ------------------------------------------------------------
@@ -228,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t n = 0;
         for (int i = item0; ok; i += item_step, ++n) {
             if (w) {
-                const bool more = walk.get(i, it);
+                const bool more = i < total;
+                if (more) it = find_item(table, p.offsets ? p.E : 1, g.mblocks, i);
                 const uint32_t slot = n % kItems;
                 if (!(ok = __all_sync(0xffffffffu, wait(items.empty + 8 * slot, ((n / kItems) & 1) ^ 1, abort_flag)))) break;
                 if (lane == 0) {
@@ -280,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         bool ok = true;
         const uint32_t base = tc::idesc_f16_f32(kPair * kM, 0);
-        const int units = nh >> wide;  // of a tile
+        const int units = nh / kHalves;  // of a tile
         for (int n = 0; ok && items.next(it); ++n) {
             if (tc::elect_one()) {
                 const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
@@ -294,15 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t u = (c + k) % kUnits;
                     if (!(ok = wait(u_full_addr + 8 * u, ((c + k) / kUnits) & 1, abort_flag))) break;
                     tc::fence_after_sync();
-                    uint32_t a = tmem + g.a_col + (u << wide) * (MATS * kK / 2);
-                    uint32_t b = desc_low(f16_addr + (u << wide) * g.half_bytes);
+                    uint32_t a = tmem + g.a_col + u * kHalves * (MATS * kK / 2);
+                    uint32_t b = desc_low(f16_addr + u * kHalves * g.half_bytes);
                     // the first MMA of a tile overwrites
 #pragma unroll
                     for (int q = 0; q < kK / 16; ++q) {
                         mma_pair_ts(acc, a + 8 * q, b + 2 * q, idesc, q ? 1 : k);
                         if (MATS == 2) mma_pair_ts(acc_up, a + kK / 2 + 8 * q, b + 2 * q, idesc, q ? 1 : k);
                     }
-                    if (MATS == 1 && wide) {
+                    if (WIDE) {
                         a += kK / 2;
                         b += g.half_bytes >> 4;
 #pragma unroll
@@ -323,11 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp < kConvert) {
         // ---- codes to f16 --------------------------------------------------------
-        // The half stages of all tiles are dealt to the groups in turn. (A wait takes a barrier two
-        // phases behind for one that is done. None is: this group's last half stage, c - 3, began
-        // once the MMAs of half stage c - 7 had ended (wide: of the load stage six back). That is
-        // after the last use but one of the unit's place, and after the last fill of the stage if
-        // there are at least 4 stages (6).)
+        // The units of all tiles are dealt to the groups in turn. (A wait takes a barrier two
+        // phases behind for one that is done. None is: this group's last unit, v - 3, began once
+        // the MMAs of unit v - 7 had ended. That is after the last use but one of the unit's
+        // place, and after the last fill of the stage if there are at least 4 stages (wide: 7).)
         const int q = warp & 3;  // quadrant of the lanes
         const uint32_t peer_full = in_first(u_full_addr);
         const int wr = 32 * q + lane;  // this thread's weight row
@@ -342,51 +413,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t x_dst0 = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3) + swap) ^ xr) << 4);
         const uint32_t x_dst1 = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3) + 1 - swap) ^ xr) << 4);
         const uint32_t a_at = tmem + ((uint32_t)(32 * q) << 16) + g.a_col;
-        uint32_t c = warp >> 2;        // this group's half stage
-        uint32_t slot = c >> 1, phase = 0;  // its load stage in the ring, and the lap
-        uint32_t end = 0;              // half stages of the tiles so far
-        int atoms = 0;                 // this warp's of the tile: every fourth
+        uint32_t v = warp >> 2;             // this group's unit
+        uint32_t slot = v * kHalves / 2, phase = 0;  // its load stage in the ring, and the lap
+        uint32_t end = 0;                   // units of the tiles so far
+        int atoms = 0;                      // this warp's of the tile: every fourth
         bool ok = true;
         Item it;
         while ((ok = items.next(it))) {
-            end += nh;
+            end += nh / kHalves;
             atoms = it.T / (kPair * 8) - q;
 #pragma unroll 1
-            for (; c < end; c += kGroups) {
-                const uint32_t turn = (c & 1) << 6, v = c >> wide, u = v % kUnits, stage = slot * stage_bytes;
+            for (; v < end; v += kGroups) {
+                const uint32_t u = v % kUnits, stage = slot * stage_bytes;
                 if (!(ok = __all_sync(0xffffffffu, wait(full_addr + 8 * slot, phase, abort_flag)))) break;
                 uint4 w[MATS][4], x[4];
+                auto load = [&](uint32_t turn) {
 #pragma unroll
-                for (int m = 0; m < MATS; ++m)
+                    for (int m = 0; m < MATS; ++m)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ turn);
+                        for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ turn);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ turn);
+                    for (int j = 0; j < 4; ++j)
+                        if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ turn);
+                };
+                auto store = [&](uint32_t place) {
+                    const uint32_t a = a_at + place * (MATS * kK / 2), dst = place * g.half_bytes;
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            uint32_t f16[16];
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) {
+                                const uint2 f = codes_to_f16(word(w[m][j + (b >> 2)], b & 3));
+                                f16[2 * b] = f.x;
+                                f16[2 * b + 1] = f.y;
+                            }
+                            tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, f16);
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (4 * j >= atoms) break;
+                        const uint2 f0 = codes_to_f16(x[j].x), f1 = codes_to_f16(x[j].y), f2 = codes_to_f16(x[j].z),
+                                    f3 = codes_to_f16(x[j].w);
+                        sts(dst + j * 4096 + x_dst0, swap ? f2 : f0, swap ? f3 : f1);
+                        sts(dst + j * 4096 + x_dst1, swap ? f0 : f2, swap ? f1 : f3);
+                    }
+                };
+                load(WIDE ? 0u : (v & 1) << 6);
                 // the MMAs have read what this unit held
                 if (!(ok = __all_sync(0xffffffffu, wait(u_empty_addr + 8 * u, ((v / kUnits) & 1) ^ 1, abort_flag)))) break;
                 tc::fence_after_sync();
-                const uint32_t at = c & ((kUnits << wide) - 1), a = a_at + at * (MATS * kK / 2), dst = at * g.half_bytes;
-#pragma unroll
-                for (int m = 0; m < MATS; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        uint32_t f16[16];
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const uint2 f = codes_to_f16(word(w[m][j + (b >> 2)], b & 3));
-                            f16[2 * b] = f.x;
-                            f16[2 * b + 1] = f.y;
-                        }
-                        tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, f16);
-                    }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (4 * j >= atoms) break;
-                    const uint2 f0 = codes_to_f16(x[j].x), f1 = codes_to_f16(x[j].y), f2 = codes_to_f16(x[j].z),
-                                f3 = codes_to_f16(x[j].w);
-                    sts(dst + j * 4096 + x_dst0, swap ? f2 : f0, swap ? f3 : f1);
-                    sts(dst + j * 4096 + x_dst1, swap ? f0 : f2, swap ? f1 : f3);
+                store(u * kHalves);
+                if (WIDE) {
+                    load(64u);
+                    store(u * kHalves + 1);
                 }
                 tc::wait_st();
                 tc::fence_async_shared();
@@ -396,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     arrive_in_first(peer_full + 8 * u);
                     arrive(empty_addr + 8 * slot);
                 }
-                slot += ((c + kGroups) >> 1) - (c >> 1);
+                slot += WIDE ? kGroups : ((v + kGroups) >> 1) - (v >> 1);
                 if (slot >= stages) {
                     slot -= stages;
                     phase ^= 1;
@@ -408,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             const unsigned long long t0 = globaltimer();
             for (uint32_t u = 0; u < kUnits; ++u)
-                if ((end >> wide) > u) settle(u_empty_addr + 8 * u, (((end >> wide) - u - 1) / kUnits) & 1, t0);
+                if (end > u) settle(u_empty_addr + 8 * u, ((end - u - 1) / kUnits) & 1, t0);
         }
         __syncwarp();
     } else if (warp >= kConvert && warp < kConvert + kEpilogue) {
@@ -450,13 +531,15 @@ Device g_devices[kMaxDevices];
 
 // Tensor memory beside the accumulator sets: kUnits units of weights as f16. A unit is a whole
 // load stage where that leaves room for two sets (short tiles: half as many hand-overs, 64 tokens
-// down 49 to 45 us), otherwise half of one (long ones: 8192x4096x4096 152 us, 169 in two units).
+// down 49 to 39 us), otherwise half of one (long ones: 8192x4096x4096 152 us, 169 with whole stages).
 constexpr int half_cols(int mats) { return mats * kK / 2; }
 constexpr int max_rows(int mats) { return mats == 2 ? 128 : 256; }
 static_assert(max_rows(1) + kUnits * half_cols(1) <= kTmemCols && 2 * max_rows(2) + kUnits * half_cols(2) <= kTmemCols, "they fit");
-constexpr int wide_units(int mats, int rows) { return mats == 1 && 2 * rows + 2 * kUnits * half_cols(1) <= kTmemCols ? 1 : 0; }
-constexpr int unit_cols(int mats, int rows) { return (kUnits << wide_units(mats, rows)) * half_cols(mats); }
-constexpr int sets_of(int mats, int rows) { return 2 * mats * rows + unit_cols(mats, rows) <= kTmemCols ? 2 : 1; }
+constexpr bool wide_units(int mats, int rows) { return mats == 1 && rows <= 96; }  // (7 load stages fit up to there)
+constexpr int halves_of(int mats, int rows) { return kUnits * (wide_units(mats, rows) ? 2 : 1); }
+constexpr int sets_of(int mats, int rows) {
+    return 2 * mats * rows + halves_of(mats, rows) * half_cols(mats) <= kTmemCols ? 2 : 1;
+}
 
 // Rows per tile: the least time of a simple model, in cycles per 128 inputs, as in
 // ops_gemm.cu: the MMAs, shared memory at 128 bytes a cycle (128 x mats + half the rows in and
@@ -485,7 +568,7 @@ cudaError_t look_up(int dev, Device &d) {
     int smem = 0, sms = 0, pairs = 0;
     cudaFuncAttributes fa;
     cudaError_t err;
-    auto k = product_gemm_q8_kernel<__half, 2>;
+    auto k = product_gemm_q8_kernel<__half, 2, false>;
     if ((err = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
         (err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
         (err = cudaFuncGetAttributes(&fa, k)) != cudaSuccess)
@@ -509,11 +592,11 @@ cudaError_t look_up(int dev, Device &d) {
     return cudaSuccess;
 }
 
-template <typename T, int MATS>
+template <typename T, int MATS, bool WIDE>
 cudaError_t launch(const Product &p, const Tiling &g, int pairs, int smem, Device &d, const CUtensorMap &tmx,
                    const CUtensorMap &tmx_half, const CUtensorMap &tmw, const CUtensorMap &tmu, cudaStream_t st) {
-    auto k = product_gemm_q8_kernel<T, MATS>;
-    const unsigned bit = 1u << (MATS - 1 + (p.dtype == MOE_DTYPE_BF16 ? 2 : 0));
+    auto k = product_gemm_q8_kernel<T, MATS, WIDE>;
+    const unsigned bit = 1u << (MATS - 1 + (WIDE ? 2 : 0) + (p.dtype == MOE_DTYPE_BF16 ? 4 : 0));
     if (!(d.ready.load(std::memory_order_acquire) & bit)) {
         const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      d.smem.load(std::memory_order_relaxed));
@@ -538,19 +621,20 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
     Tiling g;
     g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all);
-    g.wide = wide_units(mats, g.tcap);
-    g.a_col = kTmemCols - unit_cols(mats, g.tcap);
+    const bool wide = wide_units(mats, g.tcap);
+    const int halves = halves_of(mats, g.tcap);
+    g.a_col = kTmemCols - halves * half_cols(mats);
     g.bufs = sets_of(mats, g.tcap);
     g.stage_bytes = mats * kTileW + box_rows(g.tcap / kPair) * kIn;
     g.half_bytes = g.tcap / kPair * kK * 2;
     g.mblocks = mblocks;
     auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
     g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
-    const int table = p.offsets ? p.E * 4 : 0;
-    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - (kUnits << g.wide) * g.half_bytes;
+    const int table = (p.offsets ? p.E : 1) * (int)sizeof(Group);
+    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - halves * g.half_bytes;
     g.stages = min(kMaxStages, budget / g.stage_bytes);
-    if (g.stages < (g.wide ? 6 : 4)) return cudaErrorNotSupported;  // (see the converters)
-    const int smem = 1024 + g.stages * g.stage_bytes + (kUnits << g.wide) * g.half_bytes + table;
+    if (g.stages < (wide ? 7 : 4)) return cudaErrorNotSupported;  // (see the converters)
+    const int smem = 1024 + g.stages * g.stage_bytes + halves * g.half_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     // items are numbered in 32 bits, also where offsets that do not ascend give every
     // expert all rows
@@ -566,11 +650,13 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     if (mats == 2 && !encode(&tmu, p.w_up, p.K, p.N, p.ldw, planes, p.stride_e ? p.stride_e : p.ldw, kM))
         return cudaErrorNotSupported;
     const int n = (int)min(most, (long long)all);
-    if (p.dtype == MOE_DTYPE_BF16)
-        return mats == 2 ? launch<__nv_bfloat16, 2>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
-                         : launch<__nv_bfloat16, 1>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
-    return mats == 2 ? launch<__half, 2>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
-                     : launch<__half, 1>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
+    auto go = [&](auto type) {
+        using T = decltype(type);
+        return mats == 2 ? launch<T, 2, false>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
+               : wide    ? launch<T, 1, true>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st)
+                         : launch<T, 1, false>(p, g, n, smem, d, tmx, tmx_half, tmw, tmu, st);
+    };
+    return p.dtype == MOE_DTYPE_BF16 ? go(__nv_bfloat16()) : go(__half());
 }
 
 unsigned *ops_status_q8(cudaError_t *err) {
