@@ -125,8 +125,31 @@ moe_status run(const Product &a, cudaStream_t st) {
     return of(launch_product_rows(a, st));
 }
 
+// The same for 8-bit codes, with a third way for a handful of rows: dot products
+// (ops_dot_q8.cu), f16 on mma.sync (ops_rows_q8.cu), f16 on tcgen05 (ops_gemm_q8.cu). Measured
+// (us, dot / mma.sync / tcgen05):
+//   2048x2048              1 row  3.1 / 3.5 / 12      4 rows  3.5 / 3.5 / 12     64 rows  20 / 8.7 / 11
+//   8192x4096              1 row  7.5 / 9.3 / 19      4 rows  8.3 / 9.1 / 19     24 rows  26 / 19.1 / 19.3
+//   4096x4096             32 rows  22 / 10.2 / 18.7  48 rows  31 / 17.2 / 15.7
+//   2048x4096 gated       64 rows  45 / 19.7 / 23
+//   768x2048 gated, 128 experts, top 8   1 token 6.6 / 9.5 / 18    16 tokens 46 / 60 / 55   32 tokens 114 / 95 / 66
+//   the same, all on the same experts                              16 tokens 24 / 17 / 18
+//   512x1024 gated, 8 experts, top 2     8 tokens 4.0 / 4.4 / 12   32 tokens 7.2 / 6.3 / 12
+enum class Q8 { dot, rows, gemm };
+Q8 kernel_q8(const Product &a) {
+    const int groups = a.offsets ? min(a.E, a.rows) : 1;
+    const int mean = (a.rows + groups - 1) / groups;
+    const double mb = 1e-6 * groups * a.N * (double)a.K * (a.w_up ? 2 : 1);
+    const double work = mb * ((mean + 7) / 8);  // rows cost in blocks of 8
+    if (a.offsets) return a.rows <= 128 && mean <= 2 ? Q8::dot : a.rows <= 64 && work <= 60.0 ? Q8::rows : Q8::gemm;
+    if (a.rows == 1 || (a.rows <= 4 && a.K > 1024)) return Q8::dot;
+    return a.rows <= 64 && work <= (a.w_up ? 150.0 : 90.0) ? Q8::rows : Q8::gemm;
+}
+
 moe_status run_q8(const Product &a, cudaStream_t st) {
-    if (!streams(a)) {
+    const Q8 k = kernel_q8(a);
+    if (k == Q8::dot) return of(launch_product_dot_q8(a, st));
+    if (k == Q8::gemm) {
         const cudaError_t err = launch_product_gemm_q8(a, st);
         if (err != cudaErrorNotSupported) return of(err);
     }

@@ -169,10 +169,10 @@ __device__ __forceinline__ Item find_item(const Group *table, int E, int mblocks
     Item it;
     it.m = bh == 1 ? i : i / bh;
     it.e = e;
-    it.T = T;
     const int first = (band * kBand + i - it.m * bh) * T;
     it.r0 = g.lo + first;
     it.rows = min(T, g.rows - first);
+    it.T = tile_rows(it.rows, T);  // (a group's last tile may be shorter)
     return it;
 }
 
@@ -541,27 +541,30 @@ constexpr int sets_of(int mats, int rows) {
     return 2 * mats * rows + halves_of(mats, rows) * half_cols(mats) <= kTmemCols ? 2 : 1;
 }
 
-// Rows per tile: the least time of a simple model, in cycles per 128 inputs, as in
-// ops_gemm.cu: the MMAs, shared memory at 128 bytes a cycle (128 x mats + half the rows in and
-// out of the converters, x written and read as f16), the converters.
+// Rows per tile: the least time of a simple model, in cycles, as in ops_gemm.cu. Waves of tiles
+// on the pairs, each nk steps of 128 inputs: the longest of the MMAs (4 per row and matrix) and
+// the converters (fitted to 64..256 rows of 8192x4096x4096 and of the gated 8192x4096x2048;
+// short tiles hand over half stages less often); 500 for the tile itself; the epilogue of the
+// last tile, and two thirds of it for every tile with one accumulator set. Among groups, of
+// which some are larger than the mean, a larger cap may cost 8 % more (1024 tokens, 6 of
+// 256 skewed experts, gated 4096 -> 2048: 340 us with 64 rows, 297 with 128).
 int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int pairs) {
     const int mats = p.w_up ? 2 : 1;
     const int per_row = 20 + 15 * (mats - 1) + (p.act != MOE_EPI_NONE ? 15 : 0) + (p.residual ? 15 : 0);
-    int best = kStepRows;
-    long long least = -1;
+    long long cost[256 / kStepRows + 1], least = -1;
     for (int cap = max_rows(mats); cap >= kStepRows; cap -= kStepRows) {
         const int t = tile_rows(mean, cap);
         const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
         const long long waves = (items + pairs - 1) / pairs;
-        const long long step = max(max(4 * mats * t, 256 * mats + (2 + mats) * t), 200 * mats + t + 150);
-        const bool one_set = sets_of(mats, cap) == 1;
-        const long long cost = waves * nk * step + per_row * t + (one_set ? waves * per_row * t / 2 : 0);
-        if (least < 0 || cost < least) {
-            least = cost;
-            best = cap;
-        }
+        const int convert = mats == 2 ? 850 + 3 * t : 600 + 9 * t / 4;
+        const long long step = max(4 * mats * t, wide_units(mats, cap) ? convert : max(convert, 850));
+        const long long one_set = sets_of(mats, cap) == 1 ? waves * per_row * t * 2 / 3 : 0;
+        const long long c = cost[cap / kStepRows] = waves * (nk * step + 500) + per_row * t + one_set;
+        if (least < 0 || c < least) least = c;
     }
-    return best;
+    int cap = max_rows(mats);
+    while (cost[cap / kStepRows] > (p.offsets ? least + least * 8 / 100 : least)) cap -= kStepRows;
+    return cap;
 }
 
 cudaError_t look_up(int dev, Device &d) {

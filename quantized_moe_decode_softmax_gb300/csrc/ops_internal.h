@@ -73,7 +73,9 @@ cudaError_t launch_product_rows(const Product &p, cudaStream_t st);
 // many rows per expert: tcgen05 (ops_gemm.cu); cudaErrorNotSupported, with nothing
 // launched, where the driver declines a tensor map
 cudaError_t launch_product_gemm(const Product &p, cudaStream_t st);
-// the same for products of 8-bit codes (ops_rows_q8.cu, ops_gemm_q8.cu)
+// the same for products of 8-bit codes: a handful of rows per expert (ops_dot_q8.cu), few
+// (ops_rows_q8.cu), many (ops_gemm_q8.cu)
+cudaError_t launch_product_dot_q8(const Product &p, cudaStream_t st);
 cudaError_t launch_product_rows_q8(const Product &p, cudaStream_t st);
 cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st);
 // the status words of the current device's kernels with waits: set when one gave up
