@@ -4,14 +4,18 @@
 //
 // Bound: 3 bytes per value, each moved once. A row stays in registers between its
 // maximum and its codes: T threads share it, V loads of 16 bytes each, all in flight
-// before the first is used; V is as large as that allows (8), so that few threads
-// have to meet. Rows of more than 512 x 8 loads go through the same loop twice.
+// before the first is used (8192 x 4096: QUS us, QBW TB/s). Rows of more than 512 x 8 loads
+// are read twice.
 //
-// Codes are those of the exact quotient, halves to even. 127 x is exact in f32 (18
-// bits), and a quotient of two 16-bit values that is not a half is at least 1e-6 of
-// itself away from one, so that one product with 127 / max (error 2^-22) decides all
-// but the values within 1e-4 of a half; those are divided. The row is scaled by a power
-// of two first where 127 x or 127 / max would leave the range of f32.
+// Codes are those of the exact quotient, halves to even, for one product and one rounding
+// each: round(x r) with r = 127 / max rounded up. Why that is exact: let x be a times its
+// last place and max be b times that, a < 2^11. The quotient 127 a / b is j + 1/2 + d, and
+// d is 0 or at least 1 / (254 a) of the quotient, since 254 a - (2 j + 1) b is a whole number:
+// 1.9e-6, sixteen times the error of r, 2^-23. And d = 0 takes (2 j + 1) b = 254 a, so that 127
+// divides one of them. If it is 2 j + 1, the quotient is 63.5 (x is half of max): r above
+// 127 / max makes it 64, the even one. If it is b, then max is 127 c and r = 1 / c is exact for
+// c a power of two, as it always is in bf16; the other rows (7 of 1024 in f16), and those of
+// a max so small that r would be infinite, are divided value by value.
 #include "ops_common.cuh"
 #include "ptx.cuh"
 
@@ -22,63 +26,63 @@ namespace {
 constexpr float kMagic = 12582912.0f;  // 1.5 x 2^23: adding it rounds to a whole number
 constexpr int kVec = 8;                // values of a 16-byte load
 
-// |x| as bits: finite values order like numbers, NaN comes above infinity
-template <typename T> __device__ __forceinline__ uint32_t largest(uint32_t m, uint32_t two) {
-    const uint32_t lo = two & 0x7fffu, hi = (two >> 16) & 0x7fffu;
-    return max(m, max(lo, hi));
-}
+// the larger |x| of two pairs, as bits: finite values order like numbers, NaN comes above infinity
+__device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t two) { return __vmaxu2(m, two & 0x7fff7fffu); }
+
+template <typename T> struct Mantissa;  // its bits
+template <> struct Mantissa<__nv_bfloat16> { static constexpr int bits = 7; };
+template <> struct Mantissa<__half> { static constexpr int bits = 10; };
 
 template <typename T> __device__ __forceinline__ float from_bits(uint32_t b) { return unpack2<T>(b).x; }
 
-// The codes of one row: how its values become whole numbers.
+// How the values of one row become codes.
 struct Scaling {
-    float up;    // a power of two
-    float most;  // max|x| up
-    float rcp;   // 127 / most
+    enum { zeros, product, division } way;
+    float rcp;   // product: 127 / max|x|, rounded up
+    float up;    // division: a power of two
+    float most;  //           max|x| up
 };
 
 // scale of a row from the bits of its max|x|, and what its codes need
 template <typename T> __device__ __forceinline__ float scaling(uint32_t bits, Scaling &s) {
     const float most = from_bits<T>(bits);
-    if (!(most > 0.f && most < INFINITY)) {  // zeros; or an infinity or NaN, which the scale passes on
-        s.up = s.most = s.rcp = 0.f;
-        return most == 0.f ? 0.f : most;
-    }
-    s.up = most > 0x1p100f ? 0x1p-64f : most < 0x1p-60f ? 0x1p64f : 1.f;
+    s.way = Scaling::zeros;
+    s.rcp = s.up = s.most = 0.f;
+    if (!(most > 0.f && most < INFINITY)) return most;  // zeros; or an infinity or NaN, which the scale passes on
+    const uint32_t exponent = bits >> Mantissa<T>::bits, low = bits & ((1u << Mantissa<T>::bits) - 1u);
+    const uint32_t mantissa = exponent ? low | (1u << Mantissa<T>::bits) : low, c = mantissa / 127u;
+    s.way = most < 0x1p-60f || (c * 127u == mantissa && (c & (c - 1u))) ? Scaling::division : Scaling::product;
+    s.rcp = __fdiv_ru(127.f, most);
+    s.up = most < 0x1p-60f ? 0x1p64f : 1.f;
     s.most = most * s.up;
-    s.rcp = __fdiv_rn(127.f, s.most);
     return __fdiv_rn(most, 127.f);
 }
 
-__device__ __noinline__ float divided(float x, const Scaling &s) { return rintf(__fdiv_rn(127.f * x, s.most)); }
+// a whole number near kMagic: the code in its low byte
+__device__ __noinline__ float divided(float x, const Scaling &s) { return kMagic + rintf(__fdiv_rn(127.f * (x * s.up), s.most)); }
 
 // 4 codes, the first in the low byte
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const Scaling &s) {
-    float v[4] = {a, b, c, d}, q[4], off = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] *= s.up;
-        q[i] = fmaf(v[i], s.rcp, kMagic);
-        off = fmaxf(off, fabsf(fmaf(v[i], s.rcp, kMagic - q[i])));
-    }
-    if (off > 0.4999f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = kMagic + divided(v[i], s);
-    }
-    const uint32_t lo = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x0040);
-    const uint32_t hi = __byte_perm(__float_as_uint(q[2]), __float_as_uint(q[3]), 0x0040);
+__device__ __forceinline__ uint32_t bytes4(float a, float b, float c, float d) {
+    const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
 }
 
 template <typename T> __device__ __forceinline__ uint2 codes8(const uint4 &w, const Scaling &s) {
-    if (s.up == 0.f) return make_uint2(0u, 0u);
     const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y), c = unpack2<T>(w.z), d = unpack2<T>(w.w);
-    return make_uint2(codes4(a.x, a.y, b.x, b.y, s), codes4(c.x, c.y, d.x, d.y, s));
+    if (s.way == Scaling::product)
+        return make_uint2(bytes4(fmaf(a.x, s.rcp, kMagic), fmaf(a.y, s.rcp, kMagic), fmaf(b.x, s.rcp, kMagic),
+                                 fmaf(b.y, s.rcp, kMagic)),
+                          bytes4(fmaf(c.x, s.rcp, kMagic), fmaf(c.y, s.rcp, kMagic), fmaf(d.x, s.rcp, kMagic),
+                                 fmaf(d.y, s.rcp, kMagic)));
+    if (s.way == Scaling::zeros) return make_uint2(0u, 0u);
+    return make_uint2(bytes4(divided(a.x, s), divided(a.y, s), divided(b.x, s), divided(b.y, s)),
+                      bytes4(divided(c.x, s), divided(c.y, s), divided(d.x, s), divided(d.y, s)));
 }
 
 // the largest over the T threads of a row; ROWS rows per block (T >= 32)
 template <int T> __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t *part) {
-    m = __reduce_max_sync(0xffffffffu, m);
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
     if constexpr (T > 32) {
         const int warp = threadIdx.x >> 5, first = warp / (T / 32) * (T / 32);
         if ((threadIdx.x & 31) == 0) part[warp] = m;
@@ -107,10 +111,10 @@ __global__ void __launch_bounds__(B) quantize_kernel(const char *x, long long ld
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        m = largest<T_>(m, v[i].x);
-        m = largest<T_>(m, v[i].y);
-        m = largest<T_>(m, v[i].z);
-        m = largest<T_>(m, v[i].w);
+        m = larger(m, v[i].x);
+        m = larger(m, v[i].y);
+        m = larger(m, v[i].z);
+        m = larger(m, v[i].w);
     }
     m = row_max<T>(m, part);
     if (!live) return;
@@ -132,14 +136,17 @@ __global__ void __launch_bounds__(256) quantize_any_kernel(const char *x, long l
     const long long row = blockIdx.x;
     const uint16_t *src = reinterpret_cast<const uint16_t *>(x + 2 * row * ldx);
     uint32_t m = 0;
-    for (int k = threadIdx.x; k < K; k += 256) m = max(m, src[k] & 0x7fffu);
+    for (int k = threadIdx.x; k < K; k += 256) m = max(m, (uint32_t)src[k] & 0x7fffu);
     m = row_max<256>(m, part);
     Scaling s;
     const float sc = scaling<T_>(m, s);
     if (threadIdx.x == 0) scale[row] = sc;
     char *dst = codes + row * ldc;
-    for (int k = threadIdx.x; k < K; k += 256)
-        dst[k] = s.up == 0.f ? (char)0 : (char)(int)divided(from_bits<T_>(src[k]) * s.up, s);
+    for (int k = threadIdx.x; k < K; k += 256) {
+        const float v = from_bits<T_>(src[k]);
+        const float q = s.way == Scaling::product ? fmaf(v, s.rcp, kMagic) : divided(v, s);
+        dst[k] = s.way == Scaling::zeros ? (char)0 : (char)__float_as_uint(q);
+    }
 }
 
 template <typename T_>

@@ -5,18 +5,20 @@
 //   ids = the top_k experts by c_e in them, ties to the lower id;
 //   w_j = s of the j-th, divided by the sum of all of them if asked, times scale.
 //
-// Bound: latency. A row is E logits (a few hundred bytes), so one warp takes a row and
-// keeps it in registers: lane i holds the V experts V i .. V i + V - 1, which makes the
-// lowest lane of a tie the lowest id. A key is its f32 as an unsigned number that sorts
-// alike (0: not available), so that a rank costs one redux and one ballot. No block
-// synchronisation, no shared memory unless there are groups or a bias.
+// Bound: latency for a few rows, the issue of instructions for many (a row is E logits, a few
+// hundred bytes). One warp takes a row: lane i holds the V experts V i .. V i + V - 1, which
+// makes the lowest lane of a tie the lowest id. A key is its f32 as an unsigned number that
+// sorts alike (0: not available). The keys lie in shared memory and each lane keeps the
+// largest of its own, so that a rank is one redux over the lanes, and another over the V keys
+// of the lane that had it, which V lanes read side by side: about 25 instructions whatever V
+// is (50 for V = 8 and 160 for V = 32 with the keys in registers).
 //
 // The ids are those of exact scores. Without a bias the order of c is the order of the
 // logits, and no score is computed for it. With a bias (or with sums of two per group)
 // c is computed in f32, the ranks are taken to top_k + 1 places, and wherever two
 // neighbours are nearer to each other than the f32 errors (below), the row is ranked
 // again in f64, over the experts that can still be among the first. For trained
-// routers that is one row in a thousand.
+// routers that is one row in some thousands.
 #include "ops_common.cuh"
 #include "ptx.cuh"
 
@@ -27,11 +29,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Relative error of an f32 score: the sigmoid is one expf (1 ulp of CUDA's bound, 2 here),
-// one sum and one division, at most 4 x 2^-23; a softmax also rounds l - max (its error
-// times the score is at most 2^-25) and sums up to 32 terms in a lane and 5 across, 37
-// roundings of 2^-24.
+// Error of an f32 score of a key (at most 1). Sigmoid: the argument's rounding moves the result
+// by at most |l| s (1 - s) 2^-24 < 2^-26, exp2 and the reciprocal are good to 2^-22, 1 + e rounds
+// to 2^-24: together below 2^-21. A softmax also rounds l - max and its product with log2(e) (error times score at
+// most 2^-24) and sums up to 32 terms in a lane and 5 across, 37 roundings of 2^-24.
 constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-18f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint32_t sortable(float v) {
     const uint32_t b = __float_as_uint(v);
@@ -50,6 +53,10 @@ __device__ __forceinline__ float logit(const RouteArgs &a, long long row, int e)
 
 // an expert whose logit is -inf or NaN, or whose bias is, takes no part
 __device__ __forceinline__ bool takes_part(float v) { return v > -INFINITY; }
+
+// scores for keys, to the errors above
+__device__ __forceinline__ float sigmoid_key(float l) { return rcp_fast(1.0f + exp2_fast(-kLog2e * l)); }
+__device__ __forceinline__ float exp_key(float l, float m) { return l == m ? 1.f : exp2_fast(kLog2e * (l - m)); }
 
 // 1 / (1 + exp(-l)), also where it is subnormal
 __device__ __forceinline__ float sigmoid(float l) {
@@ -75,13 +82,16 @@ template <typename F> __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// Which groups stay, as a mask of bits, by the keys of all experts in `key` (shared
-// memory; -inf: not available) in precision F. 32 / 2^ceil(log2 groups) lanes share a
+// Which groups stay, as a mask of bits, by the keys of all experts in `key` (shared memory; f32
+// as sortable numbers, or f64 with -inf for those not available). F: the precision. 32 / 2^ceil(log2 groups) lanes share a
 // group. *gap: the distance of the worst group that stays from the best that does not
 // (inf if there are not both). logits: the keys are logits, and a sum of two is one of
 // their scores.
-template <typename F>
-__device__ unsigned best_groups(const RouteArgs &a, const F *key, float max_logit, bool logits, F *gap, F *worst) {
+__device__ __forceinline__ float key_value(uint32_t k) { return k ? unsortable(k) : -INFINITY; }
+__device__ __forceinline__ double key_value(double k) { return k; }
+
+template <typename F, typename K>
+__device__ unsigned best_groups(const RouteArgs &a, const K *key, float max_logit, bool logits, F *gap, F *worst) {
     const int lane = threadIdx.x & 31, size = a.E / a.groups;
     int per = 32;  // lanes per group
     while (32 / per < a.groups) per >>= 1;
@@ -90,7 +100,7 @@ __device__ unsigned best_groups(const RouteArgs &a, const F *key, float max_logi
     F m1 = none, m2 = none;
     if (g < a.groups)
         for (int i = lane % per; i < size; i += per) {
-            const F v = key[g * size + i];
+            const F v = key_value(key[g * size + i]);
             if (v > m1) {
                 m2 = m1;
                 m1 = v;
@@ -112,7 +122,7 @@ __device__ unsigned best_groups(const RouteArgs &a, const F *key, float max_logi
             auto s = [&](F v) -> F {
                 if (v == none) return 0;
                 if constexpr (sizeof(F) == 4)
-                    return a.score == MOE_SCORE_SOFTMAX ? expf(below(v, max_logit)) : sigmoid(v);
+                    return a.score == MOE_SCORE_SOFTMAX ? exp_key(v, max_logit) : sigmoid_key(v);
                 else
                     return a.score == MOE_SCORE_SOFTMAX ? (v == (F)max_logit ? 1.0 : exp(v - (F)max_logit)) : sigmoid(v);
             };
@@ -141,10 +151,11 @@ __device__ unsigned best_groups(const RouteArgs &a, const F *key, float max_logi
 }
 
 // The row again in f64: the ids of ranks lane and 32 + lane (-1: none left). again: the
-// groups too; otherwise only experts in `groups` whose f32 key is at least `from` can be
-// among the first. `key`: E doubles of this warp, then E numbers.
+// groups too; otherwise only experts with a key (of those left in `list`) of at least
+// `from`, and those of `ids`, can be among the first. key: E doubles of this warp; list: its
+// sortable keys, which the ids in question replace.
 __device__ __noinline__ int2 rank_exactly(const RouteArgs &a, long long row, bool again, unsigned groups, float from,
-                                          float max_logit, float rcp_sum, double *key) {
+                                          float max_logit, int2 ids, int next, double *key, uint32_t *list) {
     const int lane = threadIdx.x & 31, size = a.E / a.groups;
     const double none = -INFINITY;
     __syncwarp();
@@ -157,41 +168,60 @@ __device__ __noinline__ int2 rank_exactly(const RouteArgs &a, long long row, boo
         }
         sum = warp_sum(sum);
     }
-    int2 ids = make_int2(-1, -1);
     // the experts in question are dealt to the lanes: an f64 exponential takes a warp as
     // long for one lane as for 32
-    int *list = reinterpret_cast<int *>(key + a.E);
     int found = 0;
+    auto add = [&](bool take, int e) {
+        const unsigned m = __ballot_sync(0xffffffffu, take);
+        if (take) list[found + __popc(m & ((1u << lane) - 1u))] = (uint32_t)e;
+        found += __popc(m);
+    };
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
         bool take = false;
         if (e < a.E) {
-            const float l = logit(a, row, e), b = a.bias ? a.bias[e] : 0.f;
-            take = takes_part(l) && takes_part(b);
-            if (take && !again) {
-                take = (groups >> (e / size)) & 1u;
-                if (take) {
-                    const float s = a.score == MOE_SCORE_SOFTMAX ? expf(below(l, max_logit)) * rcp_sum : sigmoid(l);
-                    take = s + b >= from;
-                }
-            }
-            key[e] = none;
+            if (again) take = takes_part(logit(a, row, e)) && (!a.bias || takes_part(a.bias[e]));
+            else take = list[e] && unsortable(list[e]) >= from;
         }
-        const unsigned m = __ballot_sync(kAll, take);
-        if (take) list[found + __popc(m & ((1u << lane) - 1u))] = e;
-        found += __popc(m);
+        __syncwarp();
+        add(take, e);  // (never beyond what has been read)
+        __syncwarp();
+    }
+    if (!again) {  // the ranks so far, and the next one, have no keys any more
+        add(ids.x >= 0, ids.x);
+        add(ids.y >= 0, ids.y);
+        add(lane == 0 && next >= 0, next);
     }
     __syncwarp();
-    for (int i = lane; i < found; i += 32) {
-        const int e = list[i];
+    auto score = [&](int e) -> double {
         const float l = logit(a, row, e);
-        double c;
-        if (!a.bias) c = l;  // the order of the logits
-        else if (a.score == MOE_SCORE_SOFTMAX) c = (l == max_logit ? 1.0 : exp((double)l - (double)max_logit)) / sum;
-        else c = sigmoid((double)l);
-        if (a.bias) c += (double)a.bias[e];
-        key[e] = c;
+        if (!a.bias) return l;  // the order of the logits
+        const double s = a.score == MOE_SCORE_SOFTMAX
+                             ? (l == max_logit ? 1.0 : exp((double)l - (double)max_logit)) / sum
+                             : sigmoid((double)l);
+        return s + (double)a.bias[e];
+    };
+    int2 out = make_int2(-1, -1);
+    if (!again && found <= 32 && a.k <= 32) {
+        // one each: a rank is the number of lanes that come before
+        const int e = lane < found ? (int)list[lane] : 0x7fffffff;
+        const double c = lane < found ? score(e) : none;
+        int rank = 0;
+        for (int i = 0; i < found; ++i) {
+            const double o = __shfl_sync(0xffffffffu, c, i);
+            const int oe = __shfl_sync(0xffffffffu, e, i);
+            rank += o > c || (o == c && oe < e);
+        }
+        __syncwarp();
+        if (lane < found) list[rank] = (uint32_t)e;
+        __syncwarp();
+        if (lane < a.k && lane < found) out.x = (int)list[lane];
+        return out;
     }
+    if (again)
+        for (int e = lane; e < a.E; e += 32) key[e] = none;
+    __syncwarp();
+    for (int i = lane; i < found; i += 32) key[list[i]] = score((int)list[i]);
     __syncwarp();
     if (again && a.groups > 1) {
         double gap, worst;
@@ -201,7 +231,7 @@ __device__ __noinline__ int2 rank_exactly(const RouteArgs &a, long long row, boo
         double best = none;
         int at = 0x7fffffff;
         for (int i = lane; i < found; i += 32) {
-            const int e = list[i];
+            const int e = (int)list[i];
             const double c = key[e];
             if (((groups >> (e / size)) & 1u) && (c > best || (c == best && c > none && e < at))) {
                 best = c;
@@ -209,29 +239,30 @@ __device__ __noinline__ int2 rank_exactly(const RouteArgs &a, long long row, boo
             }
         }
         for (int d = 16; d; d >>= 1) {
-            const double ob = __shfl_xor_sync(kAll, best, d);
-            const int oa = __shfl_xor_sync(kAll, at, d);
+            const double ob = __shfl_xor_sync(0xffffffffu, best, d);
+            const int oa = __shfl_xor_sync(0xffffffffu, at, d);
             if (ob > best || (ob == best && oa < at)) {
                 best = ob;
                 at = oa;
             }
         }
         const bool none_left = !(best > none);
-        if (lane == (j & 31)) (j < 32 ? ids.x : ids.y) = none_left ? -1 : at;
+        if (lane == (j & 31)) (j < 32 ? out.x : out.y) = none_left ? -1 : at;
         if (!none_left && lane == 0) key[at] = none;
         __syncwarp();
     }
-    return ids;
+    return out;
 }
 
 template <int V>
 __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
-    extern __shared__ double scratch[];
+    extern __shared__ __align__(16) double scratch[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = (long long)blockIdx.x * kWarps + warp;
     ptx::griddep_wait();
     if (row >= a.n) return;
     double *mine = scratch + (size_t)warp * a.scratch;
+    uint32_t *keys = reinterpret_cast<uint32_t *>(mine + (a.scratch - a.keys));
     const int e0 = lane * V;
 
     // the logits, and the largest of them that takes part
@@ -302,67 +333,69 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
         if (a.bias && ok) {
             const float b = a.bias[e0 + j];
             ok = takes_part(b);
-            c = (softmax ? expf(below(c, m)) * rcp_sum : sigmoid(c)) + b;
+            c = (softmax ? exp_key(c, m) * rcp_sum : sigmoid_key(c)) + b;
         }
         key[j] = ok ? sortable(c + 0.f) : 0u;  // (-0 ties with 0)
     }
     const float err = softmax ? kSoftmaxErr : kSigmoidErr;
 
-    unsigned groups = 1u;
-    bool unsure = false, again = false;
-    float from = 0.f;
-    if (a.groups > 1) {
-        float *keys = reinterpret_cast<float *>(mine);
+    if (V % 4 == 0 && e0 + V <= a.E) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j)
+            reinterpret_cast<uint4 *>(keys + e0)[j] = make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
+    } else {
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E) keys[e0 + j] = key[j] ? unsortable(key[j]) : -INFINITY;
-        __syncwarp();
+            if (e0 + j < a.E) keys[e0 + j] = key[j];
+    }
+    __syncwarp();
+
+    unsigned groups = 1u;
+    bool unsure = false, again = false;
+    if (a.groups > 1) {
         float gap, worst;
         groups = best_groups<float>(a, keys, m, !a.bias, &gap, &worst);
         // errors of two sums of one or two keys
-        if (a.bias || a.top2) {
-            if (!(gap > 2.f * (2.f * err + 0x1p-22f * fabsf(worst)))) {
-                unsure = again = true;
-            }
-        }
+        if ((a.bias || a.top2) && !(gap > 2.f * (2.f * err + 0x1p-22f * fabsf(worst)))) unsure = again = true;
         const int size = a.E / a.groups;
         int g = e0 / size, left = size - (e0 - g * size);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (g >= 32 || !((groups >> g) & 1u)) key[j] = 0u;
+            if (g >= 32 || !((groups >> g) & 1u)) {
+                key[j] = 0u;
+                if (e0 + j < a.E) keys[e0 + j] = 0u;
+            }
             if (--left == 0) {
                 ++g;
                 left = size;
             }
         }
+        __syncwarp();
     }
 
     int2 ids = make_int2(-1, -1);  // of ranks lane and 32 + lane
     if (!unsure) {
-        float last = INFINITY;
-        int last_at = -1;
+        uint32_t best = key[0];  // of this lane's
+#pragma unroll
+        for (int j = 1; j < V; ++j) best = max(best, key[j]);
+        float last = 0.f, from = 0.f;
+        int last_at = -1, next = -1;
         const int ranks = a.bias ? a.k + 1 : a.k;
         for (int r = 0; r < ranks; ++r) {
-            uint32_t best = key[0];
-#pragma unroll
-            for (int j = 1; j < V; ++j) best = max(best, key[j]);
             const uint32_t top = __reduce_max_sync(kAll, best);
             if (top == 0u) break;
-            const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-            int j_at = 0;
-#pragma unroll
-            for (int j = V - 1; j >= 0; --j)
-                if (key[j] == top) j_at = j;
-            if (lane == owner) {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (j == j_at) key[j] = 0u;
-            }
-            const int at = __shfl_sync(kAll, e0 + j_at, owner);
-            if (r < a.k && lane == (r & 31)) (r < 32 ? ids.x : ids.y) = at;
+            const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1, first = owner * V;
+            // its keys, one to a lane
+            const uint32_t k = lane < V && first + lane < a.E ? keys[first + lane] : 0u;
+            const int at_lane = __ffs(__ballot_sync(kAll, k == top)) - 1, at = first + at_lane;
+            const uint32_t rest = __reduce_max_sync(kAll, lane == at_lane ? 0u : k);
+            if (lane == owner) best = rest;
+            if (lane == at_lane) keys[at] = 0u;
+            if (r == a.k) next = at;
+            else if (lane == (r & 31)) (r < 32 ? ids.x : ids.y) = at;
             if (a.bias) {
                 const float c = unsortable(top);
-                const float near = 2.f * (err + 0x1p-23f * (fabsf(c) + (r ? fabsf(last) : 0.f)));
+                const float near = 2.f * (err + 0x1p-23f * (fabsf(c) + fabsf(last)));
                 // (the same logit and the same bias are an exact tie)
                 if (r && !(last - c > near) &&
                     (logit(a, row, at) != logit(a, row, last_at) || a.bias[at] != a.bias[last_at]))
@@ -371,9 +404,12 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                 last = c;
                 last_at = at;
             }
+            __syncwarp();
         }
+        if (unsure) ids = rank_exactly(a, row, false, groups, from, m, ids, next, mine, keys);
+    } else {
+        ids = rank_exactly(a, row, again, groups, 0.f, m, ids, -1, mine, keys);
     }
-    if (unsure) ids = rank_exactly(a, row, again, groups, from, m, rcp_sum, mine);
 
     // weights: lane j has ranks j and 32 + j
     const int id[2] = {ids.x, ids.y};
@@ -411,8 +447,9 @@ cudaError_t launch(RouteArgs a, cudaStream_t st) {
     const int esz = a.dtype == MOE_DTYPE_F32 ? 4 : 2;
     const unsigned piece = min(16, V * esz);  // bytes of a load
     a.vector = ((uintptr_t)a.logits % piece) == 0 && (a.ldl * esz) % piece == 0;
-    // E keys (f64 where a row may have to be ranked again, and the list of its candidates)
-    a.scratch = a.bias || (a.groups > 1 && a.top2) ? a.E + (a.E + 1) / 2 : a.groups > 1 ? (a.E + 1) / 2 : 0;
+    // E keys; and E in f64 where a row may have to be ranked again
+    a.keys = (a.E + 3) / 4 * 2;
+    a.scratch = a.keys + (a.bias || (a.groups > 1 && a.top2) ? (a.E + 1) / 2 * 2 : 0);  // (of 16 bytes' alignment)
     const int smem = kWarps * a.scratch * 8;  // at most 48 KB
     return launch_overlapped(route_kernel<V>, dim3((unsigned)((a.n + kWarps - 1) / kWarps)), 32 * kWarps, smem, 1, st, a);
 }
