@@ -40,7 +40,7 @@ struct RouteArgs {
     bool top2;                   // a group's score is the sum of its best two
     bool renormalize;
     bool vector;                 // rows of logits are aligned for wide loads
-    int scratch, keys;           // doubles of shared memory per warp, and those of its keys
+    int words;                   // of shared memory per warp, 4 bytes each
     float scale;
 };
 

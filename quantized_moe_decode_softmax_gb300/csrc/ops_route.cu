@@ -6,12 +6,13 @@
 //   w_j = s of the j-th, divided by the sum of all of them if asked, times scale.
 //
 // Bound: latency for a few rows, the issue of instructions for many (a row is E logits, a few
-// hundred bytes). One warp takes a row: lane i holds the V experts V i .. V i + V - 1, which
-// makes the lowest lane of a tie the lowest id. A key is its f32 as an unsigned number that
-// sorts alike (0: not available). The keys lie in shared memory and each lane keeps the
-// largest of its own, so that a rank is one redux over the lanes, and another over the V keys
-// of the lane that had it, which V lanes read side by side: about 25 instructions whatever V
-// is (50 for V = 8 and 160 for V = 32 with the keys in registers).
+// hundred bytes). L lanes take a row: all 32 of a warp, so that a row is done soon, or 8 where
+// there are rows enough to fill the SMs, so that an instruction serves four rows
+// (8192 x 256, top 6: 5.5 us, with a bias 10.7; a warp each 9.1 and 14). Lane i holds the V experts V i .. V i + V - 1, which makes the lowest
+// lane of a tie the lowest id. A key is its f32 as an unsigned number that sorts alike
+// (0: not available). The keys lie in shared memory and each lane keeps the largest of its
+// own, so that a rank is one maximum over the lanes, and another over the V keys of the lane
+// that had it, which the lanes read side by side.
 //
 // The ids are those of exact scores. Without a bias the order of c is the order of the
 // logits, and no score is computed for it. With a bias (or with sums of two per group)
@@ -26,8 +27,9 @@ namespace moe {
 namespace ops {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kMaxK = 64;
+constexpr int kManyRows = 4096;  // rows from which on eight lanes take one
 
 // Error of an f32 score of a key (at most 1). Sigmoid: the argument's rounding moves the result
 // by at most |l| s (1 - s) 2^-24 < 2^-26, exp2 and the reciprocal are good to 2^-22, 1 + e rounds
@@ -71,42 +73,63 @@ __device__ __forceinline__ double sigmoid(double l) {
 // l - m with m >= l, where infinities of both are equal
 __device__ __forceinline__ float below(float l, float m) { return l == m ? 0.f : l - m; }
 
-__device__ __forceinline__ float warp_max(float v) {
+// over the L lanes of a row
+template <int L> __device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    for (int d = L / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
     return v;
 }
-template <typename F> __device__ __forceinline__ F warp_sum(F v) {
+template <int L> __device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    if constexpr (L == 32) {
+        return __reduce_max_sync(kAll, v);
+    } else {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+        for (int d = L / 2; d; d >>= 1) v = max(v, __shfl_xor_sync(kAll, v, d));
+        return v;
+    }
+}
+template <int L, typename F> __device__ __forceinline__ F row_sum(F v) {
+#pragma unroll
+    for (int d = L / 2; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
+}
+// the lanes of the own row where `p` holds, the row's first lane in bit 0
+template <int L> __device__ __forceinline__ unsigned row_ballot(bool p) {
+    const unsigned m = __ballot_sync(kAll, p);
+    if constexpr (L == 32) return m;
+    else return (m >> (threadIdx.x & 31 & ~(L - 1))) & ((1u << L) - 1u);
 }
 
-// Which groups stay, as a mask of bits, by the keys of all experts in `key` (shared memory; f32
-// as sortable numbers, or f64 with -inf for those not available). F: the precision. 32 / 2^ceil(log2 groups) lanes share a
-// group. *gap: the distance of the worst group that stays from the best that does not
-// (inf if there are not both). logits: the keys are logits, and a sum of two is one of
-// their scores.
+// The place of expert e among a row's keys: the V of a lane and 4 more, so that 16-byte accesses of
+// eight lanes side by side meet different banks.
+template <int V> struct Keys {
+    uint32_t *at;
+    __device__ __forceinline__ static int place(int e) { return e / V * (V + 4) + e % V; }
+    __device__ __forceinline__ uint32_t &operator[](int e) const { return at[place(e)]; }
+};
+
 __device__ __forceinline__ float key_value(uint32_t k) { return k ? unsortable(k) : -INFINITY; }
 __device__ __forceinline__ double key_value(double k) { return k; }
 
-template <typename F, typename K>
-__device__ unsigned best_groups(const RouteArgs &a, const K *key, float max_logit, bool logits, F *gap, F *worst) {
-    const int lane = threadIdx.x & 31, size = a.E / a.groups;
-    int per = 32;  // lanes per group
-    while (32 / per < a.groups) per >>= 1;
+// Which groups stay, as a mask of bits, by the keys of all experts (f32 as sortable numbers, or
+// f64 with -inf for those not available), by the L lanes of a row; at most L groups, L / 2^ceil(log2
+// groups) lanes share one. F: the precision. *gap: the distance of the worst group that stays from
+// the best that does not (inf if there are not both). logits: the keys are logits, and a sum of
+// two is one of their scores. cut, unless null: for each group the least key that its score has.
+template <int L, typename F, typename K>
+__device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key, float max_logit, bool logits, F *gap,
+                                                F *worst, float *cut) {
+    const int lane = threadIdx.x & (L - 1), size = a.E / a.groups;
+    int per = L;  // lanes per group
+    while (L / per < a.groups) per >>= 1;
     const int g = lane / per;
     const F none = -INFINITY;
     F m1 = none, m2 = none;
     if (g < a.groups)
         for (int i = lane % per; i < size; i += per) {
             const F v = key_value(key[g * size + i]);
-            if (v > m1) {
-                m2 = m1;
-                m1 = v;
-            } else if (v > m2) {
-                m2 = v;
-            }
+            m2 = v > m1 ? m1 : v > m2 ? v : m2;
+            m1 = v > m1 ? v : m1;
         }
     for (int d = 1; d < per; d <<= 1) {
         const F o1 = __shfl_xor_sync(kAll, m1, d), o2 = __shfl_xor_sync(kAll, m2, d);
@@ -115,6 +138,7 @@ __device__ unsigned best_groups(const RouteArgs &a, const K *key, float max_logi
         m2 = o2 > m2 ? o2 : m2;
         m2 = lo > m2 ? lo : m2;
     }
+    if (cut && g < a.groups && lane % per == 0) cut[g] = (float)(a.top2 && m2 > none ? m2 : m1);
     F score = m1;
     if (a.top2) {
         if (logits && m1 > none) {
@@ -133,153 +157,172 @@ __device__ unsigned best_groups(const RouteArgs &a, const K *key, float max_logi
     }
     int before = 0;
     for (int o = 0; o < a.groups; ++o) {
-        const F s = __shfl_sync(kAll, score, o * per);
+        const F s = __shfl_sync(kAll, score, o * per, L);
         before += s > score || (s == score && o < g);
     }
     const bool live = g < a.groups && m1 > none, stays = live && before < a.top_groups;
     F w = stays ? score : (F)INFINITY, b = live && !stays ? score : none;
-    for (int d = 16; d; d >>= 1) {
+    for (int d = L / 2; d; d >>= 1) {
         const F ow = __shfl_xor_sync(kAll, w, d), ob = __shfl_xor_sync(kAll, b, d);
         w = ow < w ? ow : w;
         b = ob > b ? ob : b;
     }
     *gap = w == (F)INFINITY || b == none ? (F)INFINITY : w - b;
     *worst = w;
+    // bit o: group o's lanes, the first of each
+    const unsigned lanes = row_ballot<L>(stays);
     unsigned mask = 0;
-    for (int o = 0; o < a.groups; ++o) mask |= ((__ballot_sync(kAll, stays) >> (o * per)) & 1u) << o;
+    for (int o = 0; o < a.groups; ++o) mask |= ((lanes >> (o * per)) & 1u) << o;
     return mask;
 }
 
-// The row again in f64: the ids of ranks lane and 32 + lane (-1: none left). again: the
-// groups too; otherwise only experts with a key (of those left in `list`) of at least
-// `from`, and those of `ids`, can be among the first. key: E doubles of this warp; list: its
-// sortable keys, which the ids in question replace.
-__device__ __noinline__ int2 rank_exactly(const RouteArgs &a, long long row, bool again, unsigned groups, float from,
-                                          float max_logit, int2 ids, int next, double *key, uint32_t *list) {
-    const int lane = threadIdx.x & 31, size = a.E / a.groups;
-    const double none = -INFINITY;
-    __syncwarp();
-    double sum = 1.0;
-    if (a.score == MOE_SCORE_SOFTMAX && a.bias) {
-        sum = 0.0;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit(a, row, e);
-            if (takes_part(l)) sum += l == max_logit ? 1.0 : exp((double)l - (double)max_logit);
-        }
-        sum = warp_sum(sum);
+// c_e of one expert in f64 (without a bias its logit, which has the same order). sum: the divisor of a
+// softmax
+__device__ __forceinline__ double exact_key(const RouteArgs &a, long long row, int e, float max_logit, double sum) {
+    const float l = logit(a, row, e);
+    if (!a.bias) return l;
+    const double s = a.score == MOE_SCORE_SOFTMAX ? (l == max_logit ? 1.0 : exp((double)l - (double)max_logit)) / sum
+                                                  : sigmoid((double)l);
+    return s + (double)a.bias[e];
+}
+
+__device__ __forceinline__ double exact_sum(const RouteArgs &a, long long row, float max_logit) {
+    if (a.score != MOE_SCORE_SOFTMAX || !a.bias) return 1.0;
+    double sum = 0.0;
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+        const float l = logit(a, row, e);
+        if (takes_part(l)) sum += l == max_logit ? 1.0 : exp((double)l - (double)max_logit);
     }
-    // the experts in question are dealt to the lanes: an f64 exponential takes a warp as
-    // long for one lane as for 32
+    return row_sum<32>(sum);
+}
+
+// The experts whose key, among the row's keys at `list`, is at least what `least` says for them:
+// their ids replace the keys, in order; how many. By a whole warp. (The experts in question
+// are then dealt to the lanes: an f64 exponential takes a warp as long for one lane as for 32.)
+template <int V, typename F> __device__ __forceinline__ int pick_experts(const RouteArgs &a, uint32_t *list, F least) {
+    const int lane = threadIdx.x & 31;
     int found = 0;
-    auto add = [&](bool take, int e) {
-        const unsigned m = __ballot_sync(0xffffffffu, take);
-        if (take) list[found + __popc(m & ((1u << lane) - 1u))] = (uint32_t)e;
-        found += __popc(m);
-    };
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
-        bool take = false;
-        if (e < a.E) {
-            if (again) take = takes_part(logit(a, row, e)) && (!a.bias || takes_part(a.bias[e]));
-            else take = list[e] && unsortable(list[e]) >= from;
-        }
-        __syncwarp();
-        add(take, e);  // (never beyond what has been read)
+        const uint32_t k = e < a.E ? list[Keys<V>::place(e)] : 0u;
+        const bool take = k && unsortable(k) >= least(e);
+        const unsigned m = __ballot_sync(kAll, take);
+        if (take) list[found + __popc(m & ((1u << lane) - 1u))] = (uint32_t)e;  // (never beyond what has been read)
+        found += __popc(m);
         __syncwarp();
     }
-    if (!again) {  // the ranks so far, and the next one, have no keys any more
-        add(ids.x >= 0, ids.x);
-        add(ids.y >= 0, ids.y);
-        add(lane == 0 && next >= 0, next);
-    }
+    return found;
+}
+
+// The groups of one row again in f64, by a whole warp: their mask. cut: best_groups'. key: E doubles;
+// list: the row's keys, which are lost.
+template <int V>
+__device__ __noinline__ unsigned groups_exactly(const RouteArgs &a, long long row, float err, float max_logit,
+                                                const float *cut, double *key, uint32_t *list) {
+    const int lane = threadIdx.x & 31, size = a.E / a.groups;
+    for (int e = lane; e < a.E; e += 32) key[e] = -INFINITY;
+    const double sum = exact_sum(a, row, max_logit);
+    const int found = pick_experts<V>(a, list, [&](int e) {
+        const float c = cut[e / size];
+        return !a.bias || c == INFINITY ? c : c - (4.f * err + 0x1p-21f * fabsf(c));
+    });
+    for (int i = lane; i < found; i += 32) key[list[i]] = exact_key(a, row, (int)list[i], max_logit, sum);
     __syncwarp();
-    auto score = [&](int e) -> double {
-        const float l = logit(a, row, e);
-        if (!a.bias) return l;  // the order of the logits
-        const double s = a.score == MOE_SCORE_SOFTMAX
-                             ? (l == max_logit ? 1.0 : exp((double)l - (double)max_logit)) / sum
-                             : sigmoid((double)l);
-        return s + (double)a.bias[e];
-    };
-    int2 out = make_int2(-1, -1);
-    if (!again && found <= 32 && a.k <= 32) {
+    double gap, worst;
+    return best_groups<32, double>(a, key, max_logit, !a.bias, &gap, &worst, nullptr);
+}
+
+// The ranks of one row again in f64, by a whole warp. Only the experts that `ranks` has (`ranked` of
+// them), and others that are left with a key of at least `from`, can be among the first. key: E
+// doubles; list: the row's keys, which are lost.
+template <int V>
+__device__ __noinline__ void rank_exactly(const RouteArgs &a, long long row, float from, float max_logit, int *ranks,
+                                          int ranked, double *key, uint32_t *list) {
+    const int lane = threadIdx.x & 31;
+    const double none = -INFINITY, sum = exact_sum(a, row, max_logit);
+    int found = pick_experts<V>(a, list, [&](int) { return from; });
+    for (int r = lane; r < ranked; r += 32) list[found + r] = (uint32_t)ranks[r];  // (these have no key any more)
+    found += ranked;
+    __syncwarp();
+    if (found <= 32) {
         // one each: a rank is the number of lanes that come before
         const int e = lane < found ? (int)list[lane] : 0x7fffffff;
-        const double c = lane < found ? score(e) : none;
+        const double c = lane < found ? exact_key(a, row, e, max_logit, sum) : none;
         int rank = 0;
         for (int i = 0; i < found; ++i) {
-            const double o = __shfl_sync(0xffffffffu, c, i);
-            const int oe = __shfl_sync(0xffffffffu, e, i);
+            const double o = __shfl_sync(kAll, c, i);
+            const int oe = __shfl_sync(kAll, e, i);
             rank += o > c || (o == c && oe < e);
         }
+        if (lane < found) ranks[rank] = e;
         __syncwarp();
-        if (lane < found) list[rank] = (uint32_t)e;
-        __syncwarp();
-        if (lane < a.k && lane < found) out.x = (int)list[lane];
-        return out;
+        return;
     }
-    if (again)
-        for (int e = lane; e < a.E; e += 32) key[e] = none;
+    for (int i = lane; i < found; i += 32) key[list[i]] = exact_key(a, row, (int)list[i], max_logit, sum);
     __syncwarp();
-    for (int i = lane; i < found; i += 32) key[list[i]] = score((int)list[i]);
-    __syncwarp();
-    if (again && a.groups > 1) {
-        double gap, worst;
-        groups = best_groups<double>(a, key, max_logit, !a.bias, &gap, &worst);
-    }
     for (int j = 0; j < a.k; ++j) {
         double best = none;
         int at = 0x7fffffff;
         for (int i = lane; i < found; i += 32) {
             const int e = (int)list[i];
             const double c = key[e];
-            if (((groups >> (e / size)) & 1u) && (c > best || (c == best && c > none && e < at))) {
+            if (c > best || (c == best && c > none && e < at)) {
                 best = c;
                 at = e;
             }
         }
         for (int d = 16; d; d >>= 1) {
-            const double ob = __shfl_xor_sync(0xffffffffu, best, d);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, d);
+            const double ob = __shfl_xor_sync(kAll, best, d);
+            const int oa = __shfl_xor_sync(kAll, at, d);
             if (ob > best || (ob == best && oa < at)) {
                 best = ob;
                 at = oa;
             }
         }
         const bool none_left = !(best > none);
-        if (lane == (j & 31)) (j < 32 ? out.x : out.y) = none_left ? -1 : at;
-        if (!none_left && lane == 0) key[at] = none;
+        if (lane == 0) {
+            ranks[j] = none_left ? -1 : at;
+            if (!none_left) key[at] = none;
+        }
         __syncwarp();
     }
-    return out;
 }
 
-template <int V>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
-    extern __shared__ __align__(16) double scratch[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = (long long)blockIdx.x * kWarps + warp;
+// shared memory of a warp in 4-byte words: its rows' keys, ranks and weights; E doubles
+__host__ __device__ constexpr int row_words(int L, int V) { return L * (V + 4) + kMaxK + 4 + kMaxK; }
+__host__ __device__ constexpr int warp_words(int L, int V, int E, bool f64) {
+    return 32 / L * row_words(L, V) + (f64 ? (2 * E + 3) / 4 * 4 : 0);
+}
+
+template <int L, int V>
+__global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
+    extern __shared__ __align__(16) uint32_t words[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
+    const long long first_row = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) * (32 / L);
+    const long long row = first_row + lane / L;
+    const bool live = row < a.n;
     ptx::griddep_wait();
-    if (row >= a.n) return;
-    double *mine = scratch + (size_t)warp * a.scratch;
-    uint32_t *keys = reinterpret_cast<uint32_t *>(mine + (a.scratch - a.keys));
-    const int e0 = lane * V;
+    if (first_row >= a.n) return;
+    uint32_t *own = words + (size_t)warp * a.words;
+    uint32_t *mine = own + lane / L * row_words(L, V);
+    const Keys<V> keys{mine};
+    int *ranks = reinterpret_cast<int *>(mine + L * (V + 4));
+    float *weights = reinterpret_cast<float *>(mine + L * (V + 4) + kMaxK + 4);
+    const int e0 = sub * V;
 
     // the logits, and the largest of them that takes part
     float l[V];
     const size_t esz = a.dtype == MOE_DTYPE_F32 ? 4 : 2;
     const char *src = static_cast<const char *>(a.logits) + ((size_t)row * a.ldl + e0) * esz;
-    if (a.vector && e0 + V <= a.E) {
+    if (live && a.vector && e0 + V <= a.E) {
         if (a.dtype == MOE_DTYPE_F32) {
-            if constexpr (V >= 4) {
 #pragma unroll
-                for (int j = 0; j < V / 4; ++j) {
-                    const float4 v = reinterpret_cast<const float4 *>(src)[j];
-                    l[4 * j] = v.x;
-                    l[4 * j + 1] = v.y;
-                    l[4 * j + 2] = v.z;
-                    l[4 * j + 3] = v.w;
-                }
+            for (int j = 0; j < V / 4; ++j) {
+                const float4 v = reinterpret_cast<const float4 *>(src)[j];
+                l[4 * j] = v.x;
+                l[4 * j + 1] = v.y;
+                l[4 * j + 2] = v.z;
+                l[4 * j + 3] = v.w;
             }
         } else {
             uint32_t v[V / 2];
@@ -297,22 +340,33 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
                     v[4 * j + 3] = w.w;
                 }
             }
+            if (a.dtype == MOE_DTYPE_BF16) {
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                const float2 f = a.dtype == MOE_DTYPE_BF16 ? unpack2<__nv_bfloat16>(v[j]) : unpack2<__half>(v[j]);
-                l[2 * j] = f.x;
-                l[2 * j + 1] = f.y;
+                for (int j = 0; j < V / 2; ++j) {
+                    const float2 f = unpack2<__nv_bfloat16>(v[j]);
+                    l[2 * j] = f.x;
+                    l[2 * j + 1] = f.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const float2 f = unpack2<__half>(v[j]);
+                    l[2 * j] = f.x;
+                    l[2 * j + 1] = f.y;
+                }
             }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) l[j] = e0 + j < a.E ? logit(a, row, e0 + j) : -INFINITY;
+        for (int j = 0; j < V; ++j) l[j] = live && e0 + j < a.E ? logit(a, row, e0 + j) : -INFINITY;
     }
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
     float m = -INFINITY;
+    if (softmax) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);  // (a NaN is passed over)
-    if (softmax) m = warp_max(m);
+        for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);  // (a NaN is passed over)
+        m = row_max<L>(m);
+    }
 
     // the divisor of a softmax, where its scores themselves are asked for
     float rcp_sum = 1.f;
@@ -321,146 +375,194 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (takes_part(l[j])) t += expf(below(l[j], m));
-        rcp_sum = 1.0f / warp_sum(t);
+        rcp_sum = 1.0f / row_sum<L>(t);
     }
 
     // sortable keys; 0: takes no part
-    uint32_t key[V];
+    uint32_t key[V], best = 0u;
+    if (!a.bias) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float c = l[j];
-        bool ok = takes_part(c);
-        if (a.bias && ok) {
-            const float b = a.bias[e0 + j];
-            ok = takes_part(b);
-            c = (softmax ? exp_key(c, m) * rcp_sum : sigmoid_key(c)) + b;
-        }
-        key[j] = ok ? sortable(c + 0.f) : 0u;  // (-0 ties with 0)
-    }
-    const float err = softmax ? kSoftmaxErr : kSigmoidErr;
-
-    if (V % 4 == 0 && e0 + V <= a.E) {
-#pragma unroll
-        for (int j = 0; j < V / 4; ++j)
-            reinterpret_cast<uint4 *>(keys + e0)[j] = make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
+        for (int j = 0; j < V; ++j) key[j] = takes_part(l[j]) ? sortable(l[j] + 0.f) : 0u;  // (-0 ties with 0)
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E) keys[e0 + j] = key[j];
+        for (int j = 0; j < V; ++j) {
+            const float b = e0 + j < a.E ? a.bias[e0 + j] : -INFINITY;
+            const float c = (softmax ? exp_key(l[j], m) * rcp_sum : sigmoid_key(l[j])) + b;
+            key[j] = takes_part(l[j]) && takes_part(b) ? sortable(c + 0.f) : 0u;
+        }
     }
+    const float err = softmax ? kSoftmaxErr : kSigmoidErr;
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j)
+        *reinterpret_cast<uint4 *>(mine + sub * (V + 4) + 4 * j) =
+            make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
     __syncwarp();
 
-    unsigned groups = 1u;
-    bool unsure = false, again = false;
+    double *const f64 = reinterpret_cast<double *>(own + 32 / L * row_words(L, V));
     if (a.groups > 1) {
         float gap, worst;
-        groups = best_groups<float>(a, keys, m, !a.bias, &gap, &worst);
+        unsigned groups = best_groups<L, float>(a, keys, m, !a.bias, &gap, &worst, weights);
         // errors of two sums of one or two keys
-        if ((a.bias || a.top2) && !(gap > 2.f * (2.f * err + 0x1p-22f * fabsf(worst)))) unsure = again = true;
+        const bool unsure = live && (a.bias || a.top2) && !(gap > 2.f * (2.f * err + 0x1p-22f * fabsf(worst)));
+        __syncwarp();
+        for (unsigned flagged = __ballot_sync(kAll, sub == 0 && unsure); flagged; flagged &= flagged - 1) {
+            const int at = __ffs(flagged) - 1;
+            uint32_t *words_of = own + at / L * row_words(L, V);
+            const unsigned g = groups_exactly<V>(a, first_row + at / L, err, __shfl_sync(kAll, m, at),
+                                                 reinterpret_cast<float *>(words_of + L * (V + 4) + kMaxK + 4), f64, words_of);
+            if (lane / L == at / L) groups = g;
+        }
         const int size = a.E / a.groups;
         int g = e0 / size, left = size - (e0 - g * size);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (g >= 32 || !((groups >> g) & 1u)) {
-                key[j] = 0u;
-                if (e0 + j < a.E) keys[e0 + j] = 0u;
-            }
+            if (g >= 32 || !((groups >> g) & 1u)) key[j] = 0u;
             if (--left == 0) {
                 ++g;
                 left = size;
             }
         }
         __syncwarp();
-    }
-
-    int2 ids = make_int2(-1, -1);  // of ranks lane and 32 + lane
-    if (!unsure) {
-        uint32_t best = key[0];  // of this lane's
 #pragma unroll
-        for (int j = 1; j < V; ++j) best = max(best, key[j]);
-        float last = 0.f, from = 0.f;
-        int last_at = -1, next = -1;
-        const int ranks = a.bias ? a.k + 1 : a.k;
-        for (int r = 0; r < ranks; ++r) {
-            const uint32_t top = __reduce_max_sync(kAll, best);
-            if (top == 0u) break;
-            const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1, first = owner * V;
-            // its keys, one to a lane
-            const uint32_t k = lane < V && first + lane < a.E ? keys[first + lane] : 0u;
-            const int at_lane = __ffs(__ballot_sync(kAll, k == top)) - 1, at = first + at_lane;
-            const uint32_t rest = __reduce_max_sync(kAll, lane == at_lane ? 0u : k);
-            if (lane == owner) best = rest;
-            if (lane == at_lane) keys[at] = 0u;
-            if (r == a.k) next = at;
-            else if (lane == (r & 31)) (r < 32 ? ids.x : ids.y) = at;
-            if (a.bias) {
-                const float c = unsortable(top);
-                const float near = 2.f * (err + 0x1p-23f * (fabsf(c) + fabsf(last)));
-                // (the same logit and the same bias are an exact tie)
-                if (r && !(last - c > near) &&
-                    (logit(a, row, at) != logit(a, row, last_at) || a.bias[at] != a.bias[last_at]))
-                    unsure = true;
-                from = c == INFINITY ? 3.0e38f : c - 2.f * near;
-                last = c;
-                last_at = at;
+        for (int j = 0; j < V / 4; ++j)
+            *reinterpret_cast<uint4 *>(mine + sub * (V + 4) + 4 * j) =
+                make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) best = max(best, key[j]);
+
+    // The ranks: P keys of the owner to a lane
+    constexpr int P = V > L ? V / L : 1;
+    const int places = a.bias ? a.k + 1 : a.k;  // (with a bias one more, for its distance)
+    bool unsure = false;
+    float last = 0.f, from = INFINITY;  // of the row: the key of the last rank; the least of them, less the errors
+    int ranked = 0;
+    for (int r0 = 0; r0 < places; r0 += L) {
+        uint32_t held = 0u;  // the key of rank r0 + sub
+        const int here = min(L, places - r0);
+        for (int i = 0; i < here; ++i) {
+            const uint32_t top = row_max<L>(best);
+            const int owner = __ffs(row_ballot<L>(best == top)) - 1;
+            uint32_t *theirs = mine + owner * (V + 4) + sub * P;
+            uint32_t k[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) k[q] = 0u;
+            if (P > 1 || sub < V) {
+                if constexpr (P == 4) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(theirs);
+                    k[0] = w.x;
+                    k[1] = w.y;
+                    k[2] = w.z;
+                    k[3] = w.w;
+                } else if constexpr (P == 2) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(theirs);
+                    k[0] = w.x;
+                    k[1] = w.y;
+                } else {
+                    k[0] = theirs[0];
+                }
             }
+            int at = P;
+#pragma unroll
+            for (int q = P - 1; q >= 0; --q)
+                if (k[q] == top) at = q;
+            const int first = __ffs(row_ballot<L>(at < P && top)) - 1;  // (-1: none left)
+            if (sub == first) {
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    if (q == at) k[q] = 0u;
+                theirs[at] = 0u;
+                ranks[r0 + i] = owner * V + sub * P + at;
+            }
+            if (first < 0 && sub == 0) ranks[r0 + i] = -1;
+            uint32_t rest = k[0];
+#pragma unroll
+            for (int q = 1; q < P; ++q) rest = max(rest, k[q]);
+            rest = row_max<L>(rest);
+            if (sub == owner) best = rest;
+            if (sub == i) held = top;
             __syncwarp();
         }
-        if (unsure) ids = rank_exactly(a, row, false, groups, from, m, ids, next, mine, keys);
-    } else {
-        ids = rank_exactly(a, row, again, groups, 0.f, m, ids, -1, mine, keys);
+        if (a.bias) {
+            const bool has = held != 0u;
+            const float c = has ? unsortable(held) : 0.f, up = __shfl_up_sync(kAll, c, 1, L), before = sub ? up : last;
+            const float near = 2.f * (err + 0x1p-23f * (fabsf(c) + (r0 + sub ? fabsf(before) : 0.f)));
+            bool close = has && r0 + sub > 0 && !(before - c > near);
+            if (close) {  // the same logit and the same bias are an exact tie
+                const int i = ranks[r0 + sub], j = ranks[r0 + sub - 1];
+                close = logit(a, row, i) != logit(a, row, j) || a.bias[i] != a.bias[j];
+            }
+            unsure |= row_ballot<L>(close) != 0u;  // (every lane votes, whatever its row has found)
+            from = fminf(from, has ? (c == INFINITY ? 3.0e38f : c - 2.f * near) : INFINITY);
+            last = __shfl_sync(kAll, c, L - 1, L);
+            ranked += __popc(row_ballot<L>(has));
+        }
     }
+    // rows to be ranked again, one after another by the whole warp
+    for (unsigned flagged = __ballot_sync(kAll, sub == 0 && unsure); flagged; flagged &= flagged - 1) {
+        const int at = __ffs(flagged) - 1;
+        const float f = -row_max<L>(-from);  // the lanes of the row have theirs
+        uint32_t *words_of = own + at / L * row_words(L, V);
+        rank_exactly<V>(a, first_row + at / L, __shfl_sync(kAll, f, at), __shfl_sync(kAll, m, at),
+                        reinterpret_cast<int *>(words_of + L * (V + 4)), __shfl_sync(kAll, ranked, at), f64, words_of);
+    }
+    __syncwarp();
 
-    // weights: lane j has ranks j and 32 + j
-    const int id[2] = {ids.x, ids.y};
-    float z[2], w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) z[h] = id[h] >= 0 ? logit(a, row, id[h]) : -INFINITY;
+    // weights, of L ranks at a time
     float top = -INFINITY;
-    if (a.renormalize) top = warp_max(fmaxf(z[0], z[1]));
+    for (int r = sub; r < a.k; r += L) {
+        const int id = ranks[r];
+        const float z = live && id >= 0 ? logit(a, row, id) : -INFINITY;
+        weights[r] = z;
+        top = fmaxf(top, z);
+    }
+    if (a.renormalize) top = row_max<L>(top);
     // relative to the largest chosen logit where that keeps small scores in range: they are
     // divided by their sum. (exp(l) is all of a sigmoid below -40.)
     const bool shifted = a.renormalize && (softmax || top < -40.f);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (id[h] < 0) w[h] = 0.f;
-        else if (shifted) w[h] = expf(below(z[h], top));
-        else w[h] = softmax ? expf(below(z[h], m)) * rcp_sum : sigmoid(z[h]);
+    float by = a.scale, sum = 0.f;
+    for (int r = sub; r < a.k; r += L) {
+        const float z = weights[r];
+        float w = 0.f;
+        if (z > -INFINITY) w = shifted ? expf(below(z, top)) : softmax ? expf(below(z, m)) * rcp_sum : sigmoid(z);
+        weights[r] = w;
+        sum += w;
     }
-    float by = a.scale;
     if (a.renormalize) {
-        const float sum = warp_sum(w[0] + w[1]);
+        sum = row_sum<L>(sum);
         by = sum > 0.f ? a.scale / sum : 0.f;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = lane + 32 * h;
-        if (r < a.k) {
-            a.topk_idx[row * a.k + r] = id[h];
-            a.topk_w[row * a.k + r] = w[h] * by;
-        }
+    if (!live) return;
+    for (int r = sub; r < a.k; r += L) {
+        a.topk_idx[row * a.k + r] = ranks[r];
+        a.topk_w[row * a.k + r] = weights[r] * by;
     }
 }
 
-template <int V>
+template <int L, int V>
 cudaError_t launch(RouteArgs a, cudaStream_t st) {
     const int esz = a.dtype == MOE_DTYPE_F32 ? 4 : 2;
     const unsigned piece = min(16, V * esz);  // bytes of a load
     a.vector = ((uintptr_t)a.logits % piece) == 0 && (a.ldl * esz) % piece == 0;
-    // E keys; and E in f64 where a row may have to be ranked again
-    a.keys = (a.E + 3) / 4 * 2;
-    a.scratch = a.keys + (a.bias || (a.groups > 1 && a.top2) ? (a.E + 1) / 2 * 2 : 0);  // (of 16 bytes' alignment)
-    const int smem = kWarps * a.scratch * 8;  // at most 48 KB
-    return launch_overlapped(route_kernel<V>, dim3((unsigned)((a.n + kWarps - 1) / kWarps)), 32 * kWarps, smem, 1, st, a);
+    a.words = warp_words(L, V, a.E, a.bias || (a.groups > 1 && a.top2));
+    const int warps = min(4, 48 * 1024 / (4 * a.words)), rows = warps * (32 / L);
+    return launch_overlapped(route_kernel<L, V>, dim3((unsigned)((a.n + rows - 1) / rows)), 32 * warps, 4 * warps * a.words,
+                             1, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
-    if (a.E <= 128) return launch<4>(a, st);
-    if (a.E <= 256) return launch<8>(a, st);
-    if (a.E <= 512) return launch<16>(a, st);
-    return launch<32>(a, st);
+    if (a.n >= kManyRows && a.E <= 256 && a.groups <= 8) {
+        if (a.E <= 64) return launch<8, 8>(a, st);
+        if (a.E <= 128) return launch<8, 16>(a, st);
+        return launch<8, 32>(a, st);
+    }
+    if (a.E <= 128) return launch<32, 4>(a, st);
+    if (a.E <= 256) return launch<32, 8>(a, st);
+    if (a.E <= 512) return launch<32, 16>(a, st);
+    return launch<32, 32>(a, st);
 }
 
 }  // namespace ops
