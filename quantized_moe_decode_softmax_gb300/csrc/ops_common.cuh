@@ -83,17 +83,17 @@ __device__ __forceinline__ float unary_act(int act, float z) {
     return z * (rcp_fast(k + exp2_fast(t)) * k);
 }
 
-// the same on 16 values, branching once
-__device__ __forceinline__ void unary_act_all(int act, float (&v)[16]) {
+// the same on N values, branching once
+template <int N> __device__ __forceinline__ void unary_act_all(int act, float (&v)[N]) {
     if (act == MOE_EPI_SILU) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = unary_act(MOE_EPI_SILU, v[j]);
+        for (int j = 0; j < N; ++j) v[j] = unary_act(MOE_EPI_SILU, v[j]);
     } else if (act == MOE_EPI_GELU) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = unary_act(MOE_EPI_GELU, v[j]);
+        for (int j = 0; j < N; ++j) v[j] = unary_act(MOE_EPI_GELU, v[j]);
     } else if (act == MOE_EPI_GELU_TANH) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = unary_act(MOE_EPI_GELU_TANH, v[j]);
+        for (int j = 0; j < N; ++j) v[j] = unary_act(MOE_EPI_GELU_TANH, v[j]);
     }
 }
 

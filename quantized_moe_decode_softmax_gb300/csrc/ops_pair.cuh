@@ -319,7 +319,8 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
                                             float *row_scale) {
     const int lane = threadIdx.x & 31;
     const int q = w & 3;      // the lanes this warp can read
-    const int part = w >> 2;  // its half of the tile's chunks of 16 rows
+    const int part = w >> 2;  // its half of the tile's pieces of 16 rows
+    constexpr int W = 16;     // rows of a chunk
     const uint32_t tlane = tmem + ((uint32_t)(32 * q) << 16);
     int n = 0;
     Item it;
@@ -357,16 +358,16 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
         // a residual is read two chunks ahead, the first two before the tile is done (SCALED,
         // where more warps share the registers: one); the values stay as loaded until they
         // are used, so that nothing waits for them earlier
-        uint32_t ra[16], rb[SCALED ? 1 : 16];
-        auto load_res = [&](uint32_t (&d)[16], int t0) {
+        uint32_t ra[W], rb[SCALED ? 1 : W];
+        auto load_res = [&](uint32_t (&d)[W], int t0) {
             const char *s = res + 2 * (size_t)t0 * p.ldr;
             if (g.paired) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j, s += rstep)
+                for (int j = 0; j < W / 2; ++j, s += rstep)
                     if (t0 + 2 * j + odd < rows) d[j] = *reinterpret_cast<const uint32_t *>(s);
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j, s += rstep)
+                for (int j = 0; j < W; ++j, s += rstep)
                     if (t0 + j < rows) d[j] = *reinterpret_cast<const uint16_t *>(s);
             }
         };
@@ -383,8 +384,8 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             tc::fence_before_sync();
             if (lane == 0) arrive_cluster(in_first(acc_empty_addr + 8 * buf));
         };
-        auto chunk = [&](int t0, uint32_t (&r)[16]) {
-            float v[16], u[MATS == 2 ? 16 : 1];
+        auto chunk = [&](int t0, uint32_t (&r)[W]) {
+            float v[W], u[MATS == 2 ? W : 1];
             tmem_ld16(acc + t0, v);
             if constexpr (MATS == 2) tmem_ld16(acc + g.tcap + t0, u);
             tmem_wait_ld();
@@ -392,24 +393,27 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             if constexpr (SCALED) {
                 const float4 *s = reinterpret_cast<const float4 *>(row_scale + ((t0 - 16 * part) >> 1));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < W / 4; ++j) {
                     const float4 f = s[j];
                     const float by[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        v[4 * j + i] *= by[i] * s0;
-                        if constexpr (MATS == 2) u[4 * j + i] *= by[i] * s1;
+                        v[4 * j + i] = fmaf(v[4 * j + i] * by[i], s0, b0);
+                        if constexpr (MATS == 2) u[4 * j + i] = fmaf(u[4 * j + i] * by[i], s1, b1);
                     }
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] += b0;
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += b0;
             if constexpr (MATS == 2) {
+                if constexpr (!SCALED) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) u[j] += b1;
+                    for (int j = 0; j < W; ++j) u[j] += b1;
+                }
                 if (p.limit > 0.f) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < W; ++j) {
                         v[j] = clamp_hi(v[j], p.limit);
                         u[j] = clamp_lo(clamp_hi(u[j], p.limit), -p.limit);
                     }
@@ -418,11 +422,11 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             if (p.act != MOE_EPI_NONE) unary_act_all(p.act, v);
             if constexpr (MATS == 2) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] *= u[j];
+                for (int j = 0; j < W; ++j) v[j] *= u[j];
             }
             if (res) {  // (unset past the end of the tile, where nothing is stored)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < W / 2; ++j) {
                     const uint32_t two = g.paired ? __byte_perm(r[j], __shfl_xor_sync(0xffffffffu, r[j], 1), trade)
                                                   : __byte_perm(r[2 * j], r[2 * j + 1], 0x5410u);
                     const float2 f = unpack2<T>(two);
@@ -434,24 +438,29 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             char *o = out + 2 * (size_t)t0 * p.ldo;
             if (g.paired) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j, o += ostep) {
+                for (int j = 0; j < W / 2; ++j, o += ostep) {
                     const uint32_t w = pack2<T>(v[2 * j], v[2 * j + 1]);
                     const uint32_t x = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), trade);
                     if (t0 + 2 * j + odd < rows) *reinterpret_cast<uint32_t *>(o) = x;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j, o += ostep)
+                for (int j = 0; j < W; ++j, o += ostep)
                     if (t0 + j < rows) *reinterpret_cast<T *>(o) = from_f32<T>(v[j]);
             }
         };
+        if constexpr (SCALED && MATS == 1) {  // (one copy of the code: it is fetched anew for each tile)
 #pragma unroll 1
-        for (int t0 = 16 * part; t0 < it.rows; t0 += 64) {
-            chunk(t0, ra);
-            if constexpr (SCALED) {
-                if (t0 + 32 < it.rows) chunk(t0 + 32, ra);
-            } else {
-                if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
+            for (int t0 = 16 * part; t0 < it.rows; t0 += 32) chunk(t0, ra);
+        } else {
+#pragma unroll 1
+            for (int t0 = 16 * part; t0 < it.rows; t0 += 64) {
+                chunk(t0, ra);
+                if constexpr (SCALED) {
+                    if (t0 + 32 < it.rows) chunk(t0 + 32, ra);
+                } else {
+                    if (t0 + 32 < it.rows) chunk(t0 + 32, rb);
+                }
             }
         }
         if (16 * part >= it.rows) done_reading();  // a tile of at most 16 rows has no chunk for the other half
