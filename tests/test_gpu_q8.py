@@ -155,7 +155,9 @@ def test_quantize_writes_only_its_rows():
 LINEAR = [(1, 1, 16), (1, 2048, 2048), (2, 7, 32), (7, 17, 80), (8, 768, 2048), (9, 256, 144), (16, 100, 1040),
           (17, 33, 64), (31, 64, 48), (32, 130, 528), (33, 257, 2032), (64, 16, 128), (65, 511, 208), (127, 129, 192),
           (128, 128, 64), (129, 384, 320), (200, 1000, 1104), (256, 256, 256), (257, 256, 272), (317, 520, 2032),
-          (513, 1031, 784), (1000, 40, 4096), (1024, 768, 768), (70, 300, 8192)]
+          (513, 1031, 784), (1000, 40, 4096), (1024, 768, 768), (70, 300, 8192),
+          # a handful of rows of more than 1024 inputs; many row tiles of each length
+          (2, 2048, 2048), (3, 33, 1040), (4, 130, 4112), (4, 8, 20000), (5, 100, 2064), (4096, 1030, 144), (2500, 2000, 80)]
 
 
 @pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
@@ -271,7 +273,35 @@ def test_grouped(counts, gated):
         at += c
 
 
-@pytest.mark.parametrize("rows", [40, 300])
+# a handful of rows per expert: runs of one, two and four of them, short and long rows of inputs
+FEW = [[1], [1] * 8, [2, 2, 1, 3], [0, 5, 0, 0, 1, 0, 0, 0, 2], [4] * 3 + [0] * 300, [1] * 128, [2] * 64, [9] + [1] * 40, [64] + [0] * 63,
+       [0] * 500 + [3, 1], [1, 0] * 512]
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("K", [16, 528, 1024, 1040, 2048, 4112])
+@pytest.mark.parametrize("counts", FEW, ids=lambda c: f"{len(c)}x{sum(c)}")
+def test_grouped_few_rows(counts, K, gated):
+    i = FEW.index(counts) + K // 16
+    g = gen(i)
+    E, rows, N = len(counts), sum(counts), (40, 37, 8)[i % 3]
+    t = weights(g, (E,), N, K, BF16, gated, i % 2 == 0)
+    x = rows_of(g, rows, K)
+    token = torch.randperm(rows, generator=g, device="cuda").to(torch.int32) if i % 3 else None
+    out = normal(g, (rows + 2, N))
+    before = out.clone()
+    q.moe_grouped_linear_q8(q.QuantizedRows(*x), q.LinearWeightsQ8(**t, activation="silu" if gated else "none"), offsets_of(counts),
+                            row_token=token, out=out[:rows])
+    assert torch.equal(out[rows:], before[rows:])
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            xs = [v[token[at:at + c].long()] if token is not None else v[at:at + c] for v in x]
+            ref.check(out[at:at + c], *ref8.product(*xs, act="silu" if gated else "none", **{k: v[e] for k, v in t.items()}))
+        at += c
+
+
+@pytest.mark.parametrize("rows", [5, 40, 300])
 def test_grouped_reads_and_writes_nothing_out_of_range(rows):
     """Offsets and tokens that mean nothing: what is outside the buffers' rows is not touched."""
     g = gen(rows)

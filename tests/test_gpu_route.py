@@ -21,7 +21,8 @@ def logits(seed, n, E, dtype=F32, std=1.5):
 
 
 def both(z, k, **rule):
-    """The call with and without the torch_calls module, and captured, against the reference."""
+    """The call against the reference, with and without the torch_calls module, and with the
+    rows many times over (from 4096 on, eight lanes take a row instead of a warp)."""
     router = q.Router(z.shape[1], k, **rule)
     r = q.moe_route(z, router)
     ref.check(r, z, k, **rule)
@@ -31,6 +32,14 @@ def both(z, k, **rule):
     finally:
         q.ops._calls = keep
     assert torch.equal(r.topk_idx, again.topk_idx) and torch.equal(r.topk_w, again.topk_w)
+    n = z.shape[0]
+    if n <= 64:
+        times = 4100 // n + 1
+        many = q.moe_route(z.repeat(times, 1), router)
+        ids, w = many.topk_idx.view(times, n, k), many.topk_w.view(times, n, k)
+        assert bool((ids == r.topk_idx).all())
+        assert torch.equal(w.view(torch.int32), w[:1].expand_as(w).contiguous().view(torch.int32))
+        ref.check(q.Routing(ids[0], w[0]), z, k, **rule)
     return r
 
 
@@ -97,11 +106,27 @@ def test_scores_next_to_each_other_are_told_apart():
         both(z.cuda(), 9, score=score, bias=torch.full((E,), 0.5).cuda(), groups=16, top_groups=5, group_score="top2")
 
 
-def test_many_rows_with_a_bias():
-    """Enough rows that some are ranked again."""
-    z, b = logits(77, 3000, 256, BF16)
+@pytest.mark.parametrize("n", [3000, 5001])
+def test_many_rows_with_a_bias(n):
+    """Enough rows that some are ranked again; a warp or eight lanes a row."""
+    z, b = logits(77, n, 256, BF16)
     both(z, 8, score="sigmoid", bias=b, groups=8, top_groups=4, group_score="top2")
-    both(z, 6, score="softmax", bias=0.01 * b, scale=2.5)
+    both(z[:, :200], 6, score="softmax", bias=0.01 * b[:200].contiguous(), scale=2.5)
+    both(z[:, :60].float(), 9, score="sigmoid", groups=4, top_groups=2, group_score="top2")
+
+
+def test_close_rows_side_by_side():
+    """Rows that are ranked again next to rows that are not, in every place of a warp, with more
+    ranks than lanes have a row: all lanes vote, whatever their row has found."""
+    g = torch.Generator().manual_seed(8)
+    E = 250
+    z, b = logits(78, 4500, E)
+    close = torch.rand(4500, generator=g) < 0.3
+    z[close.cuda()] = (17 + 2 * torch.rand((int(close.sum()), E), generator=g)).cuda()
+    b = (torch.randint(0, 2, (E,), generator=g) * 2.0 ** -24).cuda()
+    for k in (3, 8, 20):
+        both(z, k, score="sigmoid", bias=b)
+        both(z, k, score="sigmoid", bias=b, groups=5, top_groups=2, group_score="top2")
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -183,7 +208,7 @@ def test_strides_and_alignment(E, dtype):
 def test_no_rows_and_many_rows():
     r = q.moe_route(torch.zeros(0, 16, device="cuda"), q.Router(16, 4))
     assert r.topk_idx.shape == (0, 4) and r.topk_w.shape == (0, 4)
-    n = 70000
+    n = 70001
     z = torch.randn(n, 8, device="cuda")
     r = q.moe_route(z, q.Router(8, 2))
     top = torch.topk(z, 2)
