@@ -426,14 +426,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; v < end; v += kGroups) {
                 const uint32_t u = v % kUnits, stage = slot * stage_bytes;
                 if (!(ok = __all_sync(0xffffffffu, wait(full_addr + 8 * slot, phase, abort_flag)))) break;
-                uint4 w[MATS][4], x[4];
+                constexpr int kX = MATS == 2 ? 2 : 4;  // atoms of a warp, at most
+                uint4 w[MATS][4], x[kX];
                 auto load = [&](uint32_t turn) {
 #pragma unroll
                     for (int m = 0; m < MATS; ++m)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ turn);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < kX; ++j)
                         if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ turn);
                 };
                 auto store = [&](uint32_t place) {
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::st_32x32b_x16_async(a + m * (kK / 2) + 8 * j, f16);
                         }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < kX; ++j) {
                         if (4 * j >= atoms) break;
                         const uint2 f0 = codes_to_f16(x[j].x), f1 = codes_to_f16(x[j].y), f2 = codes_to_f16(x[j].z),
                                     f3 = codes_to_f16(x[j].w);

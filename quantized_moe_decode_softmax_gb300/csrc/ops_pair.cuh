@@ -358,14 +358,15 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
         // a residual is read two chunks ahead, the first two before the tile is done (SCALED,
         // where more warps share the registers: one); the values stay as loaded until they
         // are used, so that nothing waits for them earlier
-        uint32_t ra[W], rb[SCALED ? 1 : W];
-        auto load_res = [&](uint32_t (&d)[W], int t0) {
+        constexpr int kHeld = SCALED && MATS == 2 ? W / 2 : W;  // (half: unpaired values are read when they are used)
+        uint32_t ra[kHeld], rb[SCALED ? 1 : W];
+        auto load_res = [&](uint32_t (&d)[kHeld], int t0) {
             const char *s = res + 2 * (size_t)t0 * p.ldr;
             if (g.paired) {
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j, s += rstep)
                     if (t0 + 2 * j + odd < rows) d[j] = *reinterpret_cast<const uint32_t *>(s);
-            } else {
+            } else if constexpr (kHeld == W) {
 #pragma unroll
                 for (int j = 0; j < W; ++j, s += rstep)
                     if (t0 + j < rows) d[j] = *reinterpret_cast<const uint16_t *>(s);
@@ -384,7 +385,7 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             tc::fence_before_sync();
             if (lane == 0) arrive_cluster(in_first(acc_empty_addr + 8 * buf));
         };
-        auto chunk = [&](int t0, uint32_t (&r)[W]) {
+        auto chunk = [&](int t0, uint32_t (&r)[kHeld]) {
             float v[W], u[MATS == 2 ? W : 1];
             tmem_ld16(acc + t0, v);
             if constexpr (MATS == 2) tmem_ld16(acc + g.tcap + t0, u);
@@ -427,8 +428,17 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             if (res) {  // (unset past the end of the tile, where nothing is stored)
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j) {
-                    const uint32_t two = g.paired ? __byte_perm(r[j], __shfl_xor_sync(0xffffffffu, r[j], 1), trade)
-                                                  : __byte_perm(r[2 * j], r[2 * j + 1], 0x5410u);
+                    uint32_t two;
+                    if (g.paired) {
+                        two = __byte_perm(r[j], __shfl_xor_sync(0xffffffffu, r[j], 1), trade);
+                    } else if constexpr (kHeld < W) {
+                        const char *s = res + (size_t)(t0 + 2 * j) * rstep;
+                        const uint32_t lo = t0 + 2 * j < rows ? *reinterpret_cast<const uint16_t *>(s) : 0u;
+                        const uint32_t hi = t0 + 2 * j + 1 < rows ? *reinterpret_cast<const uint16_t *>(s + rstep) : 0u;
+                        two = lo | hi << 16;
+                    } else {
+                        two = __byte_perm(r[2 * j], r[2 * j + 1], 0x5410u);
+                    }
                     const float2 f = unpack2<T>(two);
                     v[2 * j] += f.x;
                     v[2 * j + 1] += f.y;
