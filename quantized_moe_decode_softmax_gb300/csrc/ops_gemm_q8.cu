@@ -103,19 +103,19 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d, uint32_t a, uint32_t b, 
 }
 
 // The groups in shared memory: their first item, first row, rows, and tiles x 32 + rows of a tile
-// / 16. (For one group without offsets: entry 0.)
+// / 16.
 struct Group {
     int first, lo, rows, tiles;
 };
 
 // Fill the table, by the block; the number of all items. warp_sum: kThreads / 32 numbers.
 __device__ __forceinline__ int number_groups(const Product &p, const Tiles &g, Group *table, int *warp_sum) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = p.offsets ? p.E : 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int base = 0;
-    for (int e0 = 0; e0 < E; e0 += kThreads) {
+    for (int e0 = 0; e0 < p.E; e0 += kThreads) {
         const int e = e0 + tid;
         int items = 0, lo = 0, hi = 0, t = kStepRows, nt = 0;
-        if (e < E) {
+        if (e < p.E) {
             group_rows(p, e, lo, hi);
             if (hi > lo) {
                 t = tile_rows(hi - lo, g.tcap);
@@ -137,25 +137,27 @@ __device__ __forceinline__ int number_groups(const Product &p, const Tiles &g, G
             if (w < warp) before += warp_sum[w];
             sum += warp_sum[w];
         }
-        if (e < E) table[e] = Group{before + scan - items, lo, hi - lo, nt * 32 + t / 16};
+        if (e < p.E) table[e] = Group{before + scan - items, lo, hi - lo, nt * 32 + t / 16};
         base += sum;
         __syncthreads();
     }
     return base;
 }
 
-// Item i of all (i < total), by a whole warp: two rounds of 32 comparisons find its group.
-__device__ __forceinline__ Item find_item(const Group *table, int E, int mblocks, int i) {
+// Item i of all (i < total), by a whole warp: two rounds of 32 comparisons find its group. one:
+// the only group, without offsets.
+__device__ __forceinline__ Item find_item(const Product &p, const Group *table, const Group &one, int mblocks, int i) {
     const int lane = threadIdx.x & 31;
     int e = 0;
-    if (E > 1) {
-        const int step = (E + 31) >> 5;  // <= 32
+    Group g = one;
+    if (p.offsets) {
+        const int step = (p.E + 31) >> 5;  // <= 32
         const int c = lane * step;
-        e = (__popc(__ballot_sync(0xffffffffu, c < E && table[c].first <= i)) - 1) * step;
+        e = (__popc(__ballot_sync(0xffffffffu, c < p.E && table[c].first <= i)) - 1) * step;
         const int f = e + lane;
-        e += __popc(__ballot_sync(0xffffffffu, lane < step && f < E && table[f].first <= i)) - 1;
+        e += __popc(__ballot_sync(0xffffffffu, lane < step && f < p.E && table[f].first <= i)) - 1;
+        g = table[e];
     }
-    const Group g = table[e];
     const int nt = max(g.tiles >> 5, 1), T = (g.tiles & 31) * 16;
     i -= g.first;
     // bands of kBand row tiles: the tiles of a band run side by side on one weight block, then
@@ -243,11 +245,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MATS == 2) ptx::prefetch_tensormap(&tmu);
     }
     if (warp == kMmaWarp) tmem_alloc_pair(&tslot, kTmemCols);
-    ptx::griddep_wait();
-    const int total = number_groups(p, g, table, warp_sum);
     tc::fence_before_sync();
-    __syncthreads();
-    cluster_sync();  // the peer's barriers are ready
+    cluster_arrive();
+    Group one{0, 0, p.rows, 0};
+    int total = 0;
+    if (!p.offsets) {
+        const int t = tile_rows(p.rows, g.tcap), nt = (p.rows + t - 1) / t;
+        one.tiles = nt * 32 + t / 16;
+        total = nt * g.mblocks;
+    }
+    ptx::griddep_wait();
+    if (p.offsets) total = number_groups(p, g, table, warp_sum);
+    cluster_wait();  // both CTAs' barriers are ready
     tc::fence_after_sync();
     const uint32_t tmem = tslot;
     const uint32_t ring_addr = tc::smem_u32(ring), full_addr = tc::smem_u32(full), empty_addr = tc::smem_u32(empty);
@@ -300,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = item0; ok; i += item_step, ++n) {
             if (w) {
                 const bool more = i < total;
-                if (more) it = find_item(table, p.offsets ? p.E : 1, g.mblocks, i);
+                if (more) it = find_item(p, table, one, g.mblocks, i);
                 const uint32_t slot = n % kItems;
                 if (!(ok = __all_sync(0xffffffffu, wait(items.empty + 8 * slot, ((n / kItems) & 1) ^ 1, abort_flag)))) break;
                 if (lane == 0) {
@@ -353,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         const uint32_t base = tc::idesc_f16_f32(kPair * kM, 0);
         const int units = nh / kHalves;  // of a tile
-        for (int n = 0; ok && items.next(it); ++n) {
+        int n = 0;
+        for (; ok && items.next(it); ++n) {
             if (tc::elect_one()) {
                 const uint32_t idesc = base | ((uint32_t)(it.T >> 3) << 17);
                 const int buf = g.bufs == 2 ? n & 1 : 0, use = g.bufs == 2 ? n >> 1 : n;
@@ -391,6 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, *abort_flag) && tc::elect_one()) {
             commit_pair(tc::smem_u32(&drain));
             settle(tc::smem_u32(&drain), 0, globaltimer());
+        }
+        // the other CTA's arrivals on the accumulator sets are here before this one may end
+        const unsigned long long t0 = globaltimer();
+        for (int b = 0; b < g.bufs; ++b) {
+            const int uses = (n + g.bufs - 1 - b) / g.bufs;
+            if (uses > 0) settle(acc_empty_addr + 8 * b, (uint32_t)(uses - 1) & 1, t0);
         }
         __syncwarp();
     } else if (warp < kConvert) {
@@ -498,9 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         store_tiles<T, MATS, true>(p, g, items, rank, tmem, warp - kConvert, acc_full_addr, acc_empty_addr, abort_flag,
                                    row_scale[warp - kConvert]);
     }
+    // Neither CTA ends while the other may still use its memory. (Relaxed: all arrivals that cross
+    // have been waited for, unless a wait gave up. A release would wait for the last stores to reach
+    // L2.)
     tc::fence_before_sync();
-    __syncthreads();
-    cluster_sync();  // neither CTA ends while the other may still use its memory
+    if (*abort_flag) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    cluster_wait();
     tc::fence_after_sync();
     if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
@@ -634,7 +655,7 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     g.mblocks = mblocks;
     auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
     g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
-    const int table = (p.offsets ? p.E : 1) * (int)sizeof(Group);
+    const int table = p.offsets ? p.E * (int)sizeof(Group) : 0;
     const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - halves * g.half_bytes;
     g.stages = min(kMaxStages, budget / g.stage_bytes);
     if (g.stages < (wide ? 7 : 4)) return cudaErrorNotSupported;  // (see the converters)
