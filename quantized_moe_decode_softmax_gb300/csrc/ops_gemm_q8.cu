@@ -557,10 +557,9 @@ Device g_devices[kMaxDevices];
 constexpr int half_cols(int mats) { return mats * kK / 2; }
 constexpr int max_rows(int mats) { return mats == 2 ? 128 : 256; }
 static_assert(max_rows(1) + kUnits * half_cols(1) <= kTmemCols && 2 * max_rows(2) + kUnits * half_cols(2) <= kTmemCols, "they fit");
-constexpr bool wide_units(int mats, int rows) { return mats == 1 && rows <= 96; }  // (7 load stages fit up to there)
-constexpr int halves_of(int mats, int rows) { return kUnits * (wide_units(mats, rows) ? 2 : 1); }
+constexpr bool wide_units(int mats, int rows) { return mats == 1 && rows <= 96; }  // (7 load stages fit up to there, but beside some 260 groups and more)
 constexpr int sets_of(int mats, int rows) {
-    return 2 * mats * rows + halves_of(mats, rows) * half_cols(mats) <= kTmemCols ? 2 : 1;
+    return 2 * mats * rows + kUnits * (wide_units(mats, rows) ? 2 : 1) * half_cols(mats) <= kTmemCols ? 2 : 1;
 }
 
 // Rows per tile: the least time of a simple model, in cycles, as in ops_gemm.cu. Waves of tiles
@@ -646,9 +645,6 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
     Tiling g;
     g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all);
-    const bool wide = wide_units(mats, g.tcap);
-    const int halves = halves_of(mats, g.tcap);
-    g.a_col = kTmemCols - halves * half_cols(mats);
     g.bufs = sets_of(mats, g.tcap);
     g.stage_bytes = mats * kTileW + box_rows(g.tcap / kPair) * kIn;
     g.half_bytes = g.tcap / kPair * kK * 2;
@@ -656,9 +652,17 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
     g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
     const int table = p.offsets ? p.E * (int)sizeof(Group) : 0;
-    const int budget = d.smem.load(std::memory_order_relaxed) - 1024 - table - halves * g.half_bytes;
-    g.stages = min(kMaxStages, budget / g.stage_bytes);
-    if (g.stages < (wide ? 7 : 4)) return cudaErrorNotSupported;  // (see the converters)
+    const int room = d.smem.load(std::memory_order_relaxed) - 1024 - table;
+    // (whole stages for units may not fit beside the table of many groups. 256 tokens, 8 of 1024 experts,
+    // 768 -> 2048: 268 us with half stages, 993 in the kernel for few rows.)
+    int wide = wide_units(mats, g.tcap), halves;
+    for (;; --wide) {
+        halves = wide ? 2 * kUnits : kUnits;
+        g.stages = min(kMaxStages, (room - halves * g.half_bytes) / g.stage_bytes);
+        if (g.stages >= (wide ? 7 : 4)) break;  // (see the converters)
+        if (!wide) return cudaErrorNotSupported;
+    }
+    g.a_col = kTmemCols - halves * half_cols(mats);
     const int smem = 1024 + g.stages * g.stage_bytes + halves * g.half_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     // items are numbered in 32 bits, also where offsets that do not ascend give every

@@ -60,6 +60,21 @@ def test_1024_experts(rows):
         ref.check(out[r:r + 1], *ref8.product(x.codes[r:r + 1], x.scale[r:r + 1], act="gelu", **{k: v[at] for k, v in t.items()}))
 
 
+@pytest.mark.parametrize("E,mean", [(300, 80), (1024, 90), (1024, 60), (1000, 200)])
+def test_many_experts_and_rows(E, mean):
+    """The table of the groups next to tiles of each length."""
+    g = gen(E + mean)
+    N, K, rows = 136, 272, E * mean
+    t = weights(g, (E,), N, K, BF16, False, True)
+    x = rows_of(g, rows, K)
+    e = torch.randint(0, E, (rows,), generator=g, device="cuda").sort().values
+    out = q.moe_grouped_linear_q8(x, q.LinearWeightsQ8(**t), offsets_of(torch.bincount(e, minlength=E).tolist()))
+    for r in list(range(0, rows, rows // 60)) + [rows - 1]:
+        at = int(e[r])
+        ref.check(out[r:r + 1], *ref8.product(x.codes[r:r + 1], x.scale[r:r + 1], **{k: v[at] for k, v in t.items()}))
+    q.moe_ops_check()
+
+
 @pytest.mark.parametrize("rows", [3, 100, 1000])
 def test_weights_and_rows_past_32_bits(rows):
     """Experts that begin more than 2^32 bytes into the weights, rows of x and of out that lie far
