@@ -125,25 +125,45 @@ moe_status run(const Product &a, cudaStream_t st) {
     return of(launch_product_rows(a, st));
 }
 
-// The same for 8-bit codes, with a third way for a handful of rows: dot products
-// (ops_dot_q8.cu), f16 on mma.sync (ops_rows_q8.cu), f16 on tcgen05 (ops_gemm_q8.cu). Measured
-// (us, dot / mma.sync / tcgen05):
-//   2048x2048              1 row  3.1 / 3.5 / 12      4 rows  3.5 / 3.5 / 12     64 rows  20 / 8.7 / 11
-//   8192x4096              1 row  7.5 / 9.3 / 19      4 rows  8.3 / 9.1 / 19     24 rows  26 / 19.1 / 19.3
-//   4096x4096             32 rows  22 / 10.2 / 18.7  48 rows  31 / 17.2 / 15.7
-//   2048x4096 gated       64 rows  45 / 19.7 / 23
-//   768x2048 gated, 128 experts, top 8   1 token 6.6 / 9.5 / 18    16 tokens 46 / 60 / 55   32 tokens 114 / 95 / 66
-//   the same, all on the same experts                              16 tokens 24 / 17 / 18
-//   512x1024 gated, 8 experts, top 2     8 tokens 4.0 / 4.4 / 12   32 tokens 7.2 / 6.3 / 12
+// The same for 8-bit codes, with a third way for few rows: dot products (ops_dot_q8.cu), f16 on
+// mma.sync (ops_rows_q8.cu), f16 on tcgen05 (ops_gemm_q8.cu). Measured (us, dot / mma.sync /
+// tcgen05):
+//   2048x2048              1 row  3.1 / 3.5 / 9.5     8 rows  3.7 / 3.5 / 9.5    64 rows  10.6 / 8.7 / 9.6
+//   8192x4096              1 row  7.5 / 9.3 / 14.7   16 rows  18 / 12 / 14.4     24 rows  24 / 19.2 / 14.5
+//   4096x4096             32 rows  16 / 10.1 / 13.8  48 rows  22 / 17.1 / 14.3
+//   512x4096              32 rows  4.8 / 7.0 / 13.4  64 rows  5.5 / 11.9 / 13.8
+//   1024x2048             64 rows  6.6 / 8.1 / 9.2  128 rows  10.5 / 14.5 / 9.5
+//   2048x4096 gated       16 rows  10.7 / 8.3 / 20.5 64 rows  28 / 19.7 / 20.9
+//   512x4096 gated        32 rows  5.5 / 11.6 / 20.5
+//   768x2048 gated, 128 experts, top 8   1 token 6.6 / 9.5 / 16    16 tokens 47 / 63 / 53   32 tokens 82 / 78 / 65
+//   the same, all on the same experts                              16 tokens 24 / 17 / 16
+//   512x1024 gated, 8 experts, top 2     8 tokens 4.1 / 4.4 / 10   32 tokens 7.0 / 6.2 / 10.6
+// Of a linear product the three are weighed by their times (us) as fitted to such figures: dot by
+// bytes, bytes times rows in fours, and outputs; mma.sync by its walk along K, for more than 16
+// rows in passes of 32 and rounds of 304 blocks of 16 columns; tcgen05 by its walk along K or the
+// bytes. Of 900 calls drawn at random (40..12288 columns, 128..8192 inputs, 1..256 rows) the choice
+// was more than 10 % slower than the best in 24, at most 24 %.
 enum class Q8 { dot, rows, gemm };
 Q8 kernel_q8(const Product &a) {
-    const int groups = a.offsets ? min(a.E, a.rows) : 1;
+    const int groups = a.offsets ? min(a.E, a.rows) : 1, mats = a.w_up ? 2 : 1;
     const int mean = (a.rows + groups - 1) / groups;
-    const double mb = 1e-6 * groups * a.N * (double)a.K * (a.w_up ? 2 : 1);
-    const double work = mb * ((mean + 7) / 8);  // rows cost in blocks of 8
-    if (a.offsets) return a.rows <= 128 && mean <= 2 ? Q8::dot : a.rows <= 64 && work <= 60.0 ? Q8::rows : Q8::gemm;
-    if (a.rows == 1 || (a.rows <= 4 && a.K > 1024)) return Q8::dot;
-    return a.rows <= 64 && work <= (a.w_up ? 150.0 : 90.0) ? Q8::rows : Q8::gemm;
+    const double mb = 1e-6 * groups * a.N * (double)a.K * mats;
+    if (a.offsets) {
+        const double work = mb * ((mean + 7) / 8);  // rows cost in blocks of 8
+        return a.rows <= 128 && mean <= 2 ? Q8::dot : a.rows <= 64 && work <= 60.0 ? Q8::rows : Q8::gemm;
+    }
+    const int n = a.rows;
+    if (n > 256) return Q8::gemm;
+    const double k = a.K / 1024.0;
+    const int fours = n == 1 ? 1 : (n + 3) / 4 * 4, blocks = (a.N + 15) / 16;
+    const double dot = 1.8 + mb * (0.1 + 0.0215 * fours) + 3e-5 * a.N * mats * fours;
+    const double per_k = n <= 8 ? (mats == 2 ? 1.05 : 0.48) : n <= 16 ? (mats == 2 ? 1.5 : 0.66)
+                         : blocks <= 152 ? (mats == 2 ? 2.3 : 1.33) : (mats == 2 ? 2.9 : 1.9);
+    const double rows = n <= 16 ? 1.4 + max(1.0, a.N / 2048.0) * ((mats == 2 ? 0.6 : 0.45) + k * per_k)
+                                : 1.2 + (n + 31) / 32 * ((blocks + 303) / 304) * ((mats == 2 ? 2.2 : 1.3) + k * per_k);
+    const double gemm = max(mats == 2 ? 5.6 + 3.7 * k : 4.4 + 2.15 * k, 4.0 + 0.25 * mb);
+    if (dot < gemm && (n > 64 || dot < rows)) return Q8::dot;
+    return n <= 64 && rows < gemm ? Q8::rows : Q8::gemm;
 }
 
 moe_status run_q8(const Product &a, cudaStream_t st) {

@@ -46,6 +46,29 @@ def test_100000_rows():
     q.moe_ops_check()
 
 
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("n,N,K", [(250, 40, 4096), (256, 128, 2048), (129, 70, 528), (65, 200, 1040), (33, 500, 2064), (18, 1000, 4112),
+                                   (100, 33, 16), (64, 256, 8192), (40, 1100, 2048)])
+def test_narrow_layers(n, N, K, gated):
+    """Many rows by few columns: the kernels for few rows take them too."""
+    g = gen(n)
+    t = weights(g, (), N, K, BF16, gated, n % 2 == 0)
+    x, res = rows_of(g, n, K), normal(g, (n, N))
+    out = q.moe_linear_q8(x, q.LinearWeightsQ8(**t, activation="gelu_tanh"), residual=res)
+    ref.check(out, *ref8.product(*x, act="gelu_tanh", residual=res, **t))
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("n,N,K", [(7, 3000, 1040), (8, 2048, 784), (12, 4100, 528), (16, 2050, 2064), (17, 2056, 16), (20, 2048, 2048),
+                                   (31, 2500, 1104), (40, 2064, 1040), (64, 2051, 2064), (24, 8200, 272), (64, 12290, 144)])
+def test_wide_layers(n, N, K, gated):
+    g = gen(n + N)
+    t = weights(g, (), N, K, BF16, gated, n % 2 == 0)
+    x, res = rows_of(g, n, K), normal(g, (n, N))
+    out = q.moe_linear_q8(x, q.LinearWeightsQ8(**t, activation="silu"), residual=res)
+    ref.check(out, *ref8.product(*x, act="silu", residual=res, **t))
+
+
 @pytest.mark.parametrize("rows", [60, 1500, 20000])
 def test_1024_experts(rows):
     g = gen(rows)
