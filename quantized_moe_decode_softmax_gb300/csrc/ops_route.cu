@@ -7,19 +7,19 @@
 //
 // Bound: latency for a few rows, the issue of instructions for many (a row is E logits, a few
 // hundred bytes). L lanes take a row: all 32 of a warp, so that a row is done soon, or 8 where
-// there are rows enough to fill the SMs, so that an instruction serves four rows
-// (8192 x 256, top 6: 5.5 us, with a bias 10.7; a warp each 9.1 and 14). Lane i holds the V experts V i .. V i + V - 1, which makes the lowest
-// lane of a tie the lowest id. A key is its f32 as an unsigned number that sorts alike
-// (0: not available). The keys lie in shared memory and each lane keeps the largest of its
-// own, so that a rank is one maximum over the lanes, and another over the V keys of the lane
-// that had it, which the lanes read side by side.
+// there are rows enough to fill the SMs, so that an instruction serves four rows (8192 x 256,
+// top 6: 5.5 us, with a bias 8.9; a warp each 9.1 and 14). Lane i holds the V experts V i ..
+// V i + V - 1, which makes the lowest lane of a tie the lowest id. A key is its f32 as an
+// unsigned number that sorts alike (0: not available). The keys lie in shared memory and each
+// lane keeps the largest of its own, so that a rank is one maximum over the lanes, and another
+// over the V keys of the lane that had it, which the lanes read side by side.
 //
 // The ids are those of exact scores. Without a bias the order of c is the order of the
 // logits, and no score is computed for it. With a bias (or with sums of two per group)
 // c is computed in f32, the ranks are taken to top_k + 1 places, and wherever two
 // neighbours are nearer to each other than the f32 errors (below), the row is ranked
-// again in f64, over the experts that can still be among the first. For trained
-// routers that is one row in some thousands.
+// again, over the experts that can still be among the first: in pairs of f32 or in f64. For
+// trained routers that is one row in some thousands.
 #include "ops_common.cuh"
 #include "ptx.cuh"
 
@@ -33,8 +33,10 @@ constexpr int kManyRows = 4096;  // rows from which on eight lanes take one
 
 // Error of an f32 score of a key (at most 1). Sigmoid: the argument's rounding moves the result
 // by at most |l| s (1 - s) 2^-24 < 2^-26, exp2 and the reciprocal are good to 2^-22, 1 + e rounds
-// to 2^-24: together below 2^-21. A softmax also rounds l - max and its product with log2(e) (error times score at
-// most 2^-24) and sums up to 32 terms in a lane and 5 across, 37 roundings of 2^-24.
+// to 2^-24: together below 2^-21. A softmax also rounds l - max and its product with log2(e)
+// (error times score at most 2^-24) and sums up to 32 terms in a lane and 5 across, 37
+// roundings of 2^-24. Of a score p that is less than 2^-18 p + 2^-23 p log(1 / p), and the second
+// term below 2^-23 sqrt(p).
 constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-18f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -232,20 +234,98 @@ __device__ __noinline__ unsigned groups_exactly(const RouteArgs &a, long long ro
     return best_groups<32, double>(a, key, max_logit, !a.bias, &gap, &worst, nullptr);
 }
 
-// The ranks of one row again in f64, by a whole warp. Only the experts that `ranks` has (`ranked` of
+// A number as the sum of two f32, the second at most half a last place of the first
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two sum_of(float a, float b) {  // exact (Knuth)
+    const float s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two quick_sum_of(float a, float b) {  // exact for |a| >= |b| (Dekker)
+    const float s = a + b;
+    return {s, b - (s - a)};
+}
+// a b + c. (__fmul_rn: a product that is a term of a sum as well, and must not become part of an fma)
+__device__ __forceinline__ Two times_plus(Two a, Two b, float c_hi, float c_lo) {
+    const float p = __fmul_rn(a.hi, b.hi), e = fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi);
+    const Two s = sum_of(c_hi, p);
+    return quick_sum_of(s.hi, s.lo + (e + c_lo));
+}
+// 1 / (1 + exp(-l)) to 2^-45 (the largest of 2^28 errors: 2^-45.8). exp(-|l|) = 2^k exp(r): r is
+// x - k ln 2, with ln 2 in three parts of which k times the first is exact, and exp(r) its
+// Taylor series to r^11, from r^6 / 720 on (the last term first) in two parts.
+__device__ __forceinline__ Two sigmoid_two(float l) {
+    const float x = -fabsf(l);
+    Two t = {0.f, 0.f};
+    if (x > -87.f) {
+        const float k = rintf(x * kLog2e);
+        constexpr float ln2_1 = 0x1.62e4p-1f, ln2_2 = 0x1.7f7d1cp-20f, ln2_3 = 0x1.ef357ap-45f;
+        const float a = fmaf(-k, ln2_1, x), p = __fmul_rn(k, ln2_2), e = fmaf(k, ln2_2, -p);
+        Two r = sum_of(a, -p);
+        r = quick_sum_of(r.hi, r.lo - fmaf(k, ln2_3, e));
+        float q = 1.f / 39916800.f;
+        q = fmaf(q, r.hi, 1.f / 3628800.f);
+        q = fmaf(q, r.hi, 1.f / 362880.f);
+        q = fmaf(q, r.hi, 1.f / 40320.f);
+        q = fmaf(q, r.hi, 1.f / 5040.f);
+        t = {q, 0.f};
+        t = times_plus(t, r, 0x1.6c16c2p-10f, -0x1.27d27ep-35f);  // 1 / 720
+        t = times_plus(t, r, 0x1.111112p-7f, -0x1.dddddep-32f);   // 1 / 120
+        t = times_plus(t, r, 0x1.555556p-5f, -0x1.555556p-30f);   // 1 / 24
+        t = times_plus(t, r, 0x1.555556p-3f, -0x1.555556p-28f);   // 1 / 6
+        t = times_plus(t, r, 0.5f, 0.f);
+        t = times_plus(t, r, 1.f, 0.f);
+        t = times_plus(t, r, 1.f, 0.f);
+        const float two_k = __int_as_float(((int)k + 127) << 23);
+        t = {__fmul_rn(t.hi, two_k), t.lo * two_k};
+    }
+    const Two n = l >= 0.f ? Two{1.f, 0.f} : t;
+    Two d = quick_sum_of(1.f, t.hi);
+    d.lo += t.lo;
+    const float q = n.hi / d.hi, p = __fmul_rn(q, d.hi);
+    const float rest = ((n.hi - p) - fmaf(q, d.hi, -p)) + (n.lo - q * d.lo);
+    return quick_sum_of(q, rest / d.hi);
+}
+
+// The ranks of one row again, exactly, by a whole warp. Only the experts that `ranks` has (`ranked` of
 // them), and others that are left with a key of at least `from`, can be among the first. key: E
 // doubles; list: the row's keys, which are lost.
 template <int V>
 __device__ __noinline__ void rank_exactly(const RouteArgs &a, long long row, float from, float max_logit, int *ranks,
                                           int ranked, double *key, uint32_t *list) {
     const int lane = threadIdx.x & 31;
-    const double none = -INFINITY, sum = exact_sum(a, row, max_logit);
     int found = pick_experts<V>(a, list, [&](int) { return from; });
     for (int r = lane; r < ranked; r += 32) list[found + r] = (uint32_t)ranks[r];  // (these have no key any more)
     found += ranked;
     __syncwarp();
+    if (found <= 32 && a.score == MOE_SCORE_SIGMOID) {
+        // One each: a rank is the number of lanes that come before. In pairs of f32, which are enough
+        // for all but one row in millions: c is off by less than 2^-45 + 2^-48 |c|. (8192 x 256: 9.8 us,
+        // 10.5 with the f64 exponential and division, which all other rows wait for.)
+        const int e = lane < found ? (int)list[lane] : 0x7fffffff;
+        const float l = lane < found ? logit(a, row, e) : 0.f, b = lane < found ? a.bias[e] : 0.f;
+        Two c = sigmoid_two(l);
+        const Two s = sum_of(c.hi, b);
+        c = {s.hi, s.lo + c.lo};
+        int rank = 0;
+        bool open = false;
+        for (int i = 0; i < found; ++i) {
+            const float by = (__shfl_sync(kAll, c.hi, i) - c.hi) + (__shfl_sync(kAll, c.lo, i) - c.lo);
+            const float ol = __shfl_sync(kAll, l, i), ob = __shfl_sync(kAll, b, i);
+            const int oe = __shfl_sync(kAll, e, i);
+            const bool same = ol == l && ob == b;  // an exact tie
+            open |= lane < found && !same && !(fabsf(by) > 0x1p-42f * (1.f + fabsf(c.hi)));
+            rank += same ? oe < e : by > 0.f;
+        }
+        if (!__any_sync(kAll, open)) {
+            if (lane < found) ranks[rank] = e;
+            __syncwarp();
+            return;
+        }
+    }
+    const double none = -INFINITY, sum = exact_sum(a, row, max_logit);
     if (found <= 32) {
-        // one each: a rank is the number of lanes that come before
         const int e = lane < found ? (int)list[lane] : 0x7fffffff;
         const double c = lane < found ? exact_key(a, row, e, max_logit, sum) : none;
         int rank = 0;
@@ -302,8 +382,9 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     const long long row = first_row + lane / L;
     const bool live = row < a.n;
     ptx::griddep_wait();
-    if (first_row >= a.n) return;
-    uint32_t *own = words + (size_t)warp * a.words;
+    constexpr bool kShared = L < 32;  // the biases by way of shared memory (see the launch)
+    float *biases = reinterpret_cast<float *>(words);
+    uint32_t *own = words + (kShared && a.bias ? L * (V + 4) : 0) + (size_t)warp * a.words;
     uint32_t *mine = own + lane / L * row_words(L, V);
     const Keys<V> keys{mine};
     int *ranks = reinterpret_cast<int *>(mine + L * (V + 4));
@@ -360,6 +441,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) l[j] = live && e0 + j < a.E ? logit(a, row, e0 + j) : -INFINITY;
     }
+    if (kShared && a.bias) {
+        for (int e = threadIdx.x; e < L * V; e += blockDim.x) biases[Keys<V>::place(e)] = e < a.E ? a.bias[e] : -INFINITY;
+        __syncthreads();
+    }
+    if (first_row >= a.n) return;
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
     float m = -INFINITY;
     if (softmax) {
@@ -385,10 +471,23 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         for (int j = 0; j < V; ++j) key[j] = takes_part(l[j]) ? sortable(l[j] + 0.f) : 0u;  // (-0 ties with 0)
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float b = e0 + j < a.E ? a.bias[e0 + j] : -INFINITY;
-            const float c = (softmax ? exp_key(l[j], m) * rcp_sum : sigmoid_key(l[j])) + b;
-            key[j] = takes_part(l[j]) && takes_part(b) ? sortable(c + 0.f) : 0u;
+        for (int i = 0; i < V; i += 4) {
+            float b[4];
+            if constexpr (kShared) {
+                const float4 v = *reinterpret_cast<const float4 *>(biases + sub * (V + 4) + i);
+                b[0] = v.x;
+                b[1] = v.y;
+                b[2] = v.z;
+                b[3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = e0 + i + j < a.E ? a.bias[e0 + i + j] : -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float z = l[i + j], c = (softmax ? exp_key(z, m) * rcp_sum : sigmoid_key(z)) + b[j];
+                key[i + j] = takes_part(z) && takes_part(b[j]) ? sortable(c + 0.f) : 0u;
+            }
         }
     }
     const float err = softmax ? kSoftmaxErr : kSigmoidErr;
@@ -491,7 +590,13 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             bool close = has && r0 + sub > 0 && !(before - c > near);
             if (close) {  // the same logit and the same bias are an exact tie
                 const int i = ranks[r0 + sub], j = ranks[r0 + sub - 1];
-                close = logit(a, row, i) != logit(a, row, j) || a.bias[i] != a.bias[j];
+                const float bi = a.bias[i], bj = a.bias[j];
+                close = logit(a, row, i) != logit(a, row, j) || bi != bj;
+                // by the errors of these two scores, which are c - bias (317 x 256: 5 us, 11 with kSoftmaxErr)
+                if (softmax) {
+                    const float rounding = 0x1p-22f * (fabsf(c) + fabsf(before)), p = fmaxf(c - bi, before - bj) + rounding;
+                    close = close && !(before - c > 2.f * (kSoftmaxErr * p + 0x1p-23f * sqrtf(p)) + rounding);
+                }
             }
             unsure |= row_ballot<L>(close) != 0u;  // (every lane votes, whatever its row has found)
             from = fminf(from, has ? (c == INFINITY ? 3.0e38f : c - 2.f * near) : INFINITY);
@@ -546,9 +651,12 @@ cudaError_t launch(RouteArgs a, cudaStream_t st) {
     const unsigned piece = min(16, V * esz);  // bytes of a load
     a.vector = ((uintptr_t)a.logits % piece) == 0 && (a.ldl * esz) % piece == 0;
     a.words = warp_words(L, V, a.E, a.bias || (a.groups > 1 && a.top2));
-    const int warps = min(4, 48 * 1024 / (4 * a.words)), rows = warps * (32 / L);
-    return launch_overlapped(route_kernel<L, V>, dim3((unsigned)((a.n + rows - 1) / rows)), 32 * warps, 4 * warps * a.words,
-                             1, st, a);
+    // eight lanes read the biases from a copy of the block's: from where they lie it would be V loads a
+    // lane, of 8 sectors each (8192 x 256: 8.9 us, 9.8 from there)
+    const int shared = L < 32 && a.bias ? L * (V + 4) : 0;
+    const int warps = min(4, (12 * 1024 - shared) / a.words), rows = warps * (32 / L);
+    return launch_overlapped(route_kernel<L, V>, dim3((unsigned)((a.n + rows - 1) / rows)), 32 * warps,
+                             4 * (shared + warps * a.words), 1, st, a);
 }
 
 }  // namespace

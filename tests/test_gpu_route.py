@@ -106,6 +106,21 @@ def test_scores_next_to_each_other_are_told_apart():
         both(z.cuda(), 9, score=score, bias=torch.full((E,), 0.5).cuda(), groups=16, top_groups=5, group_score="top2")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,tied,target", [(40, 6, 0.75), (200, 25, 0.5), (256, 31, 1.0), (128, 90, 0.3), (1000, 20, 2.0), (64, 33, -3.0)])
+def test_scores_that_tie_but_for_the_rounding_of_their_bias(E, tied, target, score):
+    """Score + bias is `target` for some experts, but for the bias's rounding to f32: their ranks lie
+    2^-26 |target| and less from each other."""
+    for seed in range(4):
+        g = torch.Generator().manual_seed(100 * E + seed)
+        z = (2.5 * torch.randn(E, generator=g)).to(F32)
+        s = torch.tensor(ref.scores(z.double().tolist(), score), dtype=torch.float64)
+        b = torch.full((E,), target - 1.5, dtype=torch.float64)
+        chosen = torch.randperm(E, generator=g)[:tied]
+        b[chosen] = target - s[chosen]
+        both(z[None].cuda(), min(8, tied), score=score, bias=b.to(F32).cuda(), scale=1.5)
+
+
 @pytest.mark.parametrize("n", [3000, 5001])
 def test_many_rows_with_a_bias(n):
     """Enough rows that some are ranked again; a warp or eight lanes a row."""
