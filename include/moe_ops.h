@@ -18,8 +18,9 @@
  * Together they run a layer that moe_decode_forward does not: a shared expert
  * beside the routed ones, the projections around the step, experts that a
  * checkpoint leaves unquantised or keeps in 8 bits, and any router (the grouping
- * and the combine take ids and weights, from moe_route or anywhere else). The sources of the step (mlxcel issues #1616 and #1859) have
- * the routed block only; grouping and combine follow the same readings:
+ * and the combine take ids and weights, from moe_route or anywhere else). The
+ * sources of the step (mlxcel issues #1616 and #1859) have the routed block only;
+ * grouping and combine follow the same readings:
  * #1616 Leading hypothesis (slots sorted by expert id), Current Behavior
  * (moe_weighted_sum), Implementation Notes (f32 partials with a single final
  * rounding; decline unsupported shapes, validate before dispatch).

@@ -157,7 +157,7 @@ Q8 kernel_q8(const Product &a) {
     const double k = a.K / 1024.0;
     const int fours = n == 1 ? 1 : (n + 3) / 4 * 4, blocks = (a.N + 15) / 16;
     const double dot = 1.8 + mb * (0.1 + 0.0215 * fours) + 3e-5 * a.N * mats * fours;
-    const double per_k = n <= 8 ? (mats == 2 ? 1.05 : 0.48) : n <= 16 ? (mats == 2 ? 1.5 : 0.66)
+    const double per_k = n <= 8 ? (mats == 2 ? 1.05 : 0.48) : n <= 16 ? (mats == 2 ? 1.5 : 0.6)
                          : blocks <= 152 ? (mats == 2 ? 2.3 : 1.33) : (mats == 2 ? 2.9 : 1.9);
     const double rows = n <= 16 ? 1.4 + max(1.0, a.N / 2048.0) * ((mats == 2 ? 0.6 : 0.45) + k * per_k)
                                 : 1.2 + (n + 31) / 32 * ((blocks + 303) / 304) * ((mats == 2 ? 2.2 : 1.3) + k * per_k);

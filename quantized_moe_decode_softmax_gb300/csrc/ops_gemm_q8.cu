@@ -8,20 +8,32 @@
 // full rate, where whole numbers to 2048 are exact, so the codes become f16 between
 // shared memory and the MMA. The sums in f32 are exact to 2^24.
 //
-// Tiles, work items and epilogue are those of the 16-bit products (ops_gemm.cu): a
-// pair of CTAs, 128 weight rows per CTA as the M operand, up to 256 rows of x as N. New
-// is what lies between the loads and the MMAs:
+// Tiles, work items and epilogue are those of the 16-bit products (ops_gemm.cu, ops_pair.cuh): a
+// pair of CTAs, 128 weight rows per CTA as the M operand, up to 256 rows of x (gated: 128) as N.
+// New is what lies between the loads and the MMAs:
 //   - a load stage holds 128 inputs as codes: 16 KB of weights (per matrix) and half of
-//     the tile's rows of x, 128 bytes each, by TMA with the 128-byte swizzle;
-//   - eight warps convert, four of them the first 64 inputs of a stage and four the other 64.
-//     The weights go to tensor memory (thread = weight row = lane; the MMA takes A from
-//     there), the rows of x to a second ring in shared memory, in the swizzled layout of
-//     a 16-bit tile. A half stage is handed to the MMA by itself;
+//     the tile's rows of x, 128 bytes each, by TMA with the 128-byte swizzle. A warp loads the
+//     weights, one or two the rows of x, and another finds the work items for all;
+//   - three groups of four warps convert, a unit each in turn: a half stage, or a whole one of
+//     short tiles. The weights go to tensor memory (thread = weight row = lane; the MMA takes A
+//     from there), the rows of x to a second ring in shared memory, in the swizzled layout of a
+//     16-bit tile;
 //   - A in tensor memory is what makes the rates meet: per 64 inputs at 256 rows a CTA's MMAs
 //     take 512 cycles, in which its shared memory moves 64 KB: 16 in by TMA, 16 read by the
 //     converters, 16 written by them (x) and 16 read by the MMAs (x). With A there too it
 //     would be 96. Tensor memory then has room for one accumulator set at 256 rows (two up
-//     to 192; gated: one up to 192, two up to 96).
+//     to 192; gated: one at 128 and two up to 64).
+//
+// 24 warps at 80 registers: what does not fit in those spills into the conversion loop or the
+// epilogue and costs at once (gated 8192x4096x2048, 20 bytes spilled: 165 us, without 155).
+//
+// Bound. Long products: the tensor cores, but for the epilogue of a single accumulator set, in
+// which they stand still (8192x4096x4096 147 us, 1870 TFLOP/s; gated 8192x4096x2048 152 us,
+// 1810; the tensor pipe is busy 79 % of the second's cycles). Short tiles: the converters,
+// whose 5 operations for 4 codes share the integer pipe (62 % busy), and their waits for each other:
+// about 650 cycles per 128 inputs. A few hundred rows: 2.5 us before the first MMA, and the epilogue
+// (317x2032x4104 with GELU and a residual 13.1 us: 5 of them steps, 2.7 the epilogue). Few rows
+// per expert: HBM (64 tokens, 768 -> 2048, 128 experts: 38 us, 5.3 TB/s).
 //
 // Every wait is bounded (1 s, reported through moe_ops_check); after one gives
 // up, all roles stop and the pair waits for its copies in flight before it ends.
@@ -556,8 +568,10 @@ Device g_devices[kMaxDevices];
 // down 49 to 39 us), otherwise half of one (long ones: 8192x4096x4096 152 us, 169 with whole stages).
 constexpr int half_cols(int mats) { return mats * kK / 2; }
 constexpr int max_rows(int mats) { return mats == 2 ? 128 : 256; }
-static_assert(max_rows(1) + kUnits * half_cols(1) <= kTmemCols && 2 * max_rows(2) + kUnits * half_cols(2) <= kTmemCols, "they fit");
-constexpr bool wide_units(int mats, int rows) { return mats == 1 && rows <= 96; }  // (7 load stages fit up to there, but beside some 260 groups and more)
+static_assert(max_rows(1) + kUnits * half_cols(1) <= kTmemCols && 2 * max_rows(2) + kUnits * half_cols(2) <= kTmemCols,
+              "they fit");
+// (7 load stages of whole units fit up to there, but beside some 260 groups and more)
+constexpr bool wide_units(int mats, int rows) { return mats == 1 && rows <= 96; }
 constexpr int sets_of(int mats, int rows) {
     return 2 * mats * rows + kUnits * (wide_units(mats, rows) ? 2 : 1) * half_cols(mats) <= kTmemCols ? 2 : 1;
 }

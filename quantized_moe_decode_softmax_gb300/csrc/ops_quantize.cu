@@ -4,7 +4,7 @@
 //
 // Bound: 3 bytes per value, each moved once. A row stays in registers between its
 // maximum and its codes: T threads share it, V loads of 16 bytes each, all in flight
-// before the first is used (8192 x 4096: 16.4 us, 6.1 TB/s). Rows of more than 512 x 8 loads
+// before the first is used (8192 x 4096: 15.2 us, 6.6 TB/s). Rows of more than 512 x 8 loads
 // are read twice.
 //
 // Codes are those of the exact quotient, halves to even, for one product and one rounding

@@ -135,6 +135,37 @@ def test_quantize_past_32_bits():
     assert torch.equal(r.codes[at], ref8.quantized(big[at])[0])
 
 
+MOST = 1 << 24  # rows of a call
+
+
+def test_the_longest_rows_to_quantize():
+    for dtype in (BF16, F16):
+        x = normal(gen(5), (3, 1 << 20), dtype=dtype)
+        r = q.moe_quantize_rows(x)
+        codes_, scale = ref8.quantized(x)[:2]
+        assert torch.equal(r.codes, codes_) and torch.equal(r.scale, scale.float())
+
+
+def test_the_most_rows():
+    g = gen(6)
+    x = normal(g, (MOST, 3))
+    r = q.moe_quantize_rows(x)
+    at = torch.cat([torch.arange(0, MOST, 99991, device="cuda"), torch.arange(MOST - 300, MOST, device="cuda")])
+    assert torch.equal(r.codes[at], ref8.quantized(x[at])[0])
+    del x, r
+    z = torch.randn((MOST, 2), generator=g, device="cuda")
+    r = q.moe_route(z, q.Router(2, 1, score="sigmoid", bias=torch.tensor([0.25, 0.0], device="cuda"), renormalize=False))
+    assert torch.equal(r.topk_idx[:, 0].long(), ((torch.sigmoid(z.double()) + torch.tensor([0.25, 0.0], device="cuda")).argmax(1)))
+    del z, r
+    t = weights(g, (), 3, 16, BF16, True, True)
+    x = q.QuantizedRows(codes(g, (MOST, 16)), scales(g, (MOST,), 1e-2))
+    out = q.moe_linear_q8(x, q.LinearWeightsQ8(**t, activation="silu"))
+    ref.check(out[at], *ref8.product(x.codes[at], x.scale[at], act="silu", **t))
+    with pytest.raises(q.MoeError):
+        q.moe_quantize_rows(normal(g, (MOST + 1, 1)))
+    q.moe_ops_check()
+
+
 def test_route_past_32_bits():
     z = torch.empty(4200 * (1 << 20), dtype=BF16, device="cuda").as_strided((4200, 100), (1 << 20, 1))
     z.copy_(normal(gen(3), (4200, 100)))
