@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kMmaWarp) tmem_alloc_pair(&tslot, kTmemCols);
     tc::fence_before_sync();
+    __syncwarp();
     cluster_arrive();
     Group one{0, 0, p.rows, 0};
     int total = 0;
