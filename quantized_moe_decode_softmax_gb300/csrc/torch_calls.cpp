@@ -4,16 +4,16 @@
 // A call on a few tokens is as long on the host as on the GPU, and most of that is
 // the interpreter asking each tensor for its properties and allocating the output.
 // Here the same checks and the allocation are C++ (host time of a one-token linear on
-// a Grace core: 3.6 us, 11 through ctypes). Whatever is not the usual call (another device or stream, a tensor
-// subclass, an input that asks for a gradient, any argument that does not fit)
-// returns None, and ops.py goes on from there with its own checks and messages.
+// a Grace core: 2.9 us, 11 through ctypes). Whatever is not the usual call (another device
+// or stream, a tensor subclass, an input that asks for a gradient, any argument that does
+// not fit) returns None, and ops.py goes on from there with its own checks and messages.
 // Compiled against the installed torch, without the CUDA library: ops.py passes in
 // the addresses of its entry points.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
 #include <c10/core/GradMode.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -72,6 +72,24 @@ PyObject *result(moe_status st, const at::Tensor &out, PyObject *given) {
         return given;
     }
     return THPVariable_Wrap(out);
+}
+
+// Memory on the current device for an output, from torch's allocator, and a tensor of `type`
+// and these sizes on it from byte `at` on. (at::empty finds its way to the same allocator in
+// about 1 us more; several outputs share a storage, which lives as long as any of them.)
+c10::Storage memory(int64_t bytes) {
+    c10::Allocator *a = c10::cuda::CUDACachingAllocator::get();
+    return c10::Storage(c10::Storage::use_byte_size_t(), bytes, a->allocate(bytes), a, true);
+}
+at::Tensor part_of(const c10::Storage &all, at::ScalarType type, int64_t at, at::IntArrayRef sizes) {
+    const auto meta = c10::scalarTypeToTypeMeta(type);
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all), c10::DispatchKeySet(c10::DispatchKey::CUDA), meta);
+    t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)meta.itemsize());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    return t;
+}
+at::Tensor empty(int64_t n, int64_t cols, at::ScalarType type) {
+    return part_of(memory(n * cols * (int64_t)c10::elementSize(type)), type, 0, {n, cols});
 }
 
 at::ScalarType type_of(int dtype) { return dtype == MOE_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
@@ -144,7 +162,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || n > INT32_MAX || (res && !rows(*res, n, p->N, dt, dev, &ldr)) ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
-    const at::Tensor out = given ? *given : at::empty({n, p->N}, x->options());
+    const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st = fn_linear(p, x->const_data_ptr(), ldx, (int)n, res ? res->const_data_ptr() : nullptr, ldr,
                                     out.mutable_data_ptr(), ldo, c10::cuda::getCurrentCUDAStream(dev).stream());
     return result(st, out, a[4]);
@@ -171,7 +189,7 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || x_rows == 0 || n > INT32_MAX || x_rows > INT32_MAX ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
-    const at::Tensor out = given ? *given : at::empty({n, p->N}, x->options());
+    const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st = fn_grouped(p, off->const_data_ptr<int32_t>(), token ? token->const_data_ptr<int32_t>() : nullptr,
                                      x->const_data_ptr(), ldx, (int)x_rows, (int)n, out.mutable_data_ptr(), ldo,
                                      c10::cuda::getCurrentCUDAStream(dev).stream());
@@ -196,18 +214,10 @@ PyObject *slots(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         c10::cuda::current_device() != idx->get_device())
         return other();
     const int64_t S = idx->numel();
-    const at::Tensor all = at::empty({3 * S + E + 1}, idx->options());
-    // One allocation, and four tensors on its storage, each with the values that it
-    // alone covers: a call of 8 x 8 ids takes 5.2 us of the host, 7.8 with four
-    // allocations. The storage lives as long as any of the four.
-    auto part = [&](int64_t first, at::IntArrayRef sizes) {
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
-        t.unsafeGetTensorImpl()->set_storage_offset(first);
-        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-        return t;
-    };
-    const at::Tensor token = part(0, {S}), rank = part(S, {S}), of = part(2 * S, idx->sizes()),
-                     offsets = part(3 * S, {E + 1});
+    // one allocation, and four tensors on its storage, each with the values that it alone covers
+    const c10::Storage all = memory(4 * (3 * S + E + 1));
+    const at::Tensor token = part_of(all, at::kInt, 0, {S}), rank = part_of(all, at::kInt, 4 * S, {S}),
+                     of = part_of(all, at::kInt, 8 * S, idx->sizes()), offsets = part_of(all, at::kInt, 12 * S, {E + 1});
     const moe_status st =
         fn_slots(idx->const_data_ptr<int32_t>(), (int)idx->size(0), (int)idx->size(1), (int)E, (int)lo, (int)hi,
                  offsets.mutable_data_ptr<int32_t>(), token.mutable_data_ptr<int32_t>(),
@@ -241,7 +251,7 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         (res && !rows(*res, n, N, dt, dev, &ldr)) || (given && !rows(*given, n, N, dt, dev, &ldo)) ||
         c10::cuda::current_device() != dev)
         return other();
-    const at::Tensor out = given ? *given : at::empty({n, N}, y->options());
+    const at::Tensor out = given ? *given : empty(n, N, dt);
     const moe_status st = fn_combine(dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16, y->const_data_ptr(), ldy, (int)r,
                                      of->const_data_ptr<int32_t>(), w->const_data_ptr<float>(), (int)n, (int)k, (int)N,
                                      res ? res->const_data_ptr() : nullptr, ldr, out.mutable_data_ptr(), ldo,
@@ -250,29 +260,22 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
-// a tensor of `type` and these sizes on another's storage, from byte `at` on
-at::Tensor part_of(const at::Tensor &all, at::ScalarType type, int64_t at, at::IntArrayRef sizes) {
-    const auto meta = c10::scalarTypeToTypeMeta(type);
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), meta);
-    t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)meta.itemsize());
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-    return t;
-}
-
-// two results of a call, or its status as a number
-PyObject *results(moe_status st, const at::Tensor &first, const at::Tensor &second) {
+// two results of a call as a `type` (a subclass of tuple without members), or its status as a number
+PyObject *results(moe_status st, PyTypeObject *type, const at::Tensor &first, const at::Tensor &second) {
     if (st != MOE_OK) return PyLong_FromLong(st);
-    PyObject *t = PyTuple_New(2);
+    PyObject *t = type->tp_alloc(type, 2);
     if (!t) return nullptr;
     PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(first));
     PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(second));
     return t;
 }
 
-// route(router address, logits, (bias,)): (topk_idx, topk_w)
+bool tuple_type(PyObject *o) { return PyType_Check(o) && PyType_IsSubtype((PyTypeObject *)o, &PyTuple_Type); }
+
+// route(router address, logits, (bias,), type): type of (topk_idx, topk_w)
 PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 3 || !PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 1) return other();
+    if (n_args != 4 || !PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 1 || !tuple_type(a[3])) return other();
     const auto *r = static_cast<const moe_router *>(PyLong_AsVoidPtr(a[0]));
     const at::Tensor *l;
     if (!r || !tensor(a[1], &l) || !l || l->dim() != 2 || !l->is_cuda()) return other();
@@ -288,20 +291,20 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if ((dt != at::kBFloat16 && dt != at::kHalf && dt != at::kFloat) || !rows(*l, -1, r->E, dt, dev, &ldl) || n == 0 ||
         n > INT32_MAX || k < 1 || k > 1024 || c10::cuda::current_device() != dev)
         return other();
-    const at::Tensor all = at::empty({8 * n * k}, l->options().dtype(at::kByte));
+    const c10::Storage all = memory(8 * n * k);
     const at::Tensor idx = part_of(all, at::kInt, 0, {n, k}), w = part_of(all, at::kFloat, 4 * n * k, {n, k});
     const moe_status st = fn_route(r, dt == at::kFloat ? MOE_DTYPE_F32 : dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16,
                                    l->const_data_ptr(), ldl, (int)n, idx.mutable_data_ptr<int32_t>(),
                                    w.mutable_data_ptr<float>(), c10::cuda::getCurrentCUDAStream(dev).stream());
-    return results(st, idx, w);
+    return results(st, (PyTypeObject *)a[3], idx, w);
     END_HANDLE_TH_ERRORS
 }
 
-// quantize(x): (codes, scale)
+// quantize(x, type): type of (codes, scale)
 PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
     const at::Tensor *x;
-    if (n_args != 1 || !tensor(a[0], &x) || !x || x->dim() != 2 || !x->is_cuda()) return other();
+    if (n_args != 2 || !tuple_type(a[1]) || !tensor(a[0], &x) || !x || x->dim() != 2 || !x->is_cuda()) return other();
     const int dev = (int)x->get_device();
     const at::ScalarType dt = x->scalar_type();
     const int64_t n = x->size(0), K = x->size(1);
@@ -310,12 +313,12 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         !rows(*x, -1, K, dt, dev, &ldx) || c10::cuda::current_device() != dev)
         return other();
     const int64_t at_scale = (n * K + 15) / 16 * 16;
-    const at::Tensor all = at::empty({at_scale + 4 * n}, x->options().dtype(at::kByte));
+    const c10::Storage all = memory(at_scale + 4 * n);
     const at::Tensor codes = part_of(all, at::kChar, 0, {n, K}), scale = part_of(all, at::kFloat, at_scale, {n});
     const moe_status st = fn_quantize(dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16, x->const_data_ptr(), ldx, (int)n,
                                       (int)K, codes.mutable_data_ptr<int8_t>(), K, scale.mutable_data_ptr<float>(),
                                       c10::cuda::getCurrentCUDAStream(dev).stream());
-    return results(st, codes, scale);
+    return results(st, (PyTypeObject *)a[1], codes, scale);
     END_HANDLE_TH_ERRORS
 }
 
@@ -340,7 +343,7 @@ PyObject *linear_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || n > INT32_MAX || (res && !rows(*res, n, p->N, dt, dev, &ldr)) ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
-    const at::Tensor out = given ? *given : at::empty({n, p->N}, x->options().dtype(dt));
+    const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st =
         fn_linear_q8(p, x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)n,
                      res ? res->const_data_ptr() : nullptr, ldr, out.mutable_data_ptr(), ldo,
@@ -369,7 +372,7 @@ PyObject *grouped_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || x_rows == 0 || n > INT32_MAX || x_rows > INT32_MAX ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
-    const at::Tensor out = given ? *given : at::empty({n, p->N}, x->options().dtype(dt));
+    const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st = fn_grouped_q8(
         p, off->const_data_ptr<int32_t>(), token ? token->const_data_ptr<int32_t>() : nullptr,
         x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)x_rows, (int)n, out.mutable_data_ptr(), ldo,

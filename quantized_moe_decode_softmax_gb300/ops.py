@@ -586,9 +586,9 @@ def moe_route(logits, router: Router, stream=None) -> Routing:
     float32, columns adjacent). Ids are in falling order of what decides, ties by the
     lower id; -1 with weight 0 where experts whose logit or bias is -inf leave fewer."""
     if stream is None and _calls is not None:
-        r = _calls.route(router.ref, logits, router.tensors)
+        r = _calls.route(router.ref, logits, router.tensors, Routing)
         if r is not None:
-            return Routing._make(r) if r.__class__ is not int else _raise(r, "moe_route")
+            return r if r.__class__ is not int else _raise(r, "moe_route")
     _kind(router, Router)
     bias = router.tensors[0]
     _no_grad(logits, bias)
@@ -618,11 +618,11 @@ def _route(c, code, logits, ldl, router, st):
 def moe_quantize_rows(x, stream=None) -> QuantizedRows:
     """8-bit codes of the rows of x [n, K] (bfloat16 or float16, columns adjacent) and the
     scale of each: x is about codes * scale[:, None], the largest of a row at 127."""
-    _lib()
     if stream is None and _calls is not None:
-        r = _calls.quantize(x)
+        r = _calls.quantize(x, QuantizedRows)
         if r is not None:
-            return QuantizedRows._make(r) if r.__class__ is not int else _raise(r, "moe_quantize_rows")
+            return r if r.__class__ is not int else _raise(r, "moe_quantize_rows")
+    _lib()
     _no_grad(x)
     dev, dt = x.get_device(), x.dtype
     code = _dtype_code(dt)

@@ -249,3 +249,50 @@ def test_an_output_counts_as_written():
                     loss.backward()
     finally:
         q.ops._calls = keep
+
+
+@pytest.mark.parametrize("mode", [torch.enable_grad, torch.no_grad, torch.inference_mode])
+def test_results_are_ordinary_tensors(mode):
+    """Outputs made by a call are what torch.empty makes: their dispatch keys, version counters,
+    autograd, storages."""
+    x, off = normal(gen(1), (6, 32)), offsets_of([6])
+    lw = q.LinearWeightsQ8(torch.ones(16, 32, dtype=I8, device="cuda"), torch.ones(16, device="cuda"))
+    lg = q.LinearWeightsQ8(torch.ones(1, 16, 32, dtype=I8, device="cuda"), torch.ones(1, 16, device="cuda"))
+    l16, idx = q.LinearWeights(normal(gen(2), (16, 32))), torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+    with mode():
+        made = [*q.moe_quantize_rows(x), *q.moe_route(x, q.Router(32, 4)), *q.moe_group_slots(idx, 4), q.moe_linear(x, l16)]
+        made += [q.moe_linear_q8(q.moe_quantize_rows(x), lw), q.moe_grouped_linear_q8(q.moe_quantize_rows(x), lg, off)]
+        for t in made:
+            like = torch.empty(t.shape, dtype=t.dtype, device="cuda")
+            assert torch._C._dispatch_keys(t) == torch._C._dispatch_keys(like)
+            assert t.is_inference() == like.is_inference() and t.device == like.device and t.layout == like.layout
+            assert t.is_contiguous() and not t.requires_grad and t.is_leaf
+            if not t.is_inference():
+                assert t._version == 0
+                t.add_(1)
+                assert t._version == 1
+    if mode is not torch.inference_mode:
+        out = made[-1].detach().requires_grad_()
+        (3 * out).sum().backward()
+        assert bool((out.grad == 3).all())
+        alone = made[-1]
+        alone.resize_(0)
+        assert alone.numel() == 0
+
+
+def test_results_give_their_memory_back():
+    x = normal(gen(3), (4096, 1024))
+    r = q.Router(1024, 8)
+    for call in (lambda: q.moe_quantize_rows(x), lambda: q.moe_route(x, r)):
+        call()
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        first, second = call()
+        more = torch.cuda.memory_allocated() - before
+        assert more >= first.nbytes + second.nbytes
+        keep = second.clone()
+        del first
+        assert torch.cuda.memory_allocated() - before >= more
+        assert torch.equal(keep, second)
+        del second, keep
+        assert torch.cuda.memory_allocated() == before
