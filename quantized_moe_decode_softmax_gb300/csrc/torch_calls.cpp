@@ -322,22 +322,23 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     END_HANDLE_TH_ERRORS
 }
 
-// codes [rows, K] and the scale of each row
-bool coded(PyObject *c, PyObject *s, int64_t K, int dev, const at::Tensor **x, const at::Tensor **scale, int64_t *ldx) {
-    return tensor(c, x) && *x && tensor(s, scale) && *scale && rows(**x, -1, K, at::kChar, dev, ldx) &&
+// (codes [rows, K], the scale of each row)
+bool coded(PyObject *o, int64_t K, int dev, const at::Tensor **x, const at::Tensor **scale, int64_t *ldx) {
+    return PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 2 && tensor(PyTuple_GET_ITEM(o, 0), x) && *x &&
+           tensor(PyTuple_GET_ITEM(o, 1), scale) && *scale && rows(**x, -1, K, at::kChar, dev, ldx) &&
            dense(**scale, at::kFloat, dev) && (*scale)->dim() == 1 && (*scale)->size(0) == (*x)->size(0);
 }
 
-// linear_q8(product address, device, codes, scale, residual, out, weights)
+// linear_q8(product address, device, (codes, scale), residual, out, weights)
 PyObject *linear_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 7) return other();
+    if (n_args != 6) return other();
     const auto *p = static_cast<const moe_product_q8 *>(PyLong_AsVoidPtr(a[0]));
     const int dev = (int)PyLong_AsLong(a[1]);
-    if (dev < 0 || !weights(a[6], p, dev) || p->E != 1) return other();
+    if (dev < 0 || !weights(a[5], p, dev) || p->E != 1) return other();
     const at::Tensor *x, *scale, *res, *given;
     int64_t ldx, ldr = 0, ldo = p->N;
-    if (!coded(a[2], a[3], p->K, dev, &x, &scale, &ldx) || !tensor(a[4], &res) || !tensor(a[5], &given)) return other();
+    if (!coded(a[2], p->K, dev, &x, &scale, &ldx) || !tensor(a[3], &res) || !tensor(a[4], &given)) return other();
     const at::ScalarType dt = type_of(p->dtype);
     const int64_t n = x->size(0);
     if (n == 0 || n > INT32_MAX || (res && !rows(*res, n, p->N, dt, dev, &ldr)) ||
@@ -348,21 +349,21 @@ PyObject *linear_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         fn_linear_q8(p, x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)n,
                      res ? res->const_data_ptr() : nullptr, ldr, out.mutable_data_ptr(), ldo,
                      c10::cuda::getCurrentCUDAStream(dev).stream());
-    return result(st, out, a[5]);
+    return result(st, out, a[4]);
     END_HANDLE_TH_ERRORS
 }
 
-// grouped_q8(product address, device, codes, scale, offsets, row_token, out, weights)
+// grouped_q8(product address, device, (codes, scale), offsets, row_token, out, weights)
 PyObject *grouped_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    if (n_args != 8) return other();
+    if (n_args != 7) return other();
     const auto *p = static_cast<const moe_product_q8 *>(PyLong_AsVoidPtr(a[0]));
     const int dev = (int)PyLong_AsLong(a[1]);
-    if (dev < 0 || !weights(a[7], p, dev)) return other();
+    if (dev < 0 || !weights(a[6], p, dev)) return other();
     const at::Tensor *x, *scale, *off, *token, *given;
     int64_t ldx, ldo = p->N;
-    if (!coded(a[2], a[3], p->K, dev, &x, &scale, &ldx) || !tensor(a[4], &off) || !off || !tensor(a[5], &token) ||
-        !tensor(a[6], &given))
+    if (!coded(a[2], p->K, dev, &x, &scale, &ldx) || !tensor(a[3], &off) || !off || !tensor(a[4], &token) ||
+        !tensor(a[5], &given))
         return other();
     if (!dense(*off, at::kInt, dev) || off->dim() != 1 || off->size(0) != p->E + 1 ||
         (token && (!dense(*token, at::kInt, dev) || token->dim() != 1)))
@@ -377,7 +378,7 @@ PyObject *grouped_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         p, off->const_data_ptr<int32_t>(), token ? token->const_data_ptr<int32_t>() : nullptr,
         x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)x_rows, (int)n, out.mutable_data_ptr(), ldo,
         c10::cuda::getCurrentCUDAStream(dev).stream());
-    return result(st, out, a[6]);
+    return result(st, out, a[5]);
     END_HANDLE_TH_ERRORS
 }
 

@@ -661,8 +661,8 @@ def _codes(x, K, dev):
 def moe_linear_q8(x, weights: LinearWeightsQ8, residual=None, out=None, stream=None):
     """moe_linear on codes: x is (codes [n, K] int8, scale [n] float32), as moe_quantize_rows
     returns it; out [n, N] of the weights' dtype; `out` may be `residual`."""
-    if stream is None and _calls is not None and x.__class__ in (QuantizedRows, tuple) and len(x) == 2:
-        r = _calls.linear_q8(weights.ref, weights.device_index, x[0], x[1], residual, out, weights.tensors)
+    if stream is None and _calls is not None:
+        r = _calls.linear_q8(weights.ref, weights.device_index, x, residual, out, weights.tensors)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_linear_q8")
     _kind(weights, LinearWeightsQ8)
@@ -699,8 +699,8 @@ def _linear_q8(c, codes, ldx, scale, weights, residual, ldr, out, ldo, st):
 def moe_grouped_linear_q8(x, weights: LinearWeightsQ8, offsets, row_token=None, out=None, stream=None):
     """moe_grouped_linear on codes: x is (codes, scale) of [rows, K], or of [tokens, K] with
     row_token [rows]; out [rows, N] of the weights' dtype."""
-    if stream is None and _calls is not None and x.__class__ in (QuantizedRows, tuple) and len(x) == 2:
-        r = _calls.grouped_q8(weights.ref, weights.device_index, x[0], x[1], offsets, row_token, out, weights.tensors)
+    if stream is None and _calls is not None:
+        r = _calls.grouped_q8(weights.ref, weights.device_index, x, offsets, row_token, out, weights.tensors)
         if r is not None:
             return r if r.__class__ is not int else _raise(r, "moe_grouped_linear_q8")
     _kind(weights, LinearWeightsQ8)
