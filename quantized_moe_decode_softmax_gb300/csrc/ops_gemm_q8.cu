@@ -25,11 +25,13 @@
 //     to 192; gated: one at 128 and two up to 64).
 //
 // 24 warps at 80 registers: what does not fit in those spills into the conversion loop or the
-// epilogue and costs at once (gated 8192x4096x2048, 20 bytes spilled: 165 us, without 155).
+// epilogue and costs at once (gated 8192x4096x2048, 20 bytes spilled: 165 us, without 155). So does
+// every instruction of the conversion loop: a sixth for 4 codes makes it 179, and the 8 selects a
+// piece that kept neighbouring pieces of x on different banks made it 152 of 149.
 //
 // Bound. Long products: the tensor cores, but for the epilogue of a single accumulator set, in
-// which they stand still (8192x4096x4096 147 us, 1870 TFLOP/s; gated 8192x4096x2048 152 us,
-// 1810; the tensor pipe is busy 79 % of the second's cycles). Short tiles: the converters,
+// which they stand still (8192x4096x4096 146 us, 1880 TFLOP/s; gated 8192x4096x2048 149 us,
+// 1850; the tensor pipe is busy 80 % of the second's cycles). Short tiles: the converters,
 // whose 5 operations for 4 codes share the integer pipe (62 % busy), and their waits for each other:
 // about 650 cycles per 128 inputs. A few hundred rows: 2.5 us before the first MMA, and the epilogue
 // (317x2032x4104 with GELU and a residual 13.1 us: 5 of them steps, 2.7 the epilogue). Few rows
@@ -430,17 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // place, and after the last fill of the stage if there are at least 4 stages (wide: 7).)
         const int q = warp & 3;  // quadrant of the lanes
         const uint32_t peer_full = in_first(u_full_addr);
-        const int wr = 32 * q + lane;  // this thread's weight row
-        uint32_t w_src[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w_src[j] = ring_addr + wr * 128 + ((j ^ (wr & 7)) << 4);  // (second half: bit 6 turned)
-        // this thread's pieces of x: row and 16 codes of an atom of 8 rows. The lanes of a quarter
-        // warp take rows r and r + 4 and write their two pieces in turn, which keeps them on
-        // different banks
-        const int l = lane & 7, xr = (lane >> 3) + 4 * (l >> 2), swap = l >> 2;
+        // This thread's weight row, its first 16 codes; the j-th of the four pieces of a half stage
+        // lies at that address ^ 16 j, and the second half at ^ 64.
+        const int wr = 32 * q + lane;
+        const uint32_t w_src = ring_addr + wr * 128 + ((wr & 7) << 4);
+        // This thread's pieces of x: row and 16 codes of an atom of 8 rows. The lanes of a quarter
+        // warp take rows r and r ^ 5, which lie on different banks in the reads (bit 2) and in the
+        // writes (bit 0).
+        const int l = lane & 7, xr = (lane >> 3) ^ (l & 4 ? 5 : 0);
         const uint32_t x_src = ring_addr + MATS * kTileW + q * 1024 + xr * 128 + (((l & 3) ^ xr) << 4);
-        const uint32_t x_dst0 = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3) + swap) ^ xr) << 4);
-        const uint32_t x_dst1 = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3) + 1 - swap) ^ xr) << 4);
+        const uint32_t x_dst = f16_addr + q * 1024 + xr * 128 + (((2 * (l & 3)) ^ xr) << 4);
         const uint32_t a_at = tmem + ((uint32_t)(32 * q) << 16) + g.a_col;
         uint32_t v = warp >> 2;             // this group's unit
         uint32_t slot = v * kHalves / 2, phase = 0;  // its load stage in the ring, and the lap
@@ -455,19 +456,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; v < end; v += kGroups) {
                 const uint32_t u = v % kUnits, stage = slot * stage_bytes;
                 if (!(ok = __all_sync(0xffffffffu, wait(full_addr + 8 * slot, phase, abort_flag)))) break;
-                constexpr int kX = MATS == 2 ? 2 : 4;  // atoms of a warp, at most
+                constexpr int kX = MATS == 2 || WIDE ? 2 : 4;  // atoms of a warp, at most
                 uint4 w[MATS][4], x[kX];
                 auto load = [&](uint32_t turn) {
+                    const uint32_t w_at = (w_src ^ turn) + stage, x_at = (x_src ^ turn) + stage;
 #pragma unroll
                     for (int m = 0; m < MATS; ++m)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) w[m][j] = lds((w_src[j] + stage + m * kTileW) ^ turn);
+                        for (int j = 0; j < 4; ++j) w[m][j] = lds((w_at ^ (16 * j)) + m * kTileW);
 #pragma unroll
                     for (int j = 0; j < kX; ++j)
-                        if (4 * j < atoms) x[j] = lds((x_src + stage + j * 4096) ^ turn);
+                        if (4 * j < atoms) x[j] = lds(x_at + j * 4096);
                 };
                 auto store = [&](uint32_t place) {
-                    const uint32_t a = a_at + place * (MATS * kK / 2), dst = place * g.half_bytes;
+                    const uint32_t a = a_at + place * (MATS * kK / 2), dst = x_dst + place * g.half_bytes;
 #pragma unroll
                     for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -484,10 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kX; ++j) {
                         if (4 * j >= atoms) break;
-                        const uint2 f0 = codes_to_f16(x[j].x), f1 = codes_to_f16(x[j].y), f2 = codes_to_f16(x[j].z),
-                                    f3 = codes_to_f16(x[j].w);
-                        sts(dst + j * 4096 + x_dst0, swap ? f2 : f0, swap ? f3 : f1);
-                        sts(dst + j * 4096 + x_dst1, swap ? f0 : f2, swap ? f1 : f3);
+                        sts(dst + j * 4096, codes_to_f16(x[j].x), codes_to_f16(x[j].y));
+                        sts((dst ^ 16) + j * 4096, codes_to_f16(x[j].z), codes_to_f16(x[j].w));
                     }
                 };
                 load(WIDE ? 0u : (v & 1) << 6);
@@ -564,17 +564,27 @@ struct Device {
 constexpr int kMaxDevices = 64;
 Device g_devices[kMaxDevices];
 
-// Tensor memory beside the accumulator sets: kUnits units of weights as f16. A unit is a whole
-// load stage where that leaves room for two sets (short tiles: half as many hand-overs, 64 tokens
-// down 49 to 39 us), otherwise half of one (long ones: 8192x4096x4096 152 us, 169 with whole stages).
+// A unit is a whole load stage of tiles of up to 96 rows (half as many hand-overs: 64 tokens down
+// 49 to 39 us) where enough stages fit beside them and the table of the groups (of 1024 groups: up
+// to 64 rows; 256 tokens, 8 of 1024 experts, 768 -> 2048: 210 us, 268 with 96 rows and half stages),
+// otherwise half of one (long ones: 8192x4096x4096 152 us, 169 with whole stages). room: shared
+// memory for all of that.
+// Tensor memory beside the accumulator sets holds the kUnits units of weights as f16.
 constexpr int half_cols(int mats) { return mats * kK / 2; }
 constexpr int max_rows(int mats) { return mats == 2 ? 128 : 256; }
 static_assert(max_rows(1) + kUnits * half_cols(1) <= kTmemCols && 2 * max_rows(2) + kUnits * half_cols(2) <= kTmemCols,
               "they fit");
-// (7 load stages of whole units fit up to there, but beside some 260 groups and more)
-constexpr bool wide_units(int mats, int rows) { return mats == 1 && rows <= 96; }
-constexpr int sets_of(int mats, int rows) {
-    return 2 * mats * rows + kUnits * (wide_units(mats, rows) ? 2 : 1) * half_cols(mats) <= kTmemCols ? 2 : 1;
+int stage_bytes(int mats, int rows) { return mats * kTileW + box_rows(rows / kPair) * kIn; }
+int half_bytes(int rows) { return rows / kPair * kK * 2; }
+int stages_of(int mats, int rows, bool wide, int room) {
+    return min(kMaxStages, (room - kUnits * (wide ? 2 : 1) * half_bytes(rows)) / stage_bytes(mats, rows));
+}
+int least_stages(bool wide) { return wide ? 7 : 4; }  // (see the converters)
+bool wide_units(int mats, int rows, int room) {
+    return mats == 1 && rows <= 96 && stages_of(mats, rows, true, room) >= least_stages(true);
+}
+int sets_of(int mats, int rows, bool wide) {
+    return 2 * mats * rows + kUnits * (wide ? 2 : 1) * half_cols(mats) <= kTmemCols ? 2 : 1;
 }
 
 // Rows per tile: the least time of a simple model, in cycles, as in ops_gemm.cu. Waves of tiles
@@ -584,7 +594,7 @@ constexpr int sets_of(int mats, int rows) {
 // last tile, and two thirds of it for every tile with one accumulator set. Among groups, of
 // which some are larger than the mean, a larger cap may cost 8 % more (1024 tokens, 6 of
 // 256 skewed experts, gated 4096 -> 2048: 340 us with 64 rows, 297 with 128).
-int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int pairs) {
+int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int pairs, int room) {
     const int mats = p.w_up ? 2 : 1;
     const int per_row = 20 + 15 * (mats - 1) + (p.act != MOE_EPI_NONE ? 15 : 0) + (p.residual ? 15 : 0);
     long long cost[256 / kStepRows + 1], least = -1;
@@ -593,8 +603,9 @@ int pick_rows(const Product &p, int mblocks, int groups, int mean, int nk, int p
         const long long items = (long long)groups * mblocks * ((mean + t - 1) / t);
         const long long waves = (items + pairs - 1) / pairs;
         const int convert = mats == 2 ? 850 + 3 * t : 600 + 9 * t / 4;
-        const long long step = max(4 * mats * t, wide_units(mats, cap) ? convert : max(convert, 850));
-        const long long one_set = sets_of(mats, cap) == 1 ? waves * per_row * t * 2 / 3 : 0;
+        const bool wide = wide_units(mats, cap, room);
+        const long long step = max(4 * mats * t, wide ? convert : max(convert, 850));
+        const long long one_set = sets_of(mats, cap, wide) == 1 ? waves * per_row * t * 2 / 3 : 0;
         const long long c = cost[cap / kStepRows] = waves * (nk * step + 500) + per_row * t + one_set;
         if (least < 0 || c < least) least = c;
     }
@@ -658,27 +669,22 @@ cudaError_t launch_product_gemm_q8(const Product &p, cudaStream_t st) {
     const int mats = p.w_up ? 2 : 1;
     const int mblocks = (p.N + kPair * kM - 1) / (kPair * kM);
     const int groups = p.offsets ? min(p.E, p.rows) : 1;
+    const int table = p.offsets ? p.E * (int)sizeof(Group) : 0;
+    const int room = d.smem.load(std::memory_order_relaxed) - 1024 - table;
     Tiling g;
-    g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all);
-    g.bufs = sets_of(mats, g.tcap);
-    g.stage_bytes = mats * kTileW + box_rows(g.tcap / kPair) * kIn;
-    g.half_bytes = g.tcap / kPair * kK * 2;
+    g.tcap = pick_rows(p, mblocks, groups, (p.rows + groups - 1) / groups, (p.K + kIn - 1) / kIn, all, room);
+    const bool wide = wide_units(mats, g.tcap, room);
+    const int halves = wide ? 2 * kUnits : kUnits;
+    g.a_col = kTmemCols - halves * half_cols(mats);
+    g.bufs = sets_of(mats, g.tcap, wide);
+    g.stages = stages_of(mats, g.tcap, wide, room);
+    if (g.stages < least_stages(wide)) return cudaErrorNotSupported;
+    g.stage_bytes = stage_bytes(mats, g.tcap);
+    g.half_bytes = half_bytes(g.tcap);
+    const int smem = 1024 + g.stages * g.stage_bytes + halves * g.half_bytes + table;
     g.mblocks = mblocks;
     auto pairs_up = [](const void *q, long long ld) { return ((uintptr_t)q & 3u) == 0 && ld % 2 == 0; };
     g.paired = p.N % 2 == 0 && pairs_up(p.out, p.ldo) && (!p.residual || pairs_up(p.residual, p.ldr));
-    const int table = p.offsets ? p.E * (int)sizeof(Group) : 0;
-    const int room = d.smem.load(std::memory_order_relaxed) - 1024 - table;
-    // (whole stages for units may not fit beside the table of many groups. 256 tokens, 8 of 1024 experts,
-    // 768 -> 2048: 268 us with half stages, 993 in the kernel for few rows.)
-    int wide = wide_units(mats, g.tcap), halves;
-    for (;; --wide) {
-        halves = wide ? 2 * kUnits : kUnits;
-        g.stages = min(kMaxStages, (room - halves * g.half_bytes) / g.stage_bytes);
-        if (g.stages >= (wide ? 7 : 4)) break;  // (see the converters)
-        if (!wide) return cudaErrorNotSupported;
-    }
-    g.a_col = kTmemCols - halves * half_cols(mats);
-    const int smem = 1024 + g.stages * g.stage_bytes + halves * g.half_bytes + table;
     const long long most = ((p.rows + kStepRows - 1) / kStepRows + groups) * (long long)mblocks;  // >= the items
     // items are numbered in 32 bits, also where offsets that do not ascend give every
     // expert all rows
