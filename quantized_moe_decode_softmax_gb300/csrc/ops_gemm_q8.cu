@@ -34,7 +34,7 @@
 // 1850; the tensor pipe is busy 80 % of the second's cycles). Short tiles: the converters,
 // whose 5 operations for 4 codes share the integer pipe (62 % busy), and their waits for each other:
 // about 650 cycles per 128 inputs. A few hundred rows: 2.5 us before the first MMA, and the epilogue
-// (317x2032x4104 with GELU and a residual 13.1 us: 5 of them steps, 2.7 the epilogue). Few rows
+// (317x2032x4104 with GELU and a residual 12.8 us: 5 of them steps, 2.7 the epilogue). Few rows
 // per expert: HBM (64 tokens, 768 -> 2048, 128 experts: 38 us, 5.3 TB/s).
 //
 // Every wait is bounded (1 s, reported through moe_ops_check); after one gives
