@@ -10,9 +10,10 @@
 // there are rows enough to fill the SMs, so that an instruction serves four rows (8192 x 256,
 // top 6: 5.5 us, with a bias 8.9; a warp each 9.1 and 14). Lane i holds the V experts V i ..
 // V i + V - 1, which makes the lowest lane of a tie the lowest id. A key is its f32 as an
-// unsigned number that sorts alike (0: not available). The keys lie in shared memory and each
-// lane keeps the largest of its own, so that a rank is one maximum over the lanes, and another
-// over the V keys of the lane that had it, which the lanes read side by side.
+// unsigned number that sorts alike (0: not available). Each lane keeps the largest of its own, so
+// that a rank is one maximum over the lanes, and another over the V keys of the lane that had it:
+// by that lane in its registers, or, of many keys or rows, by all lanes side by side in shared
+// memory. One row of 128: 2.7 us, of which 1.4 an empty kernel would take.
 //
 // The ids are those of exact scores. Without a bias the order of c is the order of the
 // logits, and no score is computed for it. With a bias (or with sums of two per group)
@@ -164,7 +165,8 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key
     }
     const bool live = g < a.groups && m1 > none, stays = live && before < a.top_groups;
     F w = stays ? score : (F)INFINITY, b = live && !stays ? score : none;
-    for (int d = L / 2; d; d >>= 1) {
+    // (logits are exact)
+    for (int d = a.bias || a.top2 ? L / 2 : 0; d; d >>= 1) {
         const F ow = __shfl_xor_sync(kAll, w, d), ob = __shfl_xor_sync(kAll, b, d);
         w = ow < w ? ow : w;
         b = ob > b ? ob : b;
@@ -374,7 +376,8 @@ __host__ __device__ constexpr int warp_words(int L, int V, int E, bool f64) {
     return 32 / L * row_words(L, V) + (f64 ? (2 * E + 3) / 4 * 4 : 0);
 }
 
-template <int L, int V>
+// REGS: the lanes find the ranks in their registers, instead of by way of shared memory
+template <int L, int V, bool REGS>
 __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     extern __shared__ __align__(16) uint32_t words[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
@@ -491,11 +494,15 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         }
     }
     const float err = softmax ? kSoftmaxErr : kSigmoidErr;
+    static_assert(!REGS || L == 32, "a rank's owner is one lane of the warp");
+    auto store_keys = [&] {
 #pragma unroll
-    for (int j = 0; j < V / 4; ++j)
-        *reinterpret_cast<uint4 *>(mine + sub * (V + 4) + 4 * j) =
-            make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
-    __syncwarp();
+        for (int j = 0; j < V / 4; ++j)
+            *reinterpret_cast<uint4 *>(mine + sub * (V + 4) + 4 * j) =
+                make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
+        __syncwarp();
+    };
+    if (!REGS || a.groups > 1) store_keys();
 
     double *const f64 = reinterpret_cast<double *>(own + 32 / L * row_words(L, V));
     if (a.groups > 1) {
@@ -522,16 +529,12 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             }
         }
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < V / 4; ++j)
-            *reinterpret_cast<uint4 *>(mine + sub * (V + 4) + 4 * j) =
-                make_uint4(key[4 * j], key[4 * j + 1], key[4 * j + 2], key[4 * j + 3]);
-        __syncwarp();
+        if (!REGS) store_keys();
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) best = max(best, key[j]);
 
-    // The ranks: P keys of the owner to a lane
+    // The ranks. By way of shared memory: P keys of the owner to a lane
     constexpr int P = V > L ? V / L : 1;
     const int places = a.bias ? a.k + 1 : a.k;  // (with a bias one more, for its distance)
     bool unsure = false;
@@ -540,48 +543,74 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     for (int r0 = 0; r0 < places; r0 += L) {
         uint32_t held = 0u;  // the key of rank r0 + sub
         const int here = min(L, places - r0);
-        for (int i = 0; i < here; ++i) {
-            const uint32_t top = row_max<L>(best);
-            const int owner = __ffs(row_ballot<L>(best == top)) - 1;
-            uint32_t *theirs = mine + owner * (V + 4) + sub * P;
-            uint32_t k[P];
+        if constexpr (REGS) {
+            for (int i = 0; i < here; ++i) {
+                const uint32_t top = row_max<L>(best);
+                if (lane == __ffs(__ballot_sync(kAll, best == top)) - 1) {
+                    int at = V - 1;
+                    float z = l[V - 1];
 #pragma unroll
-            for (int q = 0; q < P; ++q) k[q] = 0u;
-            if (P > 1 || sub < V) {
-                if constexpr (P == 4) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(theirs);
-                    k[0] = w.x;
-                    k[1] = w.y;
-                    k[2] = w.z;
-                    k[3] = w.w;
-                } else if constexpr (P == 2) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(theirs);
-                    k[0] = w.x;
-                    k[1] = w.y;
-                } else {
-                    k[0] = theirs[0];
+                    for (int j = V - 2; j >= 0; --j)
+                        if (key[j] == top) {
+                            at = j;
+                            z = l[j];
+                        }
+                    best = 0u;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        key[j] = j == at ? 0u : key[j];
+                        best = max(best, key[j]);
+                    }
+                    ranks[r0 + i] = top ? e0 + at : -1;  // (-1: none left)
+                    weights[r0 + i] = top ? z : -INFINITY;
                 }
+                if (lane == i) held = top;
+                __syncwarp();
             }
-            int at = P;
+        } else {
+            for (int i = 0; i < here; ++i) {
+                const uint32_t top = row_max<L>(best);
+                const int owner = __ffs(row_ballot<L>(best == top)) - 1;
+                uint32_t *theirs = mine + owner * (V + 4) + sub * P;
+                uint32_t k[P];
 #pragma unroll
-            for (int q = P - 1; q >= 0; --q)
-                if (k[q] == top) at = q;
-            const int first = __ffs(row_ballot<L>(at < P && top)) - 1;  // (-1: none left)
-            if (sub == first) {
+                for (int q = 0; q < P; ++q) k[q] = 0u;
+                if (P > 1 || sub < V) {
+                    if constexpr (P == 4) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(theirs);
+                        k[0] = w.x;
+                        k[1] = w.y;
+                        k[2] = w.z;
+                        k[3] = w.w;
+                    } else if constexpr (P == 2) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(theirs);
+                        k[0] = w.x;
+                        k[1] = w.y;
+                    } else {
+                        k[0] = theirs[0];
+                    }
+                }
+                int at = P;
 #pragma unroll
-                for (int q = 0; q < P; ++q)
-                    if (q == at) k[q] = 0u;
-                theirs[at] = 0u;
-                ranks[r0 + i] = owner * V + sub * P + at;
+                for (int q = P - 1; q >= 0; --q)
+                    if (k[q] == top) at = q;
+                const int first = __ffs(row_ballot<L>(at < P && top)) - 1;  // (-1: none left)
+                if (sub == first) {
+#pragma unroll
+                    for (int q = 0; q < P; ++q)
+                        if (q == at) k[q] = 0u;
+                    theirs[at] = 0u;
+                    ranks[r0 + i] = owner * V + sub * P + at;
+                }
+                if (first < 0 && sub == 0) ranks[r0 + i] = -1;
+                uint32_t rest = k[0];
+#pragma unroll
+                for (int q = 1; q < P; ++q) rest = max(rest, k[q]);
+                rest = row_max<L>(rest);
+                if (sub == owner) best = rest;
+                if (sub == i) held = top;
+                __syncwarp();
             }
-            if (first < 0 && sub == 0) ranks[r0 + i] = -1;
-            uint32_t rest = k[0];
-#pragma unroll
-            for (int q = 1; q < P; ++q) rest = max(rest, k[q]);
-            rest = row_max<L>(rest);
-            if (sub == owner) best = rest;
-            if (sub == i) held = top;
-            __syncwarp();
         }
         if (a.bias) {
             const bool has = held != 0u;
@@ -605,6 +634,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         }
     }
     // rows to be ranked again, one after another by the whole warp
+    if (REGS && unsure) store_keys();
     for (unsigned flagged = __ballot_sync(kAll, sub == 0 && unsure); flagged; flagged &= flagged - 1) {
         const int at = __ffs(flagged) - 1;
         const float f = -row_max<L>(-from);  // the lanes of the row have theirs
@@ -618,7 +648,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     float top = -INFINITY;
     for (int r = sub; r < a.k; r += L) {
         const int id = ranks[r];
-        const float z = live && id >= 0 ? logit(a, row, id) : -INFINITY;
+        const float z = REGS && !unsure ? weights[r] : live && id >= 0 ? logit(a, row, id) : -INFINITY;
         weights[r] = z;
         top = fmaxf(top, z);
     }
@@ -645,7 +675,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     }
 }
 
-template <int L, int V>
+template <int L, int V, bool REGS = false>
 cudaError_t launch(RouteArgs a, cudaStream_t st) {
     const int esz = a.dtype == MOE_DTYPE_F32 ? 4 : 2;
     const unsigned piece = min(16, V * esz);  // bytes of a load
@@ -655,7 +685,7 @@ cudaError_t launch(RouteArgs a, cudaStream_t st) {
     // lane, of 8 sectors each (8192 x 256: 8.9 us, 9.8 from there)
     const int shared = L < 32 && a.bias ? L * (V + 4) : 0;
     const int warps = min(4, (12 * 1024 - shared) / a.words), rows = warps * (32 / L);
-    return launch_overlapped(route_kernel<L, V>, dim3((unsigned)((a.n + rows - 1) / rows)), 32 * warps,
+    return launch_overlapped(route_kernel<L, V, REGS>, dim3((unsigned)((a.n + rows - 1) / rows)), 32 * warps,
                              4 * (shared + warps * a.words), 1, st, a);
 }
 
@@ -667,8 +697,11 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t st) {
         if (a.E <= 128) return launch<8, 16>(a, st);
         return launch<8, 32>(a, st);
     }
-    if (a.E <= 128) return launch<32, 4>(a, st);
-    if (a.E <= 256) return launch<32, 8>(a, st);
+    // in registers a rank is found sooner, and takes more instructions the more keys a lane has (us,
+    // registers / shared memory: 64 rows of 128 2.8 / 3.2, 4095 5.7 / 5.9; of 256 3.0 / 3.2 and 7.4 / 5.7,
+    // 600 rows 3.2 / 3.4, 1200 3.8 / 3.7)
+    if (a.E <= 128) return launch<32, 4, true>(a, st);
+    if (a.E <= 256) return a.n <= 800 ? launch<32, 8, true>(a, st) : launch<32, 8>(a, st);
     if (a.E <= 512) return launch<32, 16>(a, st);
     return launch<32, 32>(a, st);
 }
