@@ -17,10 +17,13 @@
 //
 // The ids are those of exact scores. Without a bias the order of c is the order of the
 // logits, and no score is computed for it. With a bias (or with sums of two per group)
-// c is computed in f32, the ranks are taken to top_k + 1 places, and wherever two
-// neighbours are nearer to each other than the f32 errors (below), the row is ranked
-// again, over the experts that can still be among the first: in pairs of f32 or in f64. For
-// trained routers that is one row in some thousands.
+// c is computed in f32, and the ranks are taken to top_k + 1 places. Neighbours among the
+// first top_k that are farther apart than the f32 errors (below), or tie exactly, stand in
+// their exact order, and so do all of these by the chain of them. At the cut there is no chain: an
+// expert far down may be off by more than the next one. So where the first expert left out is
+// within the errors of the last one chosen, all that are left out and as near are compared with it. A row
+// with a pair that this does not settle is ranked again, over the experts that can still be among
+// the first: in pairs of f32 or in f64. For trained routers that is one row in some thousands.
 #include "ops_common.cuh"
 #include "ptx.cuh"
 
@@ -75,6 +78,16 @@ __device__ __forceinline__ double sigmoid(double l) {
 
 // l - m with m >= l, where infinities of both are equal
 __device__ __forceinline__ float below(float l, float m) { return l == m ? 0.f : l - m; }
+
+// Whether keys c1 >= c2 of experts with these logits and biases may be in the wrong order: they are
+// nearer than the errors of both (`near`, at the most), and no exact tie, which goes to the lower id.
+__device__ __forceinline__ bool may_swap(bool softmax, float c1, float l1, float b1, float c2, float l2, float b2, float near) {
+    if (c1 - c2 > near || (l1 == l2 && b1 == b2)) return false;
+    if (!softmax) return true;
+    // by the errors of these two scores, which are c - bias (317 x 256: 5 us, 11 with kSoftmaxErr)
+    const float rounding = 0x1p-22f * (fabsf(c1) + fabsf(c2)), p = fmaxf(c1 - b1, c2 - b2) + rounding;
+    return !(c1 - c2 > 2.f * (kSoftmaxErr * p + 0x1p-23f * sqrtf(p)) + rounding);
+}
 
 // over the L lanes of a row
 template <int L> __device__ __forceinline__ float row_max(float v) {
@@ -536,8 +549,9 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 
     // The ranks. By way of shared memory: P keys of the owner to a lane
     constexpr int P = V > L ? V / L : 1;
-    const int places = a.bias ? a.k + 1 : a.k;  // (with a bias one more, for its distance)
+    const int places = a.bias ? a.k + 1 : a.k;  // (with a bias one more: the first that is left out)
     bool unsure = false;
+    uint32_t chosen = 0u, left_out = 0u;  // of the row: the keys of the last two places
     float last = 0.f, from = INFINITY;  // of the row: the key of the last rank; the least of them, less the errors
     int ranked = 0;
     for (int r0 = 0; r0 < places; r0 += L) {
@@ -546,6 +560,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         if constexpr (REGS) {
             for (int i = 0; i < here; ++i) {
                 const uint32_t top = row_max<L>(best);
+                chosen = left_out;
+                left_out = top;
                 if (lane == __ffs(__ballot_sync(kAll, best == top)) - 1) {
                     int at = V - 1;
                     float z = l[V - 1];
@@ -570,6 +586,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         } else {
             for (int i = 0; i < here; ++i) {
                 const uint32_t top = row_max<L>(best);
+                chosen = left_out;
+                left_out = top;
                 const int owner = __ffs(row_ballot<L>(best == top)) - 1;
                 uint32_t *theirs = mine + owner * (V + 4) + sub * P;
                 uint32_t k[P];
@@ -617,21 +635,34 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             const float c = has ? unsortable(held) : 0.f, up = __shfl_up_sync(kAll, c, 1, L), before = sub ? up : last;
             const float near = 2.f * (err + 0x1p-23f * (fabsf(c) + (r0 + sub ? fabsf(before) : 0.f)));
             bool close = has && r0 + sub > 0 && !(before - c > near);
-            if (close) {  // the same logit and the same bias are an exact tie
+            if (close) {
                 const int i = ranks[r0 + sub], j = ranks[r0 + sub - 1];
-                const float bi = a.bias[i], bj = a.bias[j];
-                close = logit(a, row, i) != logit(a, row, j) || bi != bj;
-                // by the errors of these two scores, which are c - bias (317 x 256: 5 us, 11 with kSoftmaxErr)
-                if (softmax) {
-                    const float rounding = 0x1p-22f * (fabsf(c) + fabsf(before)), p = fmaxf(c - bi, before - bj) + rounding;
-                    close = close && !(before - c > 2.f * (kSoftmaxErr * p + 0x1p-23f * sqrtf(p)) + rounding);
-                }
+                close = may_swap(softmax, before, logit(a, row, j), a.bias[j], c, logit(a, row, i), a.bias[i], near);
             }
             unsure |= row_ballot<L>(close) != 0u;  // (every lane votes, whatever its row has found)
             from = fminf(from, has ? (c == INFINITY ? 3.0e38f : c - 2.f * near) : INFINITY);
             last = __shfl_sync(kAll, c, L - 1, L);
             ranked += __popc(row_ballot<L>(has));
         }
+    }
+    // the cut: the others that are left out (the first of them, by key, has been compared)
+    if (a.bias) {
+        const float in = key_value(chosen);
+        const float near = 2.f * (err + 0x1p-23f * (fabsf(in) + fabsf(key_value(left_out))));
+        const bool others = best && !unsure && !(in - unsortable(best) > near);  // (best: of the lane's keys)
+        bool close = false;
+        if (REGS && __any_sync(kAll, others)) store_keys();
+        if (others) {
+#pragma unroll 1
+            for (int j = 0; j < V && !close; ++j) {
+                const uint32_t k = mine[sub * (V + 4) + j];
+                if (k && !(in - unsortable(k) > near)) {
+                    const int i = ranks[a.k - 1], e = e0 + j;
+                    close = may_swap(softmax, in, logit(a, row, i), a.bias[i], unsortable(k), logit(a, row, e), a.bias[e], near);
+                }
+            }
+        }
+        unsure |= row_ballot<L>(close) != 0u;
     }
     // rows to be ranked again, one after another by the whole warp
     if (REGS && unsure) store_keys();

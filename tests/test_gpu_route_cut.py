@@ -1,0 +1,97 @@
+"""moe_route with a bias where the last place is a matter of roundings: what is behind the
+cut may belong before it."""
+import math
+
+import pytest
+import torch
+
+import quantized_moe_decode_softmax_gb300 as q
+import route_reference as ref
+from test_gpu_route import both
+
+pytestmark = pytest.mark.gpu
+
+F32, F64 = torch.float32, torch.float64
+
+
+def row(*values):
+    return torch.tensor([values], dtype=F32).cuda()
+
+
+@pytest.mark.parametrize("z,b,want", [
+    ([0.0, 0.0, 0.0], [0.0, 0.0, 2.0 ** -26], 2),
+    ([0.0, 0.0, 0.0], [0.1, 0.1, math.nextafter(float(torch.tensor(0.1)), 1) + 2.0 ** -27], 2),
+    ([20.0, 20.0, 21.0], [0.0, 0.0, 0.0], 2),
+    ([21.0, 21.0, 20.0], [0.0, 0.0, 0.0], 0),
+    ([20.0, 20.0, 21.0, 21.0, 20.5], [0.0] * 5, 2),
+], ids=["bias", "next bias", "saturated", "settled", "two ties"])
+def test_an_expert_behind_a_tie_at_the_cut(z, b, want):
+    """Keys alike in f32: two experts tie exactly, one behind them is larger."""
+    r = both(row(*z), 1, score="sigmoid", bias=row(*b)[0])
+    assert r.topk_idx.tolist() == [[want]]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [7, 40, 128, 200, 256, 300, 1000])
+def test_experts_behind_many_ties(E, score):
+    """More exact ties than places, at any ids, and one or two experts that are larger by less than
+    an f32 step of a key; the cut before, among and behind the ties; few rows and many."""
+    for seed in range(3):
+        g = torch.Generator().manual_seed(10 * E + seed)
+        order = torch.randperm(E, generator=g)
+        tied, larger = order[:E // 2 + 1], order[-2:]
+        z = torch.full((E,), -1.0)
+        b = torch.full((E,), 0.5)
+        z[tied] = 18.0 if score == "sigmoid" else 1.0
+        z[larger] = 18.5 if score == "sigmoid" else 1.0 + 2.0 ** -23
+        z[order[E // 2 + 1:-2]] += torch.rand(E - E // 2 - 3, generator=g)
+        for k in sorted({1, 2, 3, E // 2, min(64, E // 2 + 2)}):
+            both(z[None].cuda(), min(k, 64), score=score, bias=b.cuda(), renormalize=seed % 2 == 0)
+    both(z[None].repeat(900, 1).cuda(), 2, score=score, bias=b.cuda())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_saturated_16_bit_logits_with_a_bias_of_zeros(dtype):
+    """A bias that training has not moved yet, and logits of few different values."""
+    g = torch.Generator().manual_seed(3)
+    z = (16.0 + torch.randint(0, 8, (60, 64), generator=g) / 8).to(dtype).cuda()
+    for k in (1, 2, 6):
+        both(z, k, score="sigmoid", bias=torch.zeros(64, device="cuda"))
+        both(z, k, score="sigmoid", bias=torch.zeros(64, device="cuda"), groups=8, top_groups=3)
+
+
+def test_a_large_score_behind_the_cut():
+    """Softmax: two small scores, whose own errors tell them apart, and a large one with a bias that
+    brings it next to them."""
+    z = row(-13.8, -13.9, -9.0, -9.0, -9.0, -0.37806016, -10.0, 0.0)
+    b = row(0.0, 0.0, -2.0, -2.0, -2.0, -0.4064935, -2.0, -2.0)[0]
+    assert both(z, 1, bias=b).topk_idx.tolist() == [[5]]
+
+
+def cancelled(E, n, seed):
+    """Rows of E logits and a bias: expert `big` has a score of about 0.85 and a bias that leaves
+    about 3e-6 of it; experts 3 and 4 have such scores, 1e-8 to 6e-8 apart; the others are far below."""
+    g = torch.Generator().manual_seed(seed)
+    big = E - 2
+    bias = torch.full((E,), -2.0, dtype=F64)
+    bias[big] = -0.84
+    bias[3] = bias[4] = 0.0
+    bias = bias.to(F32)
+    u = torch.rand((n, 3), generator=g, dtype=F64)
+    small = 3e-6 + 1e-6 * u[:, 0]
+    next_small = small - (1e-8 + 5e-8 * u[:, 1])
+    p = -float(bias[big]) + small + 2e-7 * (2 * u[:, 2] - 1)
+    z = torch.log((1 - p - small - next_small) / (E - 3))[:, None].repeat(1, E)
+    z[:, 3], z[:, 4], z[:, big] = torch.log(small), torch.log(next_small), torch.log(p)
+    return z.to(F32).cuda(), bias.cuda()
+
+
+@pytest.mark.parametrize("E", [40, 64, 250, 500])
+def test_rows_with_a_large_score_behind_the_cut(E):
+    z, b = cancelled(E, 1500, E)
+    both(z[:60].contiguous(), 1, bias=b)
+    both(z[:700].contiguous(), 1, bias=b)
+    both(z, 1, bias=b)
+    z, b = cancelled(E, 4200, E + 1)
+    both(z, 1, bias=b)
+    both(z[:, :].contiguous(), 2, bias=b)
