@@ -129,12 +129,13 @@ __device__ __forceinline__ double key_value(double k) { return k; }
 
 // Which groups stay, as a mask of bits, by the keys of all experts (f32 as sortable numbers, or
 // f64 with -inf for those not available), by the L lanes of a row; at most L groups, L / 2^ceil(log2
-// groups) lanes share one. F: the precision. *gap: the distance of the worst group that stays from
-// the best that does not (inf if there are not both). logits: the keys are logits, and a sum of
+// groups) lanes share one. F: the precision. *settled (f32): whether every group that stays is ahead of
+// all that do not by more than their errors; err is a score's, and what rounds in a sum of two goes
+// by the size of its terms, which may cancel. logits: the keys are logits, and a sum of
 // two is one of their scores. cut, unless null: for each group the least key that its score has.
 template <int L, typename F, typename K>
-__device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key, float max_logit, bool logits, F *gap,
-                                                F *worst, float *cut) {
+__device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key, float max_logit, bool logits, float err,
+                                                bool *settled, float *cut) {
     const int lane = threadIdx.x & (L - 1), size = a.E / a.groups;
     int per = L;  // lanes per group
     while (L / per < a.groups) per >>= 1;
@@ -155,7 +156,7 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key
         m2 = lo > m2 ? lo : m2;
     }
     if (cut && g < a.groups && lane % per == 0) cut[g] = (float)(a.top2 && m2 > none ? m2 : m1);
-    F score = m1;
+    F score = m1, size_of = m1 < 0 ? -m1 : m1;  // size_of: of the terms
     if (a.top2) {
         if (logits && m1 > none) {
             // (of a softmax without its common divisor)
@@ -166,9 +167,10 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key
                 else
                     return a.score == MOE_SCORE_SOFTMAX ? (v == (F)max_logit ? 1.0 : exp(v - (F)max_logit)) : sigmoid(v);
             };
-            score = s(m1) + s(m2);
+            score = size_of = s(m1) + s(m2);
         } else if (m2 > none) {
             score = m1 + m2;
+            size_of += m2 < 0 ? -m2 : m2;
         }
     }
     int before = 0;
@@ -177,15 +179,20 @@ __device__ __forceinline__ unsigned best_groups(const RouteArgs &a, const K &key
         before += s > score || (s == score && o < g);
     }
     const bool live = g < a.groups && m1 > none, stays = live && before < a.top_groups;
-    F w = stays ? score : (F)INFINITY, b = live && !stays ? score : none;
-    // (logits are exact)
-    for (int d = a.bias || a.top2 ? L / 2 : 0; d; d >>= 1) {
-        const F ow = __shfl_xor_sync(kAll, w, d), ob = __shfl_xor_sync(kAll, b, d);
-        w = ow < w ? ow : w;
-        b = ob > b ? ob : b;
+    if constexpr (sizeof(F) == 4) {
+        // (without a bias the best one is a logit, which is exact)
+        if (a.bias || a.top2) {
+            const float by = 2.f * err + 0x1p-22f * size_of;
+            float w = !stays ? INFINITY : by < INFINITY ? score - by : -INFINITY;
+            float b = !live || stays ? -INFINITY : by < INFINITY ? score + by : INFINITY;
+#pragma unroll
+            for (int d = L / 2; d; d >>= 1) {
+                w = fminf(w, __shfl_xor_sync(kAll, w, d));
+                b = fmaxf(b, __shfl_xor_sync(kAll, b, d));
+            }
+            *settled = w > b;
+        }
     }
-    *gap = w == (F)INFINITY || b == none ? (F)INFINITY : w - b;
-    *worst = w;
     // bit o: group o's lanes, the first of each
     const unsigned lanes = row_ballot<L>(stays);
     unsigned mask = 0;
@@ -245,8 +252,7 @@ __device__ __noinline__ unsigned groups_exactly(const RouteArgs &a, long long ro
     });
     for (int i = lane; i < found; i += 32) key[list[i]] = exact_key(a, row, (int)list[i], max_logit, sum);
     __syncwarp();
-    double gap, worst;
-    return best_groups<32, double>(a, key, max_logit, !a.bias, &gap, &worst, nullptr);
+    return best_groups<32, double>(a, key, max_logit, !a.bias, 0.f, nullptr, nullptr);
 }
 
 // A number as the sum of two f32, the second at most half a last place of the first
@@ -519,10 +525,9 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 
     double *const f64 = reinterpret_cast<double *>(own + 32 / L * row_words(L, V));
     if (a.groups > 1) {
-        float gap, worst;
-        unsigned groups = best_groups<L, float>(a, keys, m, !a.bias, &gap, &worst, weights);
-        // errors of two sums of one or two keys
-        const bool unsure = live && (a.bias || a.top2) && !(gap > 2.f * (2.f * err + 0x1p-22f * fabsf(worst)));
+        bool settled = true;
+        unsigned groups = best_groups<L, float>(a, keys, m, !a.bias, err, &settled, weights);
+        const bool unsure = live && !settled;
         __syncwarp();
         for (unsigned flagged = __ballot_sync(kAll, sub == 0 && unsure); flagged; flagged &= flagged - 1) {
             const int at = __ffs(flagged) - 1;
