@@ -703,6 +703,10 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     if (a.renormalize) {
         sum = row_sum<L>(sum);
         by = sum > 0.f ? a.scale / sum : 0.f;
+        if (fabsf(by) == INFINITY) {  // (a scale near the largest f32: a weight alone is no larger than it)
+            for (int r = sub; r < a.k; r += L) weights[r] /= sum;
+            by = a.scale;
+        }
     }
     if (!live) return;
     for (int r = sub; r < a.k; r += L) {
