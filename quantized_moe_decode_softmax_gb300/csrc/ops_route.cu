@@ -389,8 +389,10 @@ __device__ __noinline__ void rank_exactly(const RouteArgs &a, long long row, flo
     }
 }
 
-// shared memory of a warp in 4-byte words: its rows' keys, ranks and weights; E doubles
-__host__ __device__ constexpr int row_words(int L, int V) { return L * (V + 4) + kMaxK + 4 + kMaxK; }
+// shared memory of a warp in 4-byte words: its rows' keys, ranks and weights, of one place more than a row
+// has (the first that is left out) in multiples of 16 bytes; E doubles
+constexpr int kPlaces = kMaxK + 4;
+__host__ __device__ constexpr int row_words(int L, int V) { return L * (V + 4) + 2 * kPlaces; }
 __host__ __device__ constexpr int warp_words(int L, int V, int E, bool f64) {
     return 32 / L * row_words(L, V) + (f64 ? (2 * E + 3) / 4 * 4 : 0);
 }
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
     uint32_t *mine = own + lane / L * row_words(L, V);
     const Keys<V> keys{mine};
     int *ranks = reinterpret_cast<int *>(mine + L * (V + 4));
-    float *weights = reinterpret_cast<float *>(mine + L * (V + 4) + kMaxK + 4);
+    float *weights = reinterpret_cast<float *>(mine + L * (V + 4) + kPlaces);
     const int e0 = sub * V;
 
     // the logits, and the largest of them that takes part
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
             const int at = __ffs(flagged) - 1;
             uint32_t *words_of = own + at / L * row_words(L, V);
             const unsigned g = groups_exactly<V>(a, first_row + at / L, err, __shfl_sync(kAll, m, at),
-                                                 reinterpret_cast<float *>(words_of + L * (V + 4) + kMaxK + 4), f64, words_of);
+                                                 reinterpret_cast<float *>(words_of + L * (V + 4) + kPlaces), f64, words_of);
             if (lane / L == at / L) groups = g;
         }
         const int size = a.E / a.groups;

@@ -94,4 +94,17 @@ def test_rows_with_a_large_score_behind_the_cut(E):
     both(z, 1, bias=b)
     z, b = cancelled(E, 4200, E + 1)
     both(z, 1, bias=b)
-    both(z[:, :].contiguous(), 2, bias=b)
+    both(z, 2, bias=b)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 65, 128, 129, 256])
+def test_64_places_and_the_one_left_out(E, score):
+    """The most places, by lanes that rank in their registers (few rows) and in shared memory."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    z = 2 * torch.randn((70, E), generator=g, device="cuda")
+    b = 0.2 * torch.randn(E, generator=g, device="cuda")
+    for rows in (z[:9], z):
+        both(rows, 64, score=score, bias=b)
+    if E % 8 == 0:
+        both(z[:9], 64 if E > 64 else 32, score=score, bias=b, groups=8, top_groups=4 + (E == 64), group_score="top2")
