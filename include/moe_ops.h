@@ -229,8 +229,9 @@ typedef struct {
  * multiple of 16), 16-byte aligned, and x_scale holds a scale for each row of x. All
  * else, limits and errors included, is as there. The sum of products is exact up to
  * 2^24 in magnitude (whatever the codes for K <= 1024) and otherwise an f32 sum, and is
- * scaled, activated and rounded once. An infinite or NaN scale reaches its own row or
- * column only. UNSUPPORTED: K not a multiple of 16. */
+ * scaled (by a weight's scale first: with scales of W up to 2^97 nothing overflows that the row's
+ * scale brings back into range), activated and rounded once. An infinite or NaN scale reaches its
+ * own row or column only. UNSUPPORTED: K not a multiple of 16. */
 moe_status moe_linear_q8(const moe_product_q8 *p, const int8_t *x, int64_t ldx, const float *x_scale, int n,
                          const void *residual, int64_t ldr, void *out, int64_t ldo, void *stream);
 moe_status moe_grouped_linear_q8(const moe_product_q8 *p, const int32_t *offsets, const int32_t *row_token,

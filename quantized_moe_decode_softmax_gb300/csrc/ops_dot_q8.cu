@@ -16,6 +16,7 @@
 // find the weights in L2. 2048x2048, one row 3.1 us, 8192x4096 7.4 (4.5 TB/s); 8 of 128 experts,
 // gated 2048 -> 768, one row each 6.6 (25 MB); 64 rows of 512x4096 5.5.
 #include "ops_common.cuh"
+#include "ops_q8.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_dot_q8_kernel(const Pr
         float v[MATS];
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
-            v[m] = (float)sum[m] * sx * (m ? p.w_up_scale : p.w_scale)[(size_t)e * p.N + c];
+            v[m] = scaled((float)sum[m], (m ? p.w_up_scale : p.w_scale)[(size_t)e * p.N + c], sx);
             const T *bias = static_cast<const T *>(m ? p.bias_up : p.bias);
             if (bias) v[m] += to_f32(bias[(size_t)e * p.N + c]);
         }

@@ -394,6 +394,7 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
             tmem_wait_ld();
             if (t0 + 32 >= it.rows) done_reading();
             if constexpr (SCALED) {
+                // the column's scale first, as in scaled() of ops_q8.cuh
                 const float4 *s = reinterpret_cast<const float4 *>(row_scale + ((t0 - 16 * part) >> 1));
 #pragma unroll
                 for (int j = 0; j < W / 4; ++j) {
@@ -401,8 +402,8 @@ __device__ __forceinline__ void store_tiles(const Product &p, const Tiles &g, It
                     const float by[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        v[4 * j + i] = fmaf(v[4 * j + i] * by[i], s0, b0);
-                        if constexpr (MATS == 2) u[4 * j + i] = fmaf(u[4 * j + i] * by[i], s1, b1);
+                        v[4 * j + i] = fmaf(v[4 * j + i] * s0, by[i], b0);
+                        if constexpr (MATS == 2) u[4 * j + i] = fmaf(u[4 * j + i] * s1, by[i], b1);
                     }
                 }
             } else {

@@ -20,6 +20,12 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t q) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&l), *reinterpret_cast<const uint32_t *>(&h));
 }
 
+// A sum of products of codes, scaled. The sum is 0 or between 1 and 2^30 (K <= 65536), so that its product
+// with a weight's scale loses nothing to underflow, and stays finite up to scales of 2^97. In the
+// other order a row's scale (up to 2^121 from bf16 values) could make it infinite before a weight's
+// brings it back.
+__device__ __forceinline__ float scaled(float sum, float w_scale, float x_scale) { return sum * w_scale * x_scale; }
+
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 }  // namespace ops

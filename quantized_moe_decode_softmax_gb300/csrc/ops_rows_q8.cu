@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps, min_ctas(MATS, TB, AHEAD)) produc
                     v[m] = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) v[m] += part[w][m][i / kCols][i % kCols];
-                    v[m] = v[m] * sx * (m ? p.w_up_scale : p.w_scale)[(size_t)e * p.N + c];
+                    v[m] = scaled(v[m], (m ? p.w_up_scale : p.w_scale)[(size_t)e * p.N + c], sx);
                     const T *bias = static_cast<const T *>(m ? p.bias_up : p.bias);
                     if (bias) v[m] += to_f32(bias[(size_t)e * p.N + c]);
                 }
