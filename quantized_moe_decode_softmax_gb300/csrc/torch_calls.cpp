@@ -5,12 +5,13 @@
 // the interpreter asking each tensor for its properties and allocating the output.
 // Here the same checks and the allocation are C++ (host time of a one-token linear on
 // a Grace core: 2.9 us, 11 through ctypes). Whatever is not the usual call (another device
-// or stream, a tensor subclass, an input that asks for a gradient, any argument that does
-// not fit) returns None, and ops.py goes on from there with its own checks and messages.
+// or stream, a tensor subclass, an input that asks for a gradient, outputs that torch would
+// fill, any argument that does not fit) returns None, and ops.py goes on from there with its own checks and messages.
 // Compiled against the installed torch, without the CUDA library: ops.py passes in
 // the addresses of its entry points.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -72,6 +73,13 @@ PyObject *result(moe_status st, const at::Tensor &out, PyObject *given) {
         return given;
     }
     return THPVariable_Wrap(out);
+}
+
+// Whether torch fills new memory (torch.use_deterministic_algorithms): torch.empty does, what is
+// below does not, and such a call is not the usual one.
+bool fills() {
+    const at::Context &c = at::globalContext();
+    return c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory();
 }
 
 // Memory on the current device for an output, from torch's allocator, and a tensor of `type`
@@ -162,6 +170,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || n > INT32_MAX || (res && !rows(*res, n, p->N, dt, dev, &ldr)) ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
+    if (!given && fills()) return other();
     const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st = fn_linear(p, x->const_data_ptr(), ldx, (int)n, res ? res->const_data_ptr() : nullptr, ldr,
                                     out.mutable_data_ptr(), ldo, c10::cuda::getCurrentCUDAStream(dev).stream());
@@ -189,6 +198,7 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || x_rows == 0 || n > INT32_MAX || x_rows > INT32_MAX ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
+    if (!given && fills()) return other();
     const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st = fn_grouped(p, off->const_data_ptr<int32_t>(), token ? token->const_data_ptr<int32_t>() : nullptr,
                                      x->const_data_ptr(), ldx, (int)x_rows, (int)n, out.mutable_data_ptr(), ldo,
@@ -213,6 +223,7 @@ PyObject *slots(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         hi < 0 || hi > E || !idx->is_cuda() || !dense(*idx, at::kInt, idx->get_device()) ||
         c10::cuda::current_device() != idx->get_device())
         return other();
+    if (fills()) return other();
     const int64_t S = idx->numel();
     // one allocation, and four tensors on its storage, each with the values that it alone covers
     const c10::Storage all = memory(4 * (3 * S + E + 1));
@@ -251,6 +262,7 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         (res && !rows(*res, n, N, dt, dev, &ldr)) || (given && !rows(*given, n, N, dt, dev, &ldo)) ||
         c10::cuda::current_device() != dev)
         return other();
+    if (!given && fills()) return other();
     const at::Tensor out = given ? *given : empty(n, N, dt);
     const moe_status st = fn_combine(dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16, y->const_data_ptr(), ldy, (int)r,
                                      of->const_data_ptr<int32_t>(), w->const_data_ptr<float>(), (int)n, (int)k, (int)N,
@@ -291,6 +303,7 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if ((dt != at::kBFloat16 && dt != at::kHalf && dt != at::kFloat) || !rows(*l, -1, r->E, dt, dev, &ldl) || n == 0 ||
         n > INT32_MAX || k < 1 || k > 1024 || c10::cuda::current_device() != dev)
         return other();
+    if (fills()) return other();
     const c10::Storage all = memory(8 * n * k);
     const at::Tensor idx = part_of(all, at::kInt, 0, {n, k}), w = part_of(all, at::kFloat, 4 * n * k, {n, k});
     const moe_status st = fn_route(r, dt == at::kFloat ? MOE_DTYPE_F32 : dt == at::kHalf ? MOE_DTYPE_F16 : MOE_DTYPE_BF16,
@@ -312,6 +325,7 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if ((dt != at::kBFloat16 && dt != at::kHalf) || n == 0 || K == 0 || n > INT32_MAX || K > INT32_MAX ||
         !rows(*x, -1, K, dt, dev, &ldx) || c10::cuda::current_device() != dev)
         return other();
+    if (fills()) return other();
     const int64_t at_scale = (n * K + 15) / 16 * 16;
     const c10::Storage all = memory(at_scale + 4 * n);
     const at::Tensor codes = part_of(all, at::kChar, 0, {n, K}), scale = part_of(all, at::kFloat, at_scale, {n});
@@ -344,6 +358,7 @@ PyObject *linear_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || n > INT32_MAX || (res && !rows(*res, n, p->N, dt, dev, &ldr)) ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
+    if (!given && fills()) return other();
     const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st =
         fn_linear_q8(p, x->const_data_ptr<int8_t>(), ldx, scale->const_data_ptr<float>(), (int)n,
@@ -373,6 +388,7 @@ PyObject *grouped_q8(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (n == 0 || x_rows == 0 || n > INT32_MAX || x_rows > INT32_MAX ||
         (given && !rows(*given, n, p->N, dt, dev, &ldo)) || c10::cuda::current_device() != dev)
         return other();
+    if (!given && fills()) return other();
     const at::Tensor out = given ? *given : empty(n, p->N, dt);
     const moe_status st = fn_grouped_q8(
         p, off->const_data_ptr<int32_t>(), token ? token->const_data_ptr<int32_t>() : nullptr,
