@@ -144,6 +144,8 @@ class SharedExpert:
 
     def __init__(self, gate, up, down, activation: str = "silu", act_limit: float = 0.0):
         self._set(LinearWeights(gate, w_up=up, activation=activation, act_limit=act_limit), LinearWeights(down))
+        if self.gate_up.dtype != self.down.dtype:
+            raise TypeError(f"gate is {self.gate_up.dtype}, down is {self.down.dtype}")
 
     def _set(self, gate_up, down):
         if gate_up.grouped or down.grouped or (down.N, down.K) != (gate_up.K, gate_up.N):
@@ -154,6 +156,11 @@ class SharedExpert:
         """Raise for a step `width` wide on x that this expert cannot run beside."""
         if self.down.N != width:
             raise ValueError(f"the shared expert is {self.down.N} wide, the step {width}")
+        for w in (self.gate_up, self.down):
+            if w.status:
+                raise _abi.MoeError(w.status, "the shared expert's weights are refused")
+            if w.device_index != x.get_device():
+                raise ValueError(f"the shared expert is on {w.device}, x is on {x.device}")
         _no_grad(x, out, *self.gate_up.tensors, *self.down.tensors)
 
     def forward(self, x, residual=None, out=None, stream=None):

@@ -202,6 +202,11 @@ class _Described:
         # in one piece and in place: a call of another thread has read `ref`, or copies `c`
         (ctypes.c_char * ctypes.sizeof(c)).from_buffer(self.c).raw = bytes(c)
         self._bound = layout
+        self.status = self._asked(c)
+
+    def _asked(self, c) -> int:
+        """The status with which every call on the struct is refused, MOE_OK if none is."""
+        return _abi.MOE_OK
 
     def _addresses(self):
         """The tensors' addresses (None for none)."""
@@ -258,6 +263,13 @@ class LinearWeights(_Described):
         return moe_product(_dtype_code(w.dtype), self.E, self.N, self.K, at, at_up,
                            w.stride(-2) if self.N > 1 else self.K,
                            w.stride(0) if self.grouped and self.E > 1 else 0, at_bias, at_bias_up, *self._epilogue)
+
+    def _asked(self, c):
+        # a call on no rows, which the entry point checks and does not launch (the numbers stand in for addresses)
+        at, ldx = ctypes.addressof(c), (self.K + 15) // 16 * 16
+        if self.grouped:
+            return _c.moe_grouped_linear(at, 16, None, 32, ldx, 0, 0, 48, self.N, None)
+        return _c.moe_linear(at, 32, ldx, 0, None, 0, 48, self.N, None)
 
 
 def _check_weights(w, w_up, rows, dtype, biases):
@@ -330,6 +342,12 @@ class LinearWeightsQ8(_Described):
                               w.stride(-2) if self.N > 1 else self.K,
                               w.stride(0) if self.grouped and self.E > 1 else 0, at_scale, at_scale_up, at_bias,
                               at_bias_up, *self._epilogue)
+
+    def _asked(self, c):
+        at, ldx = ctypes.addressof(c), (self.K + 15) // 16 * 16  # (as LinearWeights')
+        if self.grouped:
+            return _c.moe_grouped_linear_q8(at, 16, None, 32, ldx, 64, 0, 0, 48, self.N, None)
+        return _c.moe_linear_q8(at, 32, ldx, 64, 0, None, 0, 48, self.N, None)
 
 
 class Router(_Described):
