@@ -108,3 +108,17 @@ def test_64_places_and_the_one_left_out(E, score):
         both(rows, 64, score=score, bias=b)
     if E % 8 == 0:
         both(z[:9], 64 if E > 64 else 32, score=score, bias=b, groups=8, top_groups=4 + (E == 64), group_score="top2")
+
+
+@pytest.mark.parametrize("E,n", [(64, 40), (250, 900), (256, 4200), (1000, 300)])
+def test_rows_of_one_large_score_and_rows_of_equal_logits(E, n):
+    """Softmax rows in which nearly all scores are next to zero, 16-bit logits that tie, rows of zeros as
+    padded batches have them; biases of zeros, of one sign, of a few steps."""
+    g = torch.Generator().manual_seed(E)
+    z = 6 * torch.randn((n, E), generator=g)
+    z[::3, 5] = 40.0
+    z[1::7] = 0.0
+    z = z.to(torch.bfloat16).cuda()
+    for b in (torch.zeros(E), -0.25 * torch.rand(E, generator=g), 2.0 ** -20 * torch.randint(0, 3, (E,), generator=g)):
+        for score in ("softmax", "sigmoid"):
+            both(z, 6, score=score, bias=b.to(F32).cuda(), renormalize=False)
