@@ -138,6 +138,11 @@ moe_status run(const Product &a, cudaStream_t st) {
 //   768x2048 gated, 128 experts, top 8   1 token 6.6 / 9.5 / 16    16 tokens 47 / 63 / 53   32 tokens 82 / 78 / 65
 //   the same, all on the same experts                              16 tokens 24 / 17 / 16
 //   512x1024 gated, 8 experts, top 2     8 tokens 4.1 / 4.4 / 10   32 tokens 7.0 / 6.2 / 10.6
+// From 8 to 128 rows none of them is near the bytes of the codes, and some calls take as long as 16-bit
+// weights do, or longer (the chosen kernel / the 16-bit product of twice the bytes): 2048x2048 32 rows 4.6 / 4.4,
+// 64 rows 8.8 / 7.9; 2048x4096 gated 64 rows 20.1 / 19.2; but 8192x4096 8 rows 8.0 / 13.7. A block of ops_rows_q8.cu
+// converts all rows of x for 16 columns, and the weights again for every 32 rows; ops_gemm_q8.cu has a pair of
+// SMs for 256 columns, so that narrow products leave most idle.
 // Of a linear product the three are weighed by their times (us) as fitted to such figures: dot by
 // bytes, bytes times rows in fours, and outputs; mma.sync by its walk along K, for more than 16
 // rows in passes of 32 and rounds of 304 blocks of 16 columns; tcgen05 by its walk along K or the

@@ -5,10 +5,11 @@
 //   ids = the top_k experts by c_e in them, ties to the lower id;
 //   w_j = s of the j-th, divided by the sum of all of them if asked, times scale.
 //
-// Bound: latency for a few rows, the issue of instructions for many (a row is E logits, a few
-// hundred bytes). L lanes take a row: all 32 of a warp, so that a row is done soon, or 8 where
+// Bound: latency, of launch and one row for a few rows, of the chain of dependent reductions that a
+// row's ranks are for many (8192 x 256: 13 warps an SM issue 1.3 instructions a cycle, the integer pipe is 27 %
+// busy, 4 % of HBM). L lanes take a row: all 32 of a warp, so that a row is done soon, or 8 where
 // there are rows enough to fill the SMs, so that an instruction serves four rows (8192 x 256,
-// top 6: 5.5 us, with a bias 8.9; a warp each 9.1 and 14). Lane i holds the V experts V i ..
+// top 6: 5.5 us, with a bias 9.0; a warp each 9.1 and 14). Lane i holds the V experts V i ..
 // V i + V - 1, which makes the lowest lane of a tie the lowest id. A key is its f32 as an
 // unsigned number that sorts alike (0: not available). Each lane keeps the largest of its own, so
 // that a rank is one maximum over the lanes, and another over the V keys of the lane that had it:

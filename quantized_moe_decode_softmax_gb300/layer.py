@@ -259,7 +259,8 @@ def _quantized(gate, up, down, activation, act_limit):
 class RouterLayer:
     """The router of a layer: logits = x weight^T (+ bias), then `rule` (a Router) makes
     ids and weights of them. weight [E, D] and bias [E] in 16 bits, and so are the logits
-    (moe_linear rounds them once); two launches."""
+    (moe_linear rounds them once, by up to 2^-9 of one in bf16; f32 logits from elsewhere go to
+    moe_route itself); two launches."""
 
     def __init__(self, weight, rule: Router, bias=None):
         self.logits, self.rule = LinearWeights(weight, bias=bias), rule
