@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
         bool others = best && !unsure && !(in - unsortable(best) > near);  // (best: of the lane's keys)
         if (softmax && __any_sync(kAll, others)) {
             // a score next to `in` is at most `in` less the least bias (of a row with one large score all others
-            // are near otherwise: 15 us for 8192 x 256, 10.6 so)
+            // are near otherwise: 15 us for 8192 x 256, 10.8 so)
             float least = INFINITY;
 #pragma unroll 4
             for (int e = sub; e < a.E; e += L) least = fminf(least, takes_part(a.bias[e]) ? a.bias[e] : INFINITY);
